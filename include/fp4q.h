@@ -390,6 +390,77 @@ size_t fp4_gemm_nvfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * the scale arrays); 0 when M, N or K is 0. */
 size_t fp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/* Scales of 8-bit (E4M3) operands, one binary32 number per block:
+ * ROW   128 consecutive elements of a row (activations, gradients);
+ * TILE  128 rows x 128 columns (weights: the same for the matrix and its
+ *       transpose).
+ * The last block of a row or column is shorter where the size is no multiple. */
+typedef enum { FP4Q_B128_ROW = 0, FP4Q_B128_TILE = 1 } fp4q_b128_kind;
+
+/*
+ * 8-bit quantization in blocks of 128, of a matrix and of its transpose from one
+ * read: for layers whose inputs or weights 4 bits hurt, and for training.  With
+ * a = max |x| of a block,
+ *   s = max(RN32(a / 448), 2^-126)   (448: the largest E4M3 value)
+ *   code = RN32(x / s) rounded to the nearest E4M3 value, ties to even
+ * so that x_hat = code * s.  E4M3 is the "fn" encoding (bias 7, no infinities,
+ * 0x7F NaN).
+ *   x           device, rows x cols contiguous, dtype xt; aligned to its element
+ *   kind        FP4Q_B128_ROW or FP4Q_B128_TILE
+ *   codes       device out or NULL: rows x ld bytes, ld = cols rounded up to 16
+ *               (the padding is written, as zeros); 16-byte aligned
+ *   scales      device out, with codes.  ROW: ceil(cols / 128) x rows floats,
+ *               block-major (the scales of one block of all rows are contiguous,
+ *               as a product reads them); TILE: ceil(rows / 128) x
+ *               ceil(cols / 128), row-major
+ *   codes_t     device out or NULL: the transpose, quantized in its own blocks
+ *               (ROW: 128 consecutive elements of a column of x): cols x ld_t
+ *               bytes, ld_t = rows rounded up to 16
+ *   scales_t    with codes_t, laid out for the transpose: ROW ceil(rows / 128) x
+ *               cols; TILE ceil(cols / 128) x ceil(rows / 128)
+ * Any rows and cols (rows * cols <= (2^31 - 1) * 512; an empty matrix is a
+ * no-op); no workspace.  Equal to calling twice, on x and on its transpose.
+ * Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN, FP4Q_ERR_HIP.
+ */
+fp4q_status fp8_quantize_b128(const void* x, int32_t xt, int64_t rows, int64_t cols, int32_t kind,
+                              uint8_t* codes, float* scales, uint8_t* codes_t, float* scales_t,
+                              void* stream);
+
+/*
+ * 8-bit matrix product C = A_hat * B_hat^T of operands as fp8_quantize_b128
+ * writes them: A (M x K) with row scales, B (N x K) with row or tile scales.
+ * With X (tokens x in), W (out x in) and dY (tokens x out), a linear layer's three
+ * products are Y = X W^T from X's codes and W's; dX = dY W from dY's codes and W's
+ * codes_t; dW = dY^T X from both codes_t with row scales.
+ *   a_codes, b_codes    device, rows of K bytes; 16-byte aligned
+ *   a_scales            device, ceil(K / 128) x M
+ *   b_kind, b_scales    FP4Q_B128_TILE: ceil(N / 128) x ceil(K / 128);
+ *                       FP4Q_B128_ROW: ceil(K / 128) x N
+ *   M, N, K             K % 16 == 0 (pass the padded row length: the padding is
+ *                       zeros), K <= 2^22, M < 2^31, N * sizeof(out element) <
+ *                       2^23; M or N == 0 is a no-op; K == 0 writes zeros
+ *   c, ct               device out, M x N row-major, FP4Q_F32 or FP4Q_BF16
+ *                       (round to nearest even); aligned to its element
+ *   ws, ws_bytes        device scratch of fp8_gemm_b128_workspace_bytes(M, N, K)
+ *                       bytes (0 for most shapes; then ws may be NULL), 16-byte
+ *                       aligned: partial products of K ranges
+ * At most 64 rows of A take a kernel that streams B once; others 256 x 256 tiles.
+ * Each block's 128 products are added by the matrix cores from zero and go under
+ * the binary32 product of the two scales into a binary32 sum, K ranges in
+ * binary64: C differs from the exact product by rounding of order (K / 128 + 8) *
+ * 2^-23 of sum |a_hat| |b_hat| (plus the output's own), and scale products below
+ * 2^-126 lose their low bits.  The same on every run for a given shape.
+ * A NaN code or scale gives NaN in the rows or columns that it belongs to.
+ * Errors as for fp4_gemm_nvfp4.
+ */
+fp4q_status fp8_gemm_b128(const uint8_t* a_codes, const float* a_scales, const uint8_t* b_codes,
+                          const float* b_scales, int32_t b_kind, int64_t M, int64_t N, int64_t K, void* c,
+                          int32_t ct, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes fp8_gemm_b128 needs: 4 * M * N per K range when K is split (a
+ * function of M, N and K only); 0 otherwise. */
+size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 /* Workspace size in bytes for any call on a rows x cols tensor (a constant
  * upper bound in this version). */
 size_t fp4q_workspace_bytes(int64_t rows, int64_t cols, int32_t block);

@@ -31,6 +31,7 @@ BF16, F32 = 0, 1
 FMT_MXFP4, FMT_UE4M3, FMT_UE5M3 = 0, 1, 2
 G_NONE, G_DYNAMIC, G_GIVEN, G_ROW = 0, 1, 2, 3
 MSE_ABS, MSE_REL = 0, 1
+B128_ROW, B128_TILE = 0, 1
 STATUS = {0: "OK", 1: "ERR_ARG", 2: "ERR_SHAPE", 3: "ERR_ALIGN", 4: "ERR_WORKSPACE", 5: "ERR_HIP"}
 
 EXPORTS = ("mxfp4_quantize", "nvfp4_quantize", "nvfp4_quantize_noalloc", "fp4_quantize_mx_nv",
@@ -38,6 +39,7 @@ EXPORTS = ("mxfp4_quantize", "nvfp4_quantize", "nvfp4_quantize_noalloc", "fp4_qu
            "fp4_dequantize",
            "fp4_block_mse", "hadamard_block_rotate", "fp4_gemm_mxfp4", "fp4_gemm_workspace_bytes",
            "fp4_gemm_nvfp4", "fp4_gemm_nvfp4_workspace_bytes",
+           "fp8_quantize_b128", "fp8_gemm_b128", "fp8_gemm_b128_workspace_bytes",
            "fp4q_workspace_bytes",
            "fp4q_last_error", "fp4q_abi_version", "fp4q_profile_events", "fp4q_profile_count")
 
@@ -82,6 +84,12 @@ def _bind(l):
     l.fp4_gemm_nvfp4.argtypes = [P, P, P, P, P, P, i64, i64, i64, P, i32, P, sz, P]
     l.fp4_gemm_nvfp4_workspace_bytes.argtypes = [i64, i64, i64]
     l.fp4_gemm_nvfp4_workspace_bytes.restype = sz
+    l.fp8_quantize_b128.argtypes = [P, i32, i64, i64, i32, P, P, P, P, P]
+    l.fp8_quantize_b128.restype = c.c_int
+    l.fp8_gemm_b128.argtypes = [P, P, P, P, i32, i64, i64, i64, P, i32, P, sz, P]
+    l.fp8_gemm_b128.restype = c.c_int
+    l.fp8_gemm_b128_workspace_bytes.argtypes = [i64, i64, i64]
+    l.fp8_gemm_b128_workspace_bytes.restype = sz
     l.fp4_block_mse.argtypes = [P, i32, P, P, i32, i32, P, i64, i64, i32, P, i32, P, P, sz, P]
     l.hadamard_block_rotate.argtypes = [P, i32, i64, i64, i32, P, P]
     for name in ("mxfp4_quantize", "nvfp4_quantize", "fp4_dequantize", "fp4_block_mse",
@@ -402,6 +410,97 @@ def fp4_gemm_nvfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, a_g: Optional[
     return out
 
 
+@dataclass
+class Fp8Quantized:
+    codes: Optional[torch.Tensor]      # float8_e4m3fn, rows x cols rounded up to 16
+    scales: Optional[torch.Tensor]     # float32
+    codes_t: Optional[torch.Tensor]    # of the transpose
+    scales_t: Optional[torch.Tensor]
+    kind: int
+
+
+def _cdiv(n: int, m: int) -> int:
+    return -(-n // m)
+
+
+def _b128_scales(rows: int, cols: int, kind: int):
+    """Shape of the scales of a rows x cols operand."""
+    return (_cdiv(cols, 128), rows) if kind == B128_ROW else (_cdiv(rows, 128), _cdiv(cols, 128))
+
+
+def fp8_quantize_b128(x: torch.Tensor, kind: int = B128_ROW, *, codes=True, transposed=False,
+                      out: Optional[Fp8Quantized] = None) -> Fp8Quantized:
+    """E4M3 codes with one float32 scale per 128 elements of a row (B128_ROW) or
+    per 128 x 128 (B128_TILE), of x and, with ``transposed``, of its transpose in
+    the same pass (``codes=False``: the transpose alone).  ``out``: preallocated
+    outputs, laid out as the call returns them; what it lacks is not computed."""
+    x = _matrix(x)
+    if kind not in (B128_ROW, B128_TILE):
+        raise ValueError(f"kind {kind} is not B128_ROW or B128_TILE")
+    rows, cols = x.shape
+    want = {}
+    if codes if out is None else out.codes is not None:
+        want["codes"] = (rows, _cdiv(cols, 16) * 16)
+        want["scales"] = _b128_scales(rows, cols, kind)
+    if transposed if out is None else out.codes_t is not None:
+        want["codes_t"] = (cols, _cdiv(rows, 16) * 16)
+        want["scales_t"] = _b128_scales(cols, rows, kind)
+    if not want:
+        raise ValueError("nothing is wanted: neither codes nor transposed")
+    got = {}
+    for name, shape in want.items():
+        dt = torch.float8_e4m3fn if name.startswith("codes") else torch.float32
+        t = None if out is None else getattr(out, name)
+        if out is None:
+            t = torch.empty(shape, dtype=dt, device=x.device)
+        elif t is None or t.shape != shape or t.dtype != dt or t.device != x.device or not t.is_contiguous():
+            raise ValueError(f"out.{name} must be a contiguous {dt} tensor of shape {shape} on {x.device}")
+        got[name] = t
+    _check(lib().fp8_quantize_b128(_ptr(x), _dtype_code(x), rows, cols, kind, _ptr(got.get("codes")),
+                                   _ptr(got.get("scales")), _ptr(got.get("codes_t")),
+                                   _ptr(got.get("scales_t")), _stream(x.device)))
+    return Fp8Quantized(got.get("codes"), got.get("scales"), got.get("codes_t"), got.get("scales_t"), kind)
+
+
+def _b128_operand(codes: torch.Tensor, scales: torch.Tensor, kind: int, what: str):
+    _matrix(codes, what + "_codes")
+    _matrix(scales, what + "_scales")
+    if codes.dtype != torch.float8_e4m3fn or scales.dtype != torch.float32:
+        raise TypeError(f"{what}: expected float8_e4m3fn codes and float32 scales")
+    want = _b128_scales(codes.shape[0], codes.shape[1], kind)
+    if tuple(scales.shape) != want:
+        raise ValueError(f"{what}_scales has shape {tuple(scales.shape)}; codes {tuple(codes.shape)} need {want}")
+
+
+def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor,
+                  b_scales: torch.Tensor, b_kind: int = B128_TILE, out_dtype=torch.float32,
+                  out: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C = A_hat @ B_hat.T for operands as fp8_quantize_b128 writes them: A with row
+    scales, B with the scales that ``b_kind`` names."""
+    if b_kind not in (B128_ROW, B128_TILE):
+        raise ValueError(f"b_kind {b_kind} is not B128_ROW or B128_TILE")
+    _b128_operand(a_codes, a_scales, B128_ROW, "a")
+    _b128_operand(b_codes, b_scales, b_kind, "b")
+    m, k = a_codes.shape
+    n = b_codes.shape[0]
+    if b_codes.shape[1] != k:
+        raise ValueError(f"a_codes has rows of {k}, b_codes of {b_codes.shape[1]}")
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=a_codes.device)
+    elif tuple(out.shape) != (m, n) or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous, {m} x {n}")
+    if any(t.device != a_codes.device for t in (a_scales, b_codes, b_scales, out)):
+        raise ValueError("operands and out must be on one device")
+    need = int(lib().fp8_gemm_b128_workspace_bytes(m, n, k))
+    if ws is None and need:
+        ws = gemm_workspace(a_codes.device, need)
+    _check(lib().fp8_gemm_b128(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), b_kind, m, n, k,
+                               _ptr(out), _dtype_code(out), _ptr(ws), 0 if ws is None else ws.numel(),
+                               _stream(a_codes.device)))
+    return out
+
+
 def fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: int, block: int,
                    g: Optional[torch.Tensor] = None, rotate: int = 0,
                    out_dtype=torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -521,3 +620,6 @@ class LaunchTimer:
             for h in self._handles:
                 if h:
                     hip.hipEventDestroy(h)
+
+
+from .fp8_linear import fp8_linear  # noqa: E402  (needs the functions above)

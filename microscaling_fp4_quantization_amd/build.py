@@ -9,8 +9,8 @@ C++.  Flags that matter for the arithmetic:
   -fno-gpu-flush-denormals-to-zero, no fast-math: IEEE binary32 and binary64
                          with subnormals and correctly rounded division
   -target-feature -packed-fp32-ops: no packed-FP32 instructions
-The GEMM source also takes -amdgpu-mfma-vgpr-form: matrix-core accumulators
-in ordinary VGPRs, which keeps them in place across the K loop.
+The GEMM sources also take -amdgpu-mfma-vgpr-form: matrix-core accumulators in
+ordinary VGPRs, which keeps them in place across the K loop.
 """
 from __future__ import annotations
 
@@ -32,7 +32,8 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contra
              "-fno-fast-math", "-fno-gpu-flush-denormals-to-zero",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wall", "-Wno-unused-function"]
-FILE_FLAGS = {"fp4q_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+FILE_FLAGS = {"fp4q_gemm.hip": VGPR_FORM, "fp4q_fp8_gemm.hip": VGPR_FORM}
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 
 

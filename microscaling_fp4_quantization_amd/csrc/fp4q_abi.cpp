@@ -53,6 +53,11 @@ fp4q_status check_dtype(const char* fn, int32_t t) {
     return FP4Q_OK;
 }
 
+fp4q_status check_kind(const char* fn, int32_t k) {
+    if (k != FP4Q_B128_ROW && k != FP4Q_B128_TILE) return fail(FP4Q_ERR_ARG, "%s: kind %d is not ROW (0) or TILE (1)", fn, k);
+    return FP4Q_OK;
+}
+
 fp4q_status check_mse(const char* fn, const float* block_mse, int32_t kind) {
     if (kind != FP4Q_MSE_ABS && kind != FP4Q_MSE_REL) return fail(FP4Q_ERR_ARG, "%s: mse_kind %d is not ABS (0) or REL (1)", fn, kind);
     if (block_mse && !aligned(block_mse, 4)) return fail(FP4Q_ERR_ALIGN, "%s: block_mse is not 4-byte aligned", fn);
@@ -374,6 +379,73 @@ fp4q_status fp4_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales, cons
 size_t fp4_gemm_nvfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
     return fp4q::gemm_nvfp4_workspace_bytes(M, N, K);
+}
+
+fp4q_status fp8_quantize_b128(const void* x, int32_t xt, int64_t rows, int64_t cols, int32_t kind,
+                              uint8_t* codes, float* scales, uint8_t* codes_t, float* scales_t,
+                              void* stream) {
+    const char* fn = "fp8_quantize_b128";
+    TRY(check_dtype(fn, xt));
+    TRY(check_kind(fn, kind));
+    // Any size: the block of 128 may be cut short by a row's end.
+    if (rows < 0 || cols < 0) return fail(FP4Q_ERR_SHAPE, "%s: negative size %lld x %lld", fn, (long long)rows, (long long)cols);
+    if (rows > 0 && cols > (int64_t)INT32_MAX * 512 / rows)
+        return fail(FP4Q_ERR_SHAPE, "%s: %lld x %lld elements exceed the limit of (2^31 - 1) * 512", fn, (long long)rows, (long long)cols);
+    if (rows > 0 && cols > 0) {
+        if (!x) return fail(FP4Q_ERR_ARG, "%s: x must not be NULL", fn);
+        if (!codes != !scales || !codes_t != !scales_t)
+            return fail(FP4Q_ERR_ARG, "%s: codes go with scales, and codes_t with scales_t", fn);
+        if (!codes && !codes_t) return fail(FP4Q_ERR_ARG, "%s: codes and codes_t must not both be NULL", fn);
+        if (!aligned(x, xt == FP4Q_F32 ? 4 : 2)) return fail(FP4Q_ERR_ALIGN, "%s: x is not aligned to its element", fn);
+        if (!aligned(codes, 16) || !aligned(codes_t, 16))
+            return fail(FP4Q_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
+        if (!aligned(scales, 4) || !aligned(scales_t, 4))
+            return fail(FP4Q_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+    }
+    fp4q::Fp8QuantJob j{x, xt, rows, cols, kind == FP4Q_B128_TILE, codes, scales, codes_t, scales_t, stream};
+    char msg[256] = {0};
+    return launched(fp4q::launch_fp8_quantize(j, msg, sizeof msg), msg);
+}
+
+fp4q_status fp8_gemm_b128(const uint8_t* a_codes, const float* a_scales, const uint8_t* b_codes,
+                          const float* b_scales, int32_t b_kind, int64_t M, int64_t N, int64_t K, void* c,
+                          int32_t ct, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "fp8_gemm_b128";
+    TRY(check_dtype(fn, ct));
+    TRY(check_kind(fn, b_kind));
+    if (M < 0 || N < 0 || K < 0) return fail(FP4Q_ERR_SHAPE, "%s: negative size", fn);
+    if (K % 16 != 0) return fail(FP4Q_ERR_SHAPE, "%s: K = %lld is not a multiple of 16", fn, (long long)K);
+    if (K > (int64_t)1 << 22) return fail(FP4Q_ERR_SHAPE, "%s: K = %lld exceeds 2^22", fn, (long long)K);
+    const int64_t eb = ct == FP4Q_F32 ? 4 : 2;
+    if (N * eb >= (int64_t)1 << 23)
+        return fail(FP4Q_ERR_SHAPE, "%s: N = %lld is too large for this output type", fn, (long long)N);
+    if (M >= (int64_t)1 << 31) return fail(FP4Q_ERR_SHAPE, "%s: M = %lld exceeds 2^31", fn, (long long)M);
+    if (M > 0 && N > 0) {
+        if (!c) return fail(FP4Q_ERR_ARG, "%s: c must not be NULL", fn);
+        if (!aligned(c, (size_t)eb)) return fail(FP4Q_ERR_ALIGN, "%s: c is not aligned to its element", fn);
+        if (K > 0) {
+            if (!a_codes || !a_scales || !b_codes || !b_scales)
+                return fail(FP4Q_ERR_ARG, "%s: codes and scales must not be NULL", fn);
+            if (!aligned(a_codes, 16) || !aligned(b_codes, 16))
+                return fail(FP4Q_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
+            if (!aligned(a_scales, 4) || !aligned(b_scales, 4))
+                return fail(FP4Q_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+            const size_t need = fp4q::fp8_gemm_workspace_bytes(M, N, K);
+            if (need > 0 && (!ws || ws_bytes < need))
+                return fail(FP4Q_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
+                            ws ? ws_bytes : (size_t)0);
+            if (need > 0 && !aligned(ws, 16))
+                return fail(FP4Q_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+        }
+    }
+    fp4q::Fp8GemmJob j{a_codes, a_scales, b_codes, b_scales, b_kind == FP4Q_B128_ROW, M, N, K, c, ct, ws, stream};
+    char msg[256] = {0};
+    return launched(fp4q::launch_fp8_gemm(j, msg, sizeof msg), msg);
+}
+
+size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0) return 0;
+    return fp4q::fp8_gemm_workspace_bytes(M, N, K);
 }
 
 fp4q_status hadamard_block_rotate(const void* x, int32_t xt, int64_t rows, int64_t cols, int32_t n_rot,

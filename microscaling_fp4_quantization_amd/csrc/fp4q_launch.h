@@ -115,6 +115,36 @@ struct GemmNvJob {
 
 size_t gemm_nvfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+// E4M3 codes with a binary32 scale per 128 elements of a row (tile false) or per
+// 128 x 128 (tile true); codes or codes_t may be NULL.
+struct Fp8QuantJob {
+    const void* x;
+    int xt;            // 0 bf16, 1 f32
+    int64_t rows, cols;
+    bool tile;
+    uint8_t* codes;
+    float* scales;
+    uint8_t* codes_t;
+    float* scales_t;
+    void* stream;
+};
+
+// Product of two such operands; b_row: B has row scales (else tile scales).
+struct Fp8GemmJob {
+    const uint8_t* a_codes;
+    const float* a_scales;
+    const uint8_t* b_codes;
+    const float* b_scales;
+    bool b_row;
+    int64_t M, N, K;
+    void* c;
+    int ct;            // 0 bf16, 1 f32
+    void* ws;          // fp8_gemm_workspace_bytes(M, N, K) bytes: partial products
+    void* stream;
+};
+
+size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 // Launch timing (fp4q_profile_events): while the calling thread has event
 // pairs left, every kernel launch records the next pair on its stream around
 // itself.  Streams and events are passed as void*.
@@ -152,5 +182,12 @@ int launch_block_mse(const MseJob& j, char* msg, size_t msg_len);
 int launch_rotate(const RotateJob& j, char* msg, size_t msg_len);
 int launch_gemm(const GemmJob& j, char* msg, size_t msg_len);
 int launch_gemm_nvfp4(const GemmNvJob& j, char* msg, size_t msg_len);
+int launch_fp8_quantize(const Fp8QuantJob& j, char* msg, size_t msg_len);
+int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len);
+
+// Adds the binary32 partial products of `splits` K ranges (splits x count, range
+// by range) in binary64 and writes c (ct: 0 bf16, 1 f32); partial and c are
+// device pointers, the stream a hipStream_t.
+void launch_splitk_reduce(const float* partial, int splits, int64_t count, void* c, int ct, void* stream);
 
 }  // namespace fp4q
