@@ -101,7 +101,9 @@ typedef enum { FP4Q_BF16 = 0, FP4Q_F32 = 1 } fp4q_dtype;
 typedef enum {
     FP4Q_FMT_MXFP4 = 0, /* E8M0 scales, block 32 */
     FP4Q_FMT_UE4M3 = 1, /* UE4M3 scales (NVFP4 at block 16), with per-tensor g */
-    FP4Q_FMT_UE5M3 = 2  /* UE5M3 scales, no per-tensor scale (g = 1) */
+    FP4Q_FMT_UE5M3 = 2, /* UE5M3 scales, no per-tensor scale (g = 1) */
+    FP4Q_FMT_E4M3_B128 = 3 /* 8-bit codes under 128 x 128 binary32 scales, as
+                              fp8_quantize_b128 writes them (moe_layer only) */
 } fp4q_format;
 
 typedef enum {
@@ -447,9 +449,11 @@ fp4q_status fp8_quantize_b128(const void* x, int32_t xt, int64_t rows, int64_t c
  * At most 64 rows of A take a kernel that streams B once; others 256 x 256 tiles.
  * Each block's 128 products are added by the matrix cores from zero and go under
  * the binary32 product of the two scales into a binary32 sum, K ranges in
- * binary64: C differs from the exact product by rounding of order (K / 128 + 8) *
- * 2^-23 of sum |a_hat| |b_hat| (plus the output's own), and scale products below
- * 2^-126 lose their low bits.  The same on every run for a given shape.
+ * binary64.  A binary32 C differs from the exact product by rounding of order
+ * (K / 128 + 8) * 2^-23 of sum |a_hat| |b_hat|.  A bf16 C of more than 64 rows is
+ * computed on the 8-bit matrix cores, whose sums hold about 16 bits (2^-15.5 of sum
+ * |a_hat| |b_hat|), and rounded.  Scale products below 2^-126 lose their low bits.
+ * The same on every run for a given shape.
  * A NaN code or scale gives NaN in the rows or columns that it belongs to.
  * Errors as for fp4_gemm_nvfp4.
  */
@@ -460,6 +464,64 @@ fp4q_status fp8_gemm_b128(const uint8_t* a_codes, const float* a_scales, const u
 /* Workspace bytes fp8_gemm_b128 needs: 4 * M * N per K range when K is split (a
  * function of M, N and K only); 0 otherwise. */
 size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* One stacked matrix of a layer's expert weights, (experts * rows) x K, exactly as
+ * the quantize calls write it. */
+typedef struct {
+    const uint8_t* codes;  /* device, 16-byte aligned */
+    const void* scales;    /* device: E8M0 bytes per 32 (MXFP4), UE4M3 bytes per 16
+                              (UE4M3; 2-byte aligned) or binary32 tile scales of the
+                              stacked matrix (E4M3_B128; 4-byte aligned) */
+    const float* g;        /* UE4M3: device per-tensor scales; NULL means 1 */
+    int32_t g_count;       /* 1 for all experts, or one per expert */
+} fp4q_expert_weights;
+
+#define FP4Q_MOE_MAX_TOKENS 64
+#define FP4Q_MOE_MAX_EXPERTS 512
+#define FP4Q_MOE_MAX_TOP_K 16
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (decoding), on quantized expert
+ * weights ("Diagnosing FP4 inference", section 2, has weights dequantized for the
+ * compute):
+ *   l = x Wr^T in binary32; the top_k experts of the largest l (ties to the lowest
+ *   index), in that order; p = softmax of their l (renormalize != 0), or their part
+ *   of the softmax over all experts (0);
+ *   y = sum over them of p_e D_e (silu(G_e x) * (U_e x)), silu(v) = v / (1 + e^-v)
+ *   x           device, tokens x dim, dtype xt; 16-byte aligned
+ *   tokens      0..64 (0: a no-op); dim, inter multiples of 32 up to 2^20; experts
+ *               1..512; top_k 1..16, at most experts
+ *   fmt         FP4Q_FMT_MXFP4 (block 32), FP4Q_FMT_UE4M3 (block 16) or
+ *               FP4Q_FMT_E4M3_B128
+ *   w13         (experts * 2 * inter) x dim: inter gate rows, then inter up rows,
+ *               expert after expert
+ *   w2          (experts * dim) x inter
+ *   router      device, experts x dim, dtype rt, 16-byte aligned; or NULL: the
+ *               caller's own routing is read from topk_ids and topk_weights
+ *   topk_ids, topk_weights  device, tokens x top_k; written, or read when router is
+ *               NULL.  A given id outside 0..experts-1 names no expert (a token
+ *               without any gets zeros); one named twice counts under the sum of
+ *               its weights.
+ *   y, yt       device out, tokens x dim
+ *   ws          moe_layer_workspace_bytes() bytes, 256-byte aligned, its first 256
+ *               bytes zero before the first call; calls leave them zero.  Calls
+ *               that overlap need distinct workspaces.
+ * Activations meet the weights' exact values; sums are binary32.  Binary32 x goes
+ * through whole; h = silu(G x) * (U x) is held to 16 bits (24 for a binary32 y).
+ * Against the exact layer y differs by rounding of order 2^-16 (binary32 y: that of
+ * binary32 sums) of sum |p D h|, and its own rounding.  Results are the same on
+ * every run.  Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN,
+ * FP4Q_ERR_WORKSPACE, FP4Q_ERR_HIP; nothing is launched on one other than
+ * FP4Q_ERR_HIP.
+ */
+fp4q_status moe_layer(const void* x, int32_t xt, int64_t tokens, int64_t dim, int64_t inter, int32_t experts,
+                      int32_t top_k, int32_t fmt, const fp4q_expert_weights* w13,
+                      const fp4q_expert_weights* w2, const void* router, int32_t rt, int32_t renormalize,
+                      int32_t* topk_ids, float* topk_weights, void* y, int32_t yt, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Workspace bytes of moe_layer (0 for sizes that it refuses, or no tokens). */
+size_t moe_layer_workspace_bytes(int64_t tokens, int64_t dim, int64_t inter, int32_t experts, int32_t top_k);
 
 /* Workspace size in bytes for any call on a rows x cols tensor (a constant
  * upper bound in this version). */

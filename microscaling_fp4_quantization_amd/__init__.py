@@ -28,7 +28,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfp4q.so")
 
 BF16, F32 = 0, 1
-FMT_MXFP4, FMT_UE4M3, FMT_UE5M3 = 0, 1, 2
+FMT_MXFP4, FMT_UE4M3, FMT_UE5M3, FMT_E4M3_B128 = 0, 1, 2, 3
 G_NONE, G_DYNAMIC, G_GIVEN, G_ROW = 0, 1, 2, 3
 MSE_ABS, MSE_REL = 0, 1
 B128_ROW, B128_TILE = 0, 1
@@ -40,6 +40,7 @@ EXPORTS = ("mxfp4_quantize", "nvfp4_quantize", "nvfp4_quantize_noalloc", "fp4_qu
            "fp4_block_mse", "hadamard_block_rotate", "fp4_gemm_mxfp4", "fp4_gemm_workspace_bytes",
            "fp4_gemm_nvfp4", "fp4_gemm_nvfp4_workspace_bytes",
            "fp8_quantize_b128", "fp8_gemm_b128", "fp8_gemm_b128_workspace_bytes",
+           "moe_layer", "moe_layer_workspace_bytes",
            "fp4q_workspace_bytes",
            "fp4q_last_error", "fp4q_abi_version", "fp4q_profile_events", "fp4q_profile_count")
 
@@ -90,6 +91,10 @@ def _bind(l):
     l.fp8_gemm_b128.restype = c.c_int
     l.fp8_gemm_b128_workspace_bytes.argtypes = [i64, i64, i64]
     l.fp8_gemm_b128_workspace_bytes.restype = sz
+    l.moe_layer.argtypes = [P, i32, i64, i64, i64, i32, i32, i32, P, P, P, i32, i32, P, P, P, i32, P, sz, P]
+    l.moe_layer.restype = c.c_int
+    l.moe_layer_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    l.moe_layer_workspace_bytes.restype = sz
     l.fp4_block_mse.argtypes = [P, i32, P, P, i32, i32, P, i64, i64, i32, P, i32, P, P, sz, P]
     l.hadamard_block_rotate.argtypes = [P, i32, i64, i64, i32, P, P]
     for name in ("mxfp4_quantize", "nvfp4_quantize", "fp4_dequantize", "fp4_block_mse",
@@ -499,6 +504,115 @@ def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
                                _ptr(out), _dtype_code(out), _ptr(ws), 0 if ws is None else ws.numel(),
                                _stream(a_codes.device)))
     return out
+
+
+class _ExpertWeightsC(ctypes.Structure):
+    """fp4q_expert_weights."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("g_count", ctypes.c_int32)]
+
+
+@dataclass
+class ExpertWeights:
+    """One stacked matrix of expert weights, (experts * rows) x K, as the quantize
+    calls write it: codes, scales and (FMT_UE4M3) g, one for all or one per expert."""
+    fmt: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    g: Optional[torch.Tensor] = None
+
+
+@dataclass
+class MoeOutput:
+    y: torch.Tensor
+    topk_ids: torch.Tensor
+    topk_weights: torch.Tensor
+
+
+def _expert_weights(w: ExpertWeights, rows: int, k: int, what: str, device) -> _ExpertWeightsC:
+    codes, scales = _matrix(w.codes, what + " codes"), _matrix(w.scales, what + " scales")
+    if w.fmt == FMT_E4M3_B128:
+        want = (rows, k), _b128_scales(rows, k, B128_TILE)
+        types = torch.float8_e4m3fn, torch.float32
+    elif w.fmt in (FMT_MXFP4, FMT_UE4M3):
+        want = (rows, k // 2), (rows, k // (32 if w.fmt == FMT_MXFP4 else 16))
+        types = torch.uint8, torch.uint8
+    else:
+        raise ValueError(f"{what}: fmt {w.fmt} is not FMT_MXFP4, FMT_UE4M3 or FMT_E4M3_B128")
+    if (codes.dtype, scales.dtype) != types:
+        raise TypeError(f"{what}: expected {types[0]} codes and {types[1]} scales")
+    if (tuple(codes.shape), tuple(scales.shape)) != want:
+        raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)}; needed {want[0]} and {want[1]}")
+    if w.g is not None and (w.g.dtype != torch.float32 or not w.g.is_contiguous() or w.g.device != codes.device):
+        raise ValueError(f"{what}: g must be contiguous float32 on the codes' device")
+    if codes.device != device or scales.device != device:
+        raise ValueError(f"{what} must be on x's device")
+    ptr = lambda t: None if t is None else t.data_ptr()
+    return _ExpertWeightsC(ptr(codes), ptr(scales), ptr(w.g), 0 if w.g is None else w.g.numel())
+
+
+_moe_workspaces = {}
+
+
+def moe_workspace(device, nbytes: int) -> torch.Tensor:
+    """A workspace of at least `nbytes` for moe_layer, zero where it has to be, kept
+    per device and current stream and grown on demand."""
+    dev = torch.device(device)
+    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    ws = _moe_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        _moe_workspaces[key] = ws
+    return ws
+
+
+def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: int, top_k: int, *,
+              router: Optional[torch.Tensor] = None, renormalize: bool = True,
+              topk_ids: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None,
+              out_dtype=None, out: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = None) -> MoeOutput:
+    """A mixture-of-experts layer for at most 64 tokens: router, top_k softmax, gate
+    and up products, silu, down product and the weighted sum.
+
+    ``w13``: (experts * 2 * inter) x dim, gate rows then up rows per expert; ``w2``:
+    (experts * dim) x inter.  ``router``: experts x dim; or None, with the routing in
+    ``topk_ids`` (int32) and ``topk_weights`` (float32), tokens x top_k.  y has x's
+    dtype unless ``out_dtype`` or ``out`` says otherwise."""
+    x = _matrix(x)
+    tokens, dim = x.shape
+    if w13.fmt != w2.fmt:
+        raise ValueError("w13 and w2 must have one format")
+    if experts < 1 or w13.codes.dim() != 2 or w13.codes.shape[0] % (2 * experts):
+        raise ValueError(f"w13 does not hold {experts} experts of gate and up rows")
+    inter = w13.codes.shape[0] // (2 * experts)
+    a = _expert_weights(w13, experts * 2 * inter, dim, "w13", x.device)
+    b = _expert_weights(w2, experts * dim, inter, "w2", x.device)
+    if router is not None:
+        _matrix(router, "router")
+        if tuple(router.shape) != (experts, dim) or router.device != x.device:
+            raise ValueError(f"router must be {experts} x {dim} on x's device")
+    elif topk_ids is None or topk_weights is None:
+        raise ValueError("without a router, topk_ids and topk_weights are needed")
+    if topk_ids is None:
+        topk_ids = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
+    if topk_weights is None:
+        topk_weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
+    for t, dt, name in ((topk_ids, torch.int32, "topk_ids"), (topk_weights, torch.float32, "topk_weights")):
+        if tuple(t.shape) != (tokens, top_k) or t.dtype != dt or not t.is_contiguous() or t.device != x.device:
+            raise ValueError(f"{name} must be contiguous {dt}, {tokens} x {top_k}, on x's device")
+    if out is None:
+        out = torch.empty((tokens, dim), dtype=out_dtype or x.dtype, device=x.device)
+    elif tuple(out.shape) != (tokens, dim) or not out.is_contiguous() or out.device != x.device:
+        raise ValueError(f"out must be contiguous, {tokens} x {dim}, on x's device")
+    if ws is None:
+        need = int(lib().moe_layer_workspace_bytes(tokens, dim, inter, experts, top_k))
+        ws = moe_workspace(x.device, need) if need else None
+    _check(lib().moe_layer(_ptr(x), _dtype_code(x), tokens, dim, inter, experts, top_k, w13.fmt,
+                           ctypes.byref(a), ctypes.byref(b), _ptr(router),
+                           0 if router is None else _dtype_code(router), int(renormalize), _ptr(topk_ids),
+                           _ptr(topk_weights), _ptr(out), _dtype_code(out), _ptr(ws),
+                           0 if ws is None else ws.numel(), _stream(x.device)))
+    return MoeOutput(out, topk_ids, topk_weights)
 
 
 def fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: int, block: int,

@@ -448,6 +448,85 @@ size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return fp4q::fp8_gemm_workspace_bytes(M, N, K);
 }
 
+static fp4q_status moe_weights(const char* fn, const char* what, const fp4q_expert_weights* w, int32_t fmt,
+                               int64_t experts, fp4q::MoeWeights& out) {
+    if (!w) return fail(FP4Q_ERR_ARG, "%s: %s must not be NULL", fn, what);
+    if (!w->codes || !w->scales) return fail(FP4Q_ERR_ARG, "%s: %s codes and scales must not be NULL", fn, what);
+    if (!aligned(w->codes, 16)) return fail(FP4Q_ERR_ALIGN, "%s: %s codes must be 16-byte aligned", fn, what);
+    const size_t sa = fmt == FP4Q_FMT_E4M3_B128 ? 4 : fmt == FP4Q_FMT_UE4M3 ? 2 : 1;
+    if (!aligned(w->scales, sa)) return fail(FP4Q_ERR_ALIGN, "%s: %s scales must be %zu-byte aligned", fn, what, sa);
+    if (w->g) {
+        if (fmt != FP4Q_FMT_UE4M3) return fail(FP4Q_ERR_ARG, "%s: %s takes per-tensor scales with UE4M3 only", fn, what);
+        if (w->g_count != 1 && w->g_count != experts)
+            return fail(FP4Q_ERR_ARG, "%s: %s has %d per-tensor scales: 1 or one per expert (%lld) are taken", fn, what,
+                        w->g_count, (long long)experts);
+        if (!aligned(w->g, 4)) return fail(FP4Q_ERR_ALIGN, "%s: %s per-tensor scales must be 4-byte aligned", fn, what);
+    }
+    out = fp4q::MoeWeights{w->codes, w->scales, w->g, w->g && w->g_count > 1};
+    return FP4Q_OK;
+}
+
+static fp4q_status moe_shape(const char* fn, int64_t tokens, int64_t dim, int64_t inter, int64_t experts, int64_t top_k) {
+    if (tokens < 0 || tokens > fp4q::kMoeMaxTokens)
+        return fail(FP4Q_ERR_SHAPE, "%s: %lld tokens: 0 to %lld are taken", fn, (long long)tokens, (long long)fp4q::kMoeMaxTokens);
+    if (dim <= 0 || dim % 32 != 0 || dim > fp4q::kMoeMaxSize || inter <= 0 || inter % 32 != 0 || inter > fp4q::kMoeMaxSize)
+        return fail(FP4Q_ERR_SHAPE, "%s: dim %lld and inter %lld must be multiples of 32 up to 2^20", fn, (long long)dim, (long long)inter);
+    if (experts < 1 || experts > fp4q::kMoeMaxExperts)
+        return fail(FP4Q_ERR_SHAPE, "%s: %lld experts: 1 to %lld are taken", fn, (long long)experts, (long long)fp4q::kMoeMaxExperts);
+    if (top_k < 1 || top_k > fp4q::kMoeMaxTopK || top_k > experts)
+        return fail(FP4Q_ERR_SHAPE, "%s: top_k %lld of %lld experts: 1 to %lld are taken", fn, (long long)top_k,
+                    (long long)experts, (long long)fp4q::kMoeMaxTopK);
+    return FP4Q_OK;
+}
+
+fp4q_status moe_layer(const void* x, int32_t xt, int64_t tokens, int64_t dim, int64_t inter, int32_t experts,
+                      int32_t top_k, int32_t fmt, const fp4q_expert_weights* w13,
+                      const fp4q_expert_weights* w2, const void* router, int32_t rt, int32_t renormalize,
+                      int32_t* topk_ids, float* topk_weights, void* y, int32_t yt, void* ws, size_t ws_bytes,
+                      void* stream) {
+    const char* fn = "moe_layer";
+    TRY(check_dtype(fn, xt));
+    TRY(check_dtype(fn, yt));
+    if (router) TRY(check_dtype(fn, rt));
+    if (fmt != FP4Q_FMT_MXFP4 && fmt != FP4Q_FMT_UE4M3 && fmt != FP4Q_FMT_E4M3_B128)
+        return fail(FP4Q_ERR_ARG, "%s: fmt %d is not MXFP4 (0), UE4M3 (1) or E4M3_B128 (3)", fn, fmt);
+    TRY(moe_shape(fn, tokens, dim, inter, experts, top_k));
+    if (tokens == 0) return ok();
+    fp4q::MoeJob j{};
+    TRY(moe_weights(fn, "w13", w13, fmt, experts, j.w13));
+    TRY(moe_weights(fn, "w2", w2, fmt, experts, j.w2));
+    if (!x || !y || !topk_ids || !topk_weights)
+        return fail(FP4Q_ERR_ARG, "%s: x, y, topk_ids and topk_weights must not be NULL", fn);
+    if (!aligned(x, 16) || !aligned(router, 16)) return fail(FP4Q_ERR_ALIGN, "%s: x and router must be 16-byte aligned", fn);
+    if (!aligned(y, yt == FP4Q_F32 ? 4 : 2)) return fail(FP4Q_ERR_ALIGN, "%s: y is not aligned to its element", fn);
+    if (!aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+        return fail(FP4Q_ERR_ALIGN, "%s: topk_ids and topk_weights must be 4-byte aligned", fn);
+    const size_t need = fp4q::moe_workspace_bytes(tokens, dim, inter, experts, top_k);
+    if (!ws || ws_bytes < need)
+        return fail(FP4Q_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
+    if (!aligned(ws, 256)) return fail(FP4Q_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+    j.x = x;
+    j.xt = xt;
+    j.T = tokens, j.D = dim, j.I = inter, j.E = experts, j.k = top_k;
+    j.fmt = fmt == FP4Q_FMT_E4M3_B128 ? 2 : fmt;
+    j.router = router;
+    j.rt = rt;
+    j.renorm = renormalize != 0;
+    j.ids = topk_ids;
+    j.wts = topk_weights;
+    j.y = y;
+    j.yt = yt;
+    j.ws = ws;
+    j.stream = stream;
+    char msg[256] = {0};
+    return launched(fp4q::launch_moe(j, msg, sizeof msg), msg);
+}
+
+size_t moe_layer_workspace_bytes(int64_t tokens, int64_t dim, int64_t inter, int32_t experts, int32_t top_k) {
+    if (moe_shape("moe_layer_workspace_bytes", tokens, dim, inter, experts, top_k) != FP4Q_OK || tokens == 0) return 0;
+    return fp4q::moe_workspace_bytes(tokens, dim, inter, experts, top_k);
+}
+
 fp4q_status hadamard_block_rotate(const void* x, int32_t xt, int64_t rows, int64_t cols, int32_t n_rot,
                                   float* out, void* stream) {
     const char* fn = "hadamard_block_rotate";

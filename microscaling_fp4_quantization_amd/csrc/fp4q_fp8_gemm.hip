@@ -268,7 +268,7 @@ constexpr int kFewMaxWaves = 16;
 template <int MT, bool BROW>
 __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_fp8_few(F8Params p) {
     constexpr int U = MT == 1 ? 4 : 2;  // K blocks in flight per wave
-    extern __shared__ float red[];      // waves x MT x 16 x 16
+    extern __shared__ __attribute__((aligned(16))) float red[];  // waves x MT x 16 x 16
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int waves = blockDim.x / kWave;

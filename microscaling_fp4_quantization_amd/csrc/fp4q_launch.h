@@ -145,6 +145,33 @@ struct Fp8GemmJob {
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+// Mixture-of-experts layer for a few tokens.
+struct MoeWeights {
+    const uint8_t* codes;  // (E * rows) x K
+    const void* scales;
+    const float* g;        // nullable (1)
+    bool g_per_expert;
+};
+struct MoeJob {
+    const void* x;
+    int xt;                // 0 bf16, 1 f32
+    int64_t T, D, I, E, k;
+    int fmt;               // 0 MXFP4, 1 UE4M3 block 16, 2 E4M3 block 128
+    MoeWeights w13, w2;
+    const void* router;    // nullable: ids and wts are given
+    int rt;
+    int renorm;
+    int* ids;
+    float* wts;
+    void* y;
+    int yt;
+    void* ws;              // moe_workspace_bytes(...) bytes, its first 256 zero
+    void* stream;
+};
+
+constexpr int64_t kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxSize = 1 << 20;
+size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t I, int64_t E, int64_t k);
+
 // Launch timing (fp4q_profile_events): while the calling thread has event
 // pairs left, every kernel launch records the next pair on its stream around
 // itself.  Streams and events are passed as void*.
@@ -184,6 +211,7 @@ int launch_gemm(const GemmJob& j, char* msg, size_t msg_len);
 int launch_gemm_nvfp4(const GemmNvJob& j, char* msg, size_t msg_len);
 int launch_fp8_quantize(const Fp8QuantJob& j, char* msg, size_t msg_len);
 int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len);
+int launch_moe(const MoeJob& j, char* msg, size_t msg_len);
 
 // Adds the binary32 partial products of `splits` K ranges (splits x count, range
 // by range) in binary64 and writes c (ct: 0 bf16, 1 f32); partial and c are
