@@ -63,14 +63,16 @@ struct F8Params {
     float* partial;    // splits > 1: splits x M x N
 };
 
-// 32 x 32 x 64 products of E4M3 operands (block scales of 1).
-constexpr int kOne = 0x7F7F7F7F;
-__device__ __forceinline__ v16f mma32(v8i b, v8i a, v16f c) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, kFmtE4M3, kFmtE4M3, 0, kOne, 0, kOne);
+// 16 x 16 x 128 products.  Lane l supplies 32 bytes of row l % 16 of each operand,
+// those of quarter l / 16 of the block, and receives column l % 16 of the second
+// operand, rows 4 (l / 16) .. + 3 of the first.  The 8-bit form is the one without
+// block scales (scale operands of 0), which ran at 4.9 PFLOP/s from registers at two
+// waves per SIMD, where the 32 x 32 x 64 one with scales reached 4.4.  On the bf16
+// cores step t takes the lane's bytes 8 t .. 8 t + 7 of both operands, so that every
+// element meets its partner once.
+__device__ __forceinline__ v4f mma16(v8i b, v8i a) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, v4f{}, kFmtE4M3, kFmtE4M3, 0, 0, 0, 0);
 }
-
-// The same on the bf16 cores, and 16 x 16 x 128: step t takes the lane's bytes 8 t ..
-// 8 t + 7 of both operands, so that every element meets its partner once.
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 struct Wide {
     bf16x8_t v[4];
@@ -85,12 +87,8 @@ __device__ __forceinline__ bf16x8_t widen8(int lo, int hi) {
 __device__ __forceinline__ Wide widen(v8i x) {
     return Wide{{widen8(x[0], x[1]), widen8(x[2], x[3]), widen8(x[4], x[5]), widen8(x[6], x[7])}};
 }
-__device__ __forceinline__ v16f mma32(const Wide& b, const Wide& a, v16f c) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[t], a.v[t], c, 0, 0, 0);
-    return c;
-}
-__device__ __forceinline__ v4f mma16(const Wide& b, const Wide& a, v4f c) {
+__device__ __forceinline__ v4f mma16(const Wide& b, const Wide& a) {
+    v4f c = {};
 #pragma unroll
     for (int t = 0; t < 4; ++t) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[t], a.v[t], c, 0, 0, 0);
     return c;
@@ -98,19 +96,122 @@ __device__ __forceinline__ v4f mma16(const Wide& b, const Wide& a, v4f c) {
 
 __device__ __forceinline__ v8i join(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
 
-// Lane l's operand of depth T (64 of the stage's 128 elements): pieces 4 T +
-// 2 (l / 32) and the next of row l % 32, stored at slot (piece + row / 2) % 8.
-template <int T>
-__device__ __forceinline__ v8i read_op(const uint8_t* codes, int row, int lane) {
-    const int p = 4 * T + 2 * (lane / kFrag), rot = row / 2;
-    const v4i lo = *reinterpret_cast<const v4i*>(codes + row * kRowStage + ((p + rot) & 7) * 16);
-    const v4i hi = *reinterpret_cast<const v4i*>(codes + row * kRowStage + ((p + 1 + rot) & 7) * 16);
-    return join(lo, hi);
+// An operand as the products take it: the codes, or their bf16 values.
+template <bool WIDE>
+struct Operand {
+    typedef v8i T;
+    static __device__ __forceinline__ v8i of(v8i x) { return x; }
+};
+template <>
+struct Operand<true> {
+    typedef Wide T;
+    static __device__ __forceinline__ Wide of(v8i x) { return widen(x); }
+};
+
+constexpr int kF16 = 16;                          // rows per fragment
+constexpr int TA = WM / kF16, TB = WN / kF16;     // fragments of a wave's tile: 8 of A, 4 of B
+
+// A row's eight 16-byte pieces sit in LDS at slot piece ^ (row / 2) % 8.  Lane l
+// takes pieces l / 16 and 4 + l / 16 of row l % 16 of a fragment (a permutation of
+// the block's elements, the same for both operands): the lanes that a ds_read_b128
+// serves together (0-3, 12-15, 20-23, 24-27, and so on) then meet 16 distinct bank
+// groups.  Fragments are 16 rows apart, which leaves the slots alone.
+__device__ __forceinline__ int op_offset(int row, int lane, int half) {
+    return row * kRowStage + ((lane / kF16 + 4 * half) ^ ((row / 2) & 7)) * 16;
+}
+__device__ __forceinline__ v8i read_op(const uint8_t* lo, const uint8_t* hi, int frag) {
+    return join(*reinterpret_cast<const v4i*>(lo + frag * kF16 * kRowStage),
+                *reinterpret_cast<const v4i*>(hi + frag * kF16 * kRowStage));
+}
+
+// The epilogue of the FP4 kernels (store_tile) for these fragments.  It is written
+// out here because theirs, cut in two to share its second half, ran 1.5% slower.
+template <int EB>
+struct EpiPlan {
+    static constexpr int kPitch = BN * EB;                   // LDS bytes per row
+    static constexpr int kRowsPass = kEpiBytes / kPitch;     // 256 (bf16) or 128 (f32)
+    static constexpr int kPasses = BM / kRowsPass;
+    static constexpr int kRowsInstr = 1024 / kPitch;         // rows per wave-wide 1 KB store
+    static constexpr int kInstr = kRowsPass / kRowsInstr / kWaves;
+    static_assert(kRowsPass % WM == 0 && kInstr * kRowsInstr * kWaves == kRowsPass, "epilogue plan");
+};
+
+// Four columns of group `grp` of LDS row r.
+template <int EB>
+__device__ __forceinline__ void put_quad(uint8_t* lds, int r, int grp, float a, float b, float c, float d) {
+    *reinterpret_cast<typename Quad<EB>::T*>(lds + r * EpiPlan<EB>::kPitch + (grp ^ (r & 31)) * 4 * EB) =
+        Quad<EB>::pack(a, b, c, d);
+}
+
+// Stores the rows of pass h from LDS, after a barrier.
+template <int EB>
+__device__ __forceinline__ void store_pass(const uint8_t* lds, int h, Rsrc rc, int wave, int lane, int64_t rows_a,
+                                           int64_t n0, int64_t N) {
+    typedef EpiPlan<EB> P;
+#pragma unroll
+    for (int k = 0; k < P::kInstr; ++k) {
+        const int r = (wave * P::kInstr + k) * P::kRowsInstr + lane / (P::kPitch / 16);
+        const int q = lane % (P::kPitch / 16);  // 16-byte unit within the row
+        u32x4_t v;
+        if (EB == 4) {
+            v = *reinterpret_cast<const u32x4_t*>(lds + r * P::kPitch + ((q ^ (r & 31)) * 16));
+        } else {
+            const int grp = (2 * q) ^ (r & 31);
+            v = *reinterpret_cast<const u32x4_t*>(lds + r * P::kPitch + (grp >> 1) * 16);
+            if (r & 1) v = u32x4_t{v[2], v[3], v[0], v[1]};
+        }
+        const int64_t row = h * P::kRowsPass + r, col = n0 + q * (16 / EB);
+        const int off = row < rows_a && col < N ? (int)(row * N * EB + col * EB) : kDropped;
+        __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, kStoreNT);
+    }
+}
+
+// Lane l, register e of acc[i][j]: row of A wm * WM + 16 j + l % 16, row of B
+// wn * WN + 16 i + 4 (l / 16) + e.
+template <int EB>
+__device__ __forceinline__ void store_tile16(const v4f (&acc)[TB][TA], uint8_t* lds, Rsrc rc, int wave, int wm,
+                                             int wn, int lane, int64_t rows_a, int64_t n0, int64_t N) {
+    typedef EpiPlan<EB> P;
+#pragma unroll
+    for (int h = 0; h < P::kPasses; ++h) {
+        if (wm * WM / P::kRowsPass == h) {
+#pragma unroll
+            for (int j = 0; j < TA; ++j)
+#pragma unroll
+                for (int i = 0; i < TB; ++i)
+                    put_quad<EB>(lds, wm * WM + j * kF16 + lane % kF16 - h * P::kRowsPass,
+                                 (wn * WN + i * kF16) / 4 + lane / kF16, acc[i][j][0], acc[i][j][1], acc[i][j][2],
+                                 acc[i][j][3]);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        store_pass<EB>(lds, h, rc, wave, lane, rows_a, n0, N);
+        if (h + 1 < P::kPasses) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+}
+
+// Rows of C that are not whole 16-byte units: element by element.
+__device__ __forceinline__ void store_direct16(const v4f (&acc)[TB][TA], Rsrc rc, int ct, int wm, int wn, int lane,
+                                               int64_t rows_a, int64_t n0, int64_t N) {
+    const int eb = ct == 1 ? 4 : 2;
+#pragma unroll
+    for (int j = 0; j < TA; ++j) {
+        const int row = wm * WM + j * kF16 + lane % kF16;
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t col = n0 + wn * WN + i * kF16 + 4 * (lane / kF16) + e;
+                const int off = row < rows_a && col < N ? (int)((row * N + col) * eb) : kDropped;
+                if (ct == 1) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][e]), rc, off, 0, kStoreNT);
+                else __builtin_amdgcn_raw_buffer_store_b16((unsigned short)to_bf16(acc[i][j][e]), rc, off, 0, kStoreNT);
+            }
+    }
 }
 
 template <bool BROW, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
+    typedef Operand<WIDE> Op;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave >> 2, wn = wave & 3;  // 2 x 4 waves of 128 x 64
@@ -129,120 +230,130 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const Rsrc rb = make_rsrc(p.b + n0 * K, rows_b * K);
 
     // Code load q of a wave moves rows 8 d .. 8 d + 7, d = wave + 8 (q % 4), of A
-    // (q < 4) or B: lane l fetches row 8 d + l / 8 into slot l % 8 of that row,
-    // which holds piece (l % 8 - row / 2) % 8 (the same for every q: row / 2 = 4 d +
-    // l / 16 and d = wave mod 2).
-    const int piece = ((lane % 8) - 4 * (wave & 1) - lane / 16) & 7;
+    // (q < 4) or B: lane l fetches row 8 d + l / 8 into slot l % 8 of that row (row /
+    // 2 = 4 d + l / 16 and d = wave mod 2, so that the piece is the same for every q).
+    const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
     const int lane_off = (lane / 8) * K + piece * 16;
-    auto issue = [&](uint8_t* stage, int s) {
-        const int k0 = s * kBlock;
-        const int base = k0 + piece * 16 < K ? lane_off + k0 : kPastWindow;
-#pragma unroll
-        for (int q = 0; q < kLoads; ++q) {
-            const bool is_a = q < kLoads / 2;
-            const int d = wave + kWaves * (q % (kLoads / 2));
-            uint8_t* dst = stage + (is_a ? 0 : BM * kRowStage) + d * 8 * kRowStage;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (LdsPtr)dst, 16, base + 8 * d * K, 0, 0, 0);
-        }
-        // Scales: waves 0-3 bring 64 rows of A each, waves 4-7 of B; B's tile
-        // scales are spread to one per row.
-        const int r = (wave % 4) * kWave + lane;
-        uint8_t* dst = stage + kCodeBytes + wave * kWave * 4;
-        if (wave < 4) {
-            const Rsrc rs = make_rsrc(p.sa + (int64_t)s * p.M + m0, rows_a * 4);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)dst, 4, r * 4, 0, 0, 0);
-        } else if (BROW) {
-            const Rsrc rs = make_rsrc(p.sb + (int64_t)s * p.N + n0, rows_b * 4);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)dst, 4, r * 4, 0, 0, 0);
+    // Scales of a stage: waves 0-3 bring 64 rows of A each, waves 4-7 of B; B's tile
+    // scales are spread to one per row.  Chosen once per wave, so that the K loop
+    // has no branch: a stage's window starts sc_step floats after the one before.
+    const bool sc_a = wave < 4;
+    const int sc_row = (wave % 4) * kWave + lane;
+    const float* sc_base = sc_a ? p.sa + m0 : BROW ? p.sb + n0 : p.sb + n0 / kBlock * S;
+    const int64_t sc_step = sc_a ? p.M : BROW ? p.N : 1;
+    const int sc_size = (int)(sc_a ? rows_a : BROW ? rows_b : (rows_b + kBlock - 1) / kBlock * S) * 4;
+    const int sc_shrink = sc_a || BROW ? 0 : 4;  // the tile scales' window ends where it did
+    const int sc_off = (sc_a || BROW ? sc_row : sc_row / kBlock * S) * 4;
+    // Load L of stage s: the code loads, then the scales.  A stage past the range
+    // reads zero codes (and some other stage's scales).
+    auto issue = [&](int s, int L) {
+        uint8_t* stage = lds + (s & 1) * kStageBytes;
+        if (L < kLoads) {
+            const int k0 = s * kBlock;
+            const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
+            const int d = wave + kWaves * (L % (kLoads / 2));
+            uint8_t* dst = stage + (L < kLoads / 2 ? 0 : BM * kRowStage) + d * 8 * kRowStage;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? ra : rb, (LdsPtr)dst, 16, base + 8 * d * K, 0, 0, 0);
         } else {
-            const Rsrc rs = make_rsrc(p.sb + n0 / kBlock * S, (rows_b + kBlock - 1) / kBlock * S * 4);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)dst, 4, (r / kBlock * S + s) * 4, 0, 0, 0);
+            const int at = s < s_hi ? s : s_lo;
+            const Rsrc rs = make_rsrc(sc_base + at * sc_step, sc_size - at * sc_shrink);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(stage + kCodeBytes + wave * kWave * 4), 4, sc_off, 0, 0, 0);
         }
     };
 
-    v16f acc[FB][FA];
+    v4f acc[TB][TA];
 #pragma unroll
-    for (int i = 0; i < FB; ++i)
+    for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < FA; ++j) acc[i][j] = v16f{};
+        for (int j = 0; j < TA; ++j) acc[i][j] = v4f{};
 
-    const int a_row = wm * WM + lane % kFrag;  // within the tile
-    const int b_row = wn * WN + lane % kFrag;
-    if (s_lo < s_hi) issue(lds + (s_lo & 1) * kStageBytes, s_lo);
+    // Groups of products: NI fragments of B against fragment j of A.  While a
+    // group's products run, the previous group's are scaled into the sums, the next
+    // fragment of A is read and loads of the next stage go out, kEarly per group: early
+    // enough to land within the stage, without a burst that fills the load queue.
+    // Where registers allow (kCarry), the last group's products of a stage are
+    // scaled in the next one, while its first operands are on their way from LDS.
+    constexpr int NI = WIDE ? 2 : TB, kPasses = TB / NI, kGroups = kPasses * TA;
+    constexpr bool kCarry = !BROW && !WIDE;
+    constexpr int kEarly = 2;
+    v4f t[2][NI];
+    float f_old = 0.0f, sb_old = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) t[1][i] = v4f{};
+    const int a_row = wm * WM + lane % kF16;  // within the tile
+    const int b_row = wn * WN + lane % kF16;
+    const int a_lo = op_offset(a_row, lane, 0), a_hi = op_offset(a_row, lane, 1);
+    const int b_lo = BM * kRowStage + op_offset(b_row, lane, 0), b_hi = BM * kRowStage + op_offset(b_row, lane, 1);
+    auto scale_in = [&](int i0, int i, int j, const v4f& d, float f, const v4f& sb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i0 + i][j][e] = fmaf(BROW ? d[e] * sb[e] : d[e], f, acc[i0 + i][j][e]);
+    };
+    if (s_lo < s_hi) {  // K = 0 has no operands to read
+#pragma unroll
+        for (int L = 0; L <= kLoads; ++L) issue(s_lo, L);
+    }
     for (int s = s_lo; s < s_hi; ++s) {
         const uint8_t* here = lds + (s & 1) * kStageBytes;
-        // Stage s has landed, and no wave still reads stage s - 1.
-        wait_all_barrier();
-        if (s + 1 < s_hi) issue(lds + ((s + 1) & 1) * kStageBytes, s + 1);
-        const uint8_t* ca = here;
-        const uint8_t* cb = here + BM * kRowStage;
-        const float* fa = reinterpret_cast<const float*>(here + kCodeBytes);
-        const float* fb = fa + BM;
-        if (!BROW && !WIDE) {
-            const float sb = fb[wn * WN];
-            v8i b[FB][2];
+        const float* fa = reinterpret_cast<const float*>(here + kCodeBytes) + a_row;
+        const float* fb = reinterpret_cast<const float*>(here + kCodeBytes) + BM + wn * WN;
+        // Stage s has landed, and no wave still reads stage s - 1.  (The compiler's own
+        // wait, so that it adds none before the first operands arrive.)
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+        v8i a_next = read_op(here + a_lo, here + a_hi, 0);
+        float f_next, sb_tile;
 #pragma unroll
-            for (int i = 0; i < FB; ++i) {
-                b[i][0] = read_op<0>(cb, b_row + i * kFrag, lane);
-                b[i][1] = read_op<1>(cb, b_row + i * kFrag, lane);
+        for (int g = 0; g < kPasses; ++g) {
+            typename Op::T b[NI];
+            v4f sb[BROW ? NI : 1];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                __builtin_amdgcn_sched_barrier(0);  // the first products wait for as few reads as can be
+                b[i] = Op::of(read_op(here + b_lo, here + b_hi, g * NI + i));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (g == 0) f_next = fa[0], sb_tile = BROW ? 1.0f : fb[0];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                if (BROW) sb[i] = *reinterpret_cast<const v4f*>(fb + (g * NI + i) * kF16 + 4 * (lane / kF16));
             }
 #pragma unroll
-            for (int j = 0; j < FA; ++j) {
-                const v8i a0 = read_op<0>(ca, a_row + j * kFrag, lane);
-                const v8i a1 = read_op<1>(ca, a_row + j * kFrag, lane);
-                const float f = fa[a_row + j * kFrag] * sb;
-                v16f t[FB];
+            for (int j = 0; j < TA; ++j) {
+                const int n = g * TA + j;
+                const typename Op::T a = Op::of(a_next);
+                const float f = f_next;
+                if (n + 1 < kGroups) {
+                    a_next = read_op(here + a_lo, here + a_hi, (n + 1) % TA);
+                    f_next = fa[(n + 1) % TA * kF16];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                const float scale = BROW ? f_old : f_old * sb_old;
 #pragma unroll
-                for (int i = 0; i < FB; ++i) t[i] = mma32(b[i][0], a0, v16f{});
+                for (int i = 0; i < NI; ++i) {
+                    t[n % 2][i] = mma16(b[i], a);
+                    if (kCarry || j > 0)
+                        scale_in(g * NI, i, (j + TA - 1) % TA, t[(n + 1) % 2][i], scale, sb[BROW ? i : 0]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (i == 0) {
 #pragma unroll
-                for (int i = 0; i < FB; ++i) t[i] = mma32(b[i][1], a1, t[i]);
-#pragma unroll
-                for (int i = 0; i < FB; ++i)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(t[i][e], f, acc[i][j][e]);
+                        for (int e = 0; e < kEarly; ++e)
+                            if (n * kEarly + e <= kLoads) issue(s + 1, n * kEarly + e);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                f_old = f;
+                if (j == 0) sb_old = sb_tile;
             }
-        } else {
+            if (!kCarry) {
+                const float scale = BROW ? f_old : f_old * sb_old;
 #pragma unroll
-            for (int i = 0; i < FB; ++i) {
-                const v8i b0 = read_op<0>(cb, b_row + i * kFrag, lane);
-                const v8i b1 = read_op<1>(cb, b_row + i * kFrag, lane);
-                Wide w0, w1;
-                if (WIDE) w0 = widen(b0), w1 = widen(b1);
-                // Result register e of lane l is row 8 (e / 4) + 4 (l / 32) + e % 4.
-                v4f sb[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    if (BROW) sb[g] = *reinterpret_cast<const v4f*>(fb + wn * WN + i * kFrag + 8 * g + 4 * (lane / kFrag));
-                    else sb[g] = v4f{} + fb[wn * WN];
-                }
-                v8i a0 = read_op<0>(ca, a_row, lane), a1 = read_op<1>(ca, a_row, lane);
-#pragma unroll
-                for (int j = 0; j < FA; ++j) {
-                    const float f = fa[a_row + j * kFrag];
-                    v16f t;
-                    if (WIDE) {
-                        t = mma32(w0, widen(a0), v16f{});
-                        t = mma32(w1, widen(a1), t);
-                    } else {
-                        t = mma32(b0, a0, v16f{});
-                        t = mma32(b1, a1, t);
-                    }
-                    if (j + 1 < FA) {
-                        a0 = read_op<0>(ca, a_row + (j + 1) * kFrag, lane);
-                        a1 = read_op<1>(ca, a_row + (j + 1) * kFrag, lane);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);  // no more of A at once than the registers hold
-                    if (BROW) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(t[e] * sb[e / 4][e % 4], f, acc[i][j][e]);
-                    } else {
-                        const float g = f * sb[0][0];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(t[e], g, acc[i][j][e]);
-                    }
-                }
+                for (int i = 0; i < NI; ++i) scale_in(g * NI, i, TA - 1, t[1][i], scale, sb[BROW ? i : 0]);
             }
         }
+    }
+    if (kCarry) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) scale_in(0, i, TA - 1, t[1][i], f_old * sb_old, v4f{});
     }
     wait_all_barrier();  // LDS is reused below
 
@@ -250,9 +361,9 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const int ct = splits > 1 ? 1 : p.ct;
     const int eb = ct == 1 ? 4 : 2;
     const Rsrc rc = make_rsrc(static_cast<char*>(c) + m0 * p.N * eb, rows_a * p.N * eb);
-    if (((p.N * eb) & 15) != 0) store_direct(acc, rc, ct, wm, wn, lane, rows_a, n0, p.N);
-    else if (ct == 1) store_tile<4>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
-    else store_tile<2>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
+    if (((p.N * eb) & 15) != 0) store_direct16(acc, rc, ct, wm, wn, lane, rows_a, n0, p.N);
+    else if (ct == 1) store_tile16<4>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
+    else store_tile16<2>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
 }
 
 // ---------------------------------------------------------------------------
@@ -318,7 +429,7 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_fp8_few(F8Params 
             const Wide bw = widen(join(b[u][0], b[u][1]));
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                const v4f d = mma16(bw, widen(join(a[u][t][0], a[u][t][1])), v4f{});
+                const v4f d = mma16(bw, widen(join(a[u][t][0], a[u][t][1])));
                 const float f = BROW ? sa[u][t] : sa[u][t] * sb[u][0];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(BROW ? d[e] * sb[u][e] : d[e], f, acc[t][e]);
