@@ -446,11 +446,12 @@ fp4q_status fp8_quantize_b128(const void* x, int32_t xt, int64_t rows, int64_t c
  *   ws, ws_bytes        device scratch of fp8_gemm_b128_workspace_bytes(M, N, K)
  *                       bytes (0 for most shapes; then ws may be NULL), 16-byte
  *                       aligned: partial products of K ranges
- * At most 64 rows of A take a kernel that streams B once; others 256 x 256 tiles.
+ * At most 16 rows of A take a kernel that streams B once; others 64 x 64, 128 x 128 or
+ * 256 x 256 tiles, by the shape.
  * Each block's 128 products are added by the matrix cores from zero and go under
  * the binary32 product of the two scales into a binary32 sum, K ranges in
  * binary64.  A binary32 C differs from the exact product by rounding of order
- * (K / 128 + 8) * 2^-23 of sum |a_hat| |b_hat|.  A bf16 C of more than 64 rows is
+ * (K / 128 + 8) * 2^-23 of sum |a_hat| |b_hat|.  A bf16 C of more than 16 rows is
  * computed on the 8-bit matrix cores, whose sums hold about 16 bits (2^-15.5 of sum
  * |a_hat| |b_hat|), and rounded.  Scale products below 2^-126 lose their low bits.
  * The same on every run for a given shape.

@@ -22,7 +22,9 @@
 //  k_gemm_fp8        a workgroup of 8 waves computes a 256 x 256 tile of C, as
 //                    the FP4 kernels do, one K block of 128 bytes per row (a
 //                    cache line) per stage, through two LDS stages;
-//  k_gemm_fp8_few    at most 64 rows of A: one pass over B, 16 rows of B per
+//  k_gemm_fp8_mid    the same in 128 x 128 or 64 x 64 tiles, for products that the
+//                    large tile leaves the chip idle with;
+//  k_gemm_fp8_few    at most 16 rows of A: one pass over B, 16 rows of B per
 //                    workgroup, K blocks dealt to its waves in turn; bound by the
 //                    read of B, so always on the bf16 form.
 //
@@ -166,12 +168,33 @@ __device__ __forceinline__ void store_pass(const uint8_t* lds, int h, Rsrc rc, i
     }
 }
 
+// The same rows element by element, for rows of C that are not whole 16-byte units:
+// a wave's store is one run of 64 elements.
+template <int EB>
+__device__ __forceinline__ void store_pass_any(const uint8_t* lds, int h, Rsrc rc, int wave, int lane,
+                                               int64_t rows_a, int64_t n0, int64_t N) {
+    typedef EpiPlan<EB> P;
+    for (int r = wave; r < P::kRowsPass; r += kWaves) {
+        const int64_t row = h * P::kRowsPass + r;
+        if (row >= rows_a) break;
+#pragma unroll
+        for (int c0 = 0; c0 < BN; c0 += kWave) {
+            const int c = c0 + lane;
+            const uint8_t* src = lds + r * P::kPitch + ((c / 4) ^ (r & 31)) * 4 * EB + c % 4 * EB;
+            const int off = n0 + c < N ? (int)((row * N + n0 + c) * EB) : kDropped;
+            if (EB == 4) __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<const uint32_t*>(src), rc, off, 0, kStoreNT);
+            else __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<const uint16_t*>(src), rc, off, 0, kStoreNT);
+        }
+    }
+}
+
 // Lane l, register e of acc[i][j]: row of A wm * WM + 16 j + l % 16, row of B
 // wn * WN + 16 i + 4 (l / 16) + e.
 template <int EB>
 __device__ __forceinline__ void store_tile16(const v4f (&acc)[TB][TA], uint8_t* lds, Rsrc rc, int wave, int wm,
                                              int wn, int lane, int64_t rows_a, int64_t n0, int64_t N) {
     typedef EpiPlan<EB> P;
+    const bool whole = ((N * EB) & 15) == 0;
 #pragma unroll
     for (int h = 0; h < P::kPasses; ++h) {
         if (wm * WM / P::kRowsPass == h) {
@@ -184,27 +207,9 @@ __device__ __forceinline__ void store_tile16(const v4f (&acc)[TB][TA], uint8_t* 
                                  acc[i][j][3]);
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        store_pass<EB>(lds, h, rc, wave, lane, rows_a, n0, N);
+        if (whole) store_pass<EB>(lds, h, rc, wave, lane, rows_a, n0, N);
+        else store_pass_any<EB>(lds, h, rc, wave, lane, rows_a, n0, N);
         if (h + 1 < P::kPasses) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    }
-}
-
-// Rows of C that are not whole 16-byte units: element by element.
-__device__ __forceinline__ void store_direct16(const v4f (&acc)[TB][TA], Rsrc rc, int ct, int wm, int wn, int lane,
-                                               int64_t rows_a, int64_t n0, int64_t N) {
-    const int eb = ct == 1 ? 4 : 2;
-#pragma unroll
-    for (int j = 0; j < TA; ++j) {
-        const int row = wm * WM + j * kF16 + lane % kF16;
-#pragma unroll
-        for (int i = 0; i < TB; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t col = n0 + wn * WN + i * kF16 + 4 * (lane / kF16) + e;
-                const int off = row < rows_a && col < N ? (int)((row * N + col) * eb) : kDropped;
-                if (ct == 1) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][e]), rc, off, 0, kStoreNT);
-                else __builtin_amdgcn_raw_buffer_store_b16((unsigned short)to_bf16(acc[i][j][e]), rc, off, 0, kStoreNT);
-            }
     }
 }
 
@@ -361,25 +366,171 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const int ct = splits > 1 ? 1 : p.ct;
     const int eb = ct == 1 ? 4 : 2;
     const Rsrc rc = make_rsrc(static_cast<char*>(c) + m0 * p.N * eb, rows_a * p.N * eb);
-    if (((p.N * eb) & 15) != 0) store_direct16(acc, rc, ct, wm, wn, lane, rows_a, n0, p.N);
-    else if (ct == 1) store_tile16<4>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
+    if (ct == 1) store_tile16<4>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
     else store_tile16<2>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
 }
 
 // ---------------------------------------------------------------------------
-// At most 64 rows of A: C is a pass over B.  A workgroup takes 16 rows of B; its
+// Products with too few 256 x 256 tiles to fill the chip: the same in tiles of T x T
+// (128 or 64), four waves of T / 2 x T / 2, through two LDS stages; two or four
+// workgroups share a CU and cover each other's waits (a third stage, which leaves room
+// for fewer, was 5% slower at T = 64 and 1.4 times as slow at T = 128).
+
+template <int T>
+struct MidPlan {
+    static constexpr int kF = T / 2 / kF16;                // fragments per wave and side
+    static constexpr int kCode = 2 * T * kRowStage;        // a stage's codes: T rows of A, T of B
+    static constexpr int kStage = kCode + 2 * T * 4;       // and scales
+    static constexpr int kCodeLoads = 2 * T / 8 / 4;       // direct loads per wave and stage
+    static constexpr int kPitch = T + 4;                   // floats per row of the staged result: 16-byte
+                                                           // writes of 16 rows fall in distinct banks
+    static constexpr int kLds = 2 * kStage > T * kPitch * 4 ? 2 * kStage : T * kPitch * 4;
+};
+
+template <int T, bool BROW, bool WIDE>
+__global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_fp8_mid(F8Params p) {
+    typedef MidPlan<T> P;
+    typedef Operand<WIDE> Op;
+    constexpr int F = P::kF;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / 2, wn = wave % 2;
+    const int64_t tiles_m = (p.M + T - 1) / T, tiles_n = (p.N + T - 1) / T;
+    const int splits = p.splits, split = (int)(blockIdx.x % splits);
+    int64_t tm, tn;
+    tile_of(blockIdx.x / splits, tiles_m, tiles_n, tm, tn);
+    const int64_t m0 = tm * T, n0 = tn * T;
+    const int rows_a = (int)(p.M - m0 < T ? p.M - m0 : T), rows_b = (int)(p.N - n0 < T ? p.N - n0 : T);
+    const int K = (int)p.K, S = p.S;
+    const int per = (S + splits - 1) / splits;
+    const int s_lo = split * per, s_hi = s_lo + per < S ? s_lo + per : S;
+    const Rsrc ra = make_rsrc(p.a + m0 * K, (int64_t)rows_a * K);
+    const Rsrc rb = make_rsrc(p.b + n0 * K, (int64_t)rows_b * K);
+
+    // Code load q of a wave moves rows 8 d .. 8 d + 7 of the 2 T (A's, then B's), d =
+    // 4 q + wave; slots as in the tile kernel (T is a multiple of 16).
+    const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
+    const int lane_off = (lane / 8) * K + piece * 16;
+    // Scales: waves 0 and 1 bring A's, 2 and 3 B's, 64 each (T = 64: the same twice).
+    const bool sc_a = wave < 2;
+    const int sc_row = (wave % 2 * kWave + lane) % T;
+    const float* sc_base = sc_a ? p.sa + m0 : BROW ? p.sb + n0 : p.sb + n0 / kBlock * S;
+    const int64_t sc_step = sc_a ? p.M : BROW ? p.N : 1;
+    const int sc_size = (sc_a ? rows_a : BROW ? rows_b : S) * 4;
+    const int sc_shrink = sc_a || BROW ? 0 : 4;
+    const int sc_off = sc_a || BROW ? sc_row * 4 : 0;  // a tile's 64 or 128 rows are in one block of B
+    auto issue = [&](int s) {
+        uint8_t* stage = lds + (s & 1) * P::kStage;
+        const int k0 = s * kBlock;
+        const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
+#pragma unroll
+        for (int q = 0; q < P::kCodeLoads; ++q) {
+            const int d = 4 * q + wave;
+            const bool is_a = q < P::kCodeLoads / 2;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (LdsPtr)(stage + d * 8 * kRowStage), 16,
+                                                     base + (is_a ? 8 * d : 8 * d - T) * K, 0, 0, 0);
+        }
+        const int at = s < s_hi ? s : s_lo;
+        const Rsrc rs = make_rsrc(sc_base + at * sc_step, sc_size - at * sc_shrink);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, (LdsPtr)(stage + P::kCode + ((sc_a ? 0 : T) + wave % 2 * kWave % T) * 4), 4, sc_off, 0, 0, 0);
+    };
+
+    v4f acc[F][F];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = v4f{};
+    const int a_row = wm * (T / 2) + lane % kF16, b_row = wn * (T / 2) + lane % kF16;
+    const int a_lo = op_offset(a_row, lane, 0), a_hi = op_offset(a_row, lane, 1);
+    const int b_lo = T * kRowStage + op_offset(b_row, lane, 0), b_hi = T * kRowStage + op_offset(b_row, lane, 1);
+    if (s_lo < s_hi) issue(s_lo);  // K = 0 has no operands to read
+    for (int s = s_lo; s < s_hi; ++s) {
+        const uint8_t* here = lds + (s & 1) * P::kStage;
+        // Stage s has landed, and no wave still reads stage s - 1.
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+        issue(s + 1);
+        const float* fa = reinterpret_cast<const float*>(here + P::kCode) + a_row;
+        const float* fb = reinterpret_cast<const float*>(here + P::kCode) + T + wn * (T / 2);
+        typename Op::T b[F];
+        v4f sb[BROW ? F : 1];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            b[i] = Op::of(read_op(here + b_lo, here + b_hi, i));
+            if (BROW) sb[i] = *reinterpret_cast<const v4f*>(fb + i * kF16 + 4 * (lane / kF16));
+        }
+        const float sb_tile = BROW ? 1.0f : fb[0];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const typename Op::T a = Op::of(read_op(here + a_lo, here + a_hi, j));
+            const float f = fa[j * kF16] * sb_tile;
+            v4f t[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) t[i] = mma16(b[i], a);
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(BROW ? t[i][e] * sb[i][e] : t[i][e], f, acc[i][j][e]);
+        }
+    }
+    wait_all_barrier();  // LDS is reused below
+
+    // The tile as binary32 in LDS, then whole row segments to memory.
+    float* st = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+            *reinterpret_cast<v4f*>(st + (a_row + j * kF16) * P::kPitch + wn * (T / 2) + i * kF16 + 4 * (lane / kF16)) =
+                acc[i][j];
+    __syncthreads();
+    void* c = splits > 1 ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.c;
+    const int ct = splits > 1 ? 1 : p.ct;
+    const int eb = ct == 1 ? 4 : 2;
+    const Rsrc rc = make_rsrc(static_cast<char*>(c) + m0 * p.N * eb, (int64_t)rows_a * p.N * eb);
+    const int cols = rows_b;  // columns of C in this tile
+    if (((p.N * eb) & 15) == 0) {
+        const int units = T * eb / 16;  // 16-byte units per row
+        for (int u = threadIdx.x; u < rows_a * units; u += 256) {
+            const int r = u / units, col = u % units * (16 / eb);
+            const float* src = st + r * P::kPitch + col;
+            u32x4_t v;
+            if (ct == 1) {
+                v = *reinterpret_cast<const u32x4_t*>(src);
+            } else {
+                const v4f x = *reinterpret_cast<const v4f*>(src), y = *reinterpret_cast<const v4f*>(src + 4);
+                v = u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < cols ? (int)((r * p.N + n0 + col) * eb) : kDropped, 0, kStoreNT);
+        }
+    } else {
+        for (int u = threadIdx.x; u < rows_a * T; u += 256) {
+            const int r = u / T, col = u % T;
+            const float v = st[r * P::kPitch + col];
+            const int off = col < cols ? (int)((r * p.N + n0 + col) * eb) : kDropped;
+            if (ct == 1) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rc, off, 0, kStoreNT);
+            else __builtin_amdgcn_raw_buffer_store_b16((unsigned short)to_bf16(v), rc, off, 0, kStoreNT);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// At most 16 rows of A: C is a pass over B.  A workgroup takes 16 rows of B; its
 // waves take K blocks in turn, so that together they stream whole runs of each
 // row, and their sums meet in LDS (added in binary64, in wave order).  Lane l holds
-// row l % 16 and elements 32 (l / 16) .. + 31 of the block of each operand, both
-// read straight into registers: B is used once, A comes from the caches.
-constexpr int kFewMaxM = 64;
+// bytes 16 (l / 16) .. + 15 of both halves of the block of row l % 16 of each operand,
+// read straight into registers: B is used once, A comes from the caches.  (More rows
+// of A take 64 x 64 tiles: 32 x 3584 x 18944 took 36 us here against 22.)
+constexpr int kFewMaxM = 16;
 constexpr int kFewRows = 16;
 constexpr int kFewMaxWaves = 16;
 
-template <int MT, bool BROW>
+template <bool BROW>
 __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_fp8_few(F8Params p) {
-    constexpr int U = MT == 1 ? 4 : 2;  // K blocks in flight per wave
-    extern __shared__ __attribute__((aligned(16))) float red[];  // waves x MT x 16 x 16
+    constexpr int U = 2;  // K blocks in flight per wave (1 x 3584 x 3584: 4.9 us, 5.9 with 4)
+    __shared__ __attribute__((aligned(16))) float red[kFewMaxWaves * 256];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int waves = blockDim.x / kWave;
@@ -392,58 +543,46 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_fp8_few(F8Params 
     const Rsrc rsa = make_rsrc(p.sa, (int64_t)S * M * 4);
     const float* sb_tile = p.sb + n0 / kBlock * S;
 
-    v4f acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = v4f{};
+    v4f acc = {};
     for (int s0 = wave; s0 < S; s0 += waves * U) {
-        v4i b[U][2], a[U][MT][2];
-        float sa[U][MT], sb[U][4];
+        u32x4_t b[U][2], a[U][2];
+        float sa[U], sb[U][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * waves;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int pos = s * kBlock + q * 32 + h * 16;
-                const bool in = s < S && pos < K;
-                b[u][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, in ? r * K + pos : kDropped, 0, 0));
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    a[u][t][h] = __builtin_bit_cast(
-                        v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? (t * 16 + r) * K + pos : kDropped, 0, 0));
+                const int pos = s * kBlock + h * 64 + q * 16;
+                const int off = s < S && pos < K ? r * K + pos : kDropped;
+                b[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, off, 0, 0);
+                a[u][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, off, 0, 0);
             }
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-                sa[u][t] = __builtin_bit_cast(
-                    float, __builtin_amdgcn_raw_buffer_load_b32(rsa, s < S ? (s * M + t * 16 + r) * 4 : kDropped, 0, 0));
+            sa[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsa, s < S ? (s * M + r) * 4 : kDropped, 0, 0));
             if (BROW) {
                 const Rsrc rs = make_rsrc(p.sb + (int64_t)(s < S ? s : 0) * p.N + n0, rows_b * 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    sb[u][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (4 * q + e) * 4, 0, 0));
+                    sb[u][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (4 * q + e) * 4, 0, 0));
             } else {
                 sb[u][0] = sb_tile[s < S ? s : 0];
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const Wide bw = widen(join(b[u][0], b[u][1]));
+            const Wide bw = widen(join(__builtin_bit_cast(v4i, b[u][0]), __builtin_bit_cast(v4i, b[u][1])));
+            const Wide aw = widen(join(__builtin_bit_cast(v4i, a[u][0]), __builtin_bit_cast(v4i, a[u][1])));
+            const v4f d = mma16(bw, aw);
+            const float f = BROW ? sa[u] : sa[u] * sb[u][0];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const v4f d = mma16(bw, widen(join(a[u][t][0], a[u][t][1])));
-                const float f = BROW ? sa[u][t] : sa[u][t] * sb[u][0];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(BROW ? d[e] * sb[u][e] : d[e], f, acc[t][e]);
-            }
+            for (int e = 0; e < 4; ++e) acc[e] = fmaf(BROW ? d[e] * sb[u][e] : d[e], f, acc[e]);
         }
     }
-    // Register e of lane l: row of A 16 t + l % 16, row of B 4 (l / 16) + e.
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        *reinterpret_cast<v4f*>(red + ((wave * MT + t) * 16 + r) * 16 + 4 * q) = acc[t];
+    // Register e of lane l: row of A l % 16, row of B 4 (l / 16) + e.
+    *reinterpret_cast<v4f*>(red + (wave * 16 + r) * 16 + 4 * q) = acc;
     __syncthreads();
-    for (int e = threadIdx.x; e < MT * 256; e += blockDim.x) {
+    for (int e = threadIdx.x; e < 256; e += blockDim.x) {
         double sum = 0.0;
-        for (int w = 0; w < waves; ++w) sum += red[w * MT * 256 + e];
+        for (int w = 0; w < waves; ++w) sum += red[w * 256 + e];
         const int m = e / 16, n = e % 16;
         if (m < M && n < rows_b) {
             const int64_t at = m * p.N + n0 + n;
@@ -453,42 +592,66 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_fp8_few(F8Params 
     }
 }
 
-// K ranges per tile: as for the FP4 products, the count that makes the modelled
-// time least (rounds of workgroups x stages, plus the partial products' trip
-// through memory), in units of a stage.  A function of the shape only.
-constexpr int kChipGroups = 256;
-constexpr double kStageTraffic = 5e6;  // bytes of memory traffic in one stage's time
+// Which tile, and how many K ranges per tile: the pair that makes the modelled time
+// least.  A function of the shape and the output's type only; the workspace holds
+// either type's ranges.
 constexpr int64_t kMaxPartialBytes = (int64_t)1 << 28;
 
-int splits_for(int64_t M, int64_t N, int64_t K) {
+struct Choice {
+    int tile;    // 256, 128 or 64
+    int splits;
+};
+
+// Costs in microseconds, fitted to measured products (100 x 3584 x 3584 to 14336 x
+// 4096 x 4096): a K block of one workgroup while its CU is shared (`each`, on the 8-bit
+// and on the bf16 cores) and its latency when it is not (`alone`), a workgroup's start and
+// epilogue, and how many share a CU.
+struct TileCost {
+    int tile, per_cu;
+    double alone, each, each_wide, fixed;
+};
+constexpr TileCost kTileCosts[] = {{256, 1, 1.5, 1.5, 3.7, 6.0}, {128, 2, 0.7, 0.53, 0.95, 4.0}, {64, 4, 0.45, 0.22, 0.30, 3.0}};
+constexpr int kCus = 256;
+
+Choice choose(int64_t M, int64_t N, int64_t K, bool wide) {
     const int64_t S = (K + kBlock - 1) / kBlock;
-    const int64_t tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
-    if (S < 2 || tiles >= 2 * kChipGroups || N * 4 >= ((int64_t)1 << 23)) return 1;
-    auto cost = [&](int64_t sp) {
-        const double rounds = (double)((tiles * sp + kChipGroups - 1) / kChipGroups);
-        const double run = rounds * (double)((S + sp - 1) / sp + 3);
-        return sp == 1 ? run : run + 4.0 + 8.0 * (double)sp * (double)M * (double)N / kStageTraffic;
-    };
-    int64_t best = 1;
-    for (int64_t sp = 2; sp <= std::min<int64_t>(S, 64); ++sp) {
-        if (4 * sp * M * N > kMaxPartialBytes) break;
-        if ((S + sp - 1) / sp * (sp - 1) >= S) continue;  // a range would be empty
-        if (cost(sp) < cost(best)) best = sp;
+    const bool may_split = N * 4 < ((int64_t)1 << 23);
+    Choice best{256, 1};
+    double least = 1e300;
+    for (const TileCost& c : kTileCosts) {
+        const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
+        const double each = wide ? c.each_wide : c.each;
+        for (int64_t sp = 1; sp <= std::min<int64_t>(std::max<int64_t>(S, 1), 64); ++sp) {
+            const int64_t per = (S + sp - 1) / sp;
+            if (sp > 1 && (!may_split || tiles * sp > 4 * kCus || 4 * sp * M * N > kMaxPartialBytes)) break;
+            if (sp > 1 && per * (sp - 1) >= S) continue;  // a range would be empty
+            // Workgroups on the busiest CU, a full share at a time.
+            const int64_t groups = (tiles * sp + kCus - 1) / kCus, full = groups / c.per_cu, rest = groups % c.per_cu;
+            double t = (double)full * ((double)per * std::max(c.alone, each * c.per_cu) + c.fixed);
+            if (rest) t += (double)per * std::max(c.alone, each * (double)rest) + c.fixed;
+            // The partial products' trip through memory, and the launch that adds them.
+            if (sp > 1) t += 3.0 + 8.0 * (double)sp * (double)M * (double)N / 8e6;
+            if (t < least) least = t, best = Choice{c.tile, (int)sp};
+        }
     }
-    return (int)best;
+    return best;
 }
 
-template <int MT, bool BROW>
-void launch_few(const F8Params& p, int waves, hipStream_t stream) {
-    const unsigned grid = (unsigned)((p.N + kFewRows - 1) / kFewRows);
-    FP4Q_LAUNCH((k_gemm_fp8_few<MT, BROW>), dim3(grid), dim3(waves * kWave), waves * MT * 256 * 4, stream, p);
+template <bool BROW, bool WIDE>
+void launch_tile(const F8Params& p, int tile, unsigned groups, hipStream_t stream) {
+    if (tile == 256)
+        FP4Q_LAUNCH((k_gemm_fp8<BROW, WIDE>), dim3(groups), dim3(kThreads), 0, stream, p);
+    else if (tile == 128)
+        FP4Q_LAUNCH((k_gemm_fp8_mid<128, BROW, WIDE>), dim3(groups), dim3(256), MidPlan<128>::kLds, stream, p);
+    else
+        FP4Q_LAUNCH((k_gemm_fp8_mid<64, BROW, WIDE>), dim3(groups), dim3(256), MidPlan<64>::kLds, stream, p);
 }
 
 }  // namespace
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M <= kFewMaxM) return 0;
-    const int sp = splits_for(M, N, K);
+    const int sp = std::max(choose(M, N, K, false).splits, choose(M, N, K, true).splits);  // whatever the output's type
     return sp > 1 ? (size_t)(4 * sp * M * N) : 0;
 }
 
@@ -502,32 +665,24 @@ int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len) {
         // Enough waves to keep memory busy whatever N: 16 per workgroup while
         // there are fewer workgroups than CUs.
         const int64_t groups = (j.N + kFewRows - 1) / kFewRows;
-        int waves = groups <= 256 ? 16 : groups <= 1024 ? 8 : 4;
+        int waves = groups <= 256 ? kFewMaxWaves : groups <= 1024 ? 8 : 4;
         while (waves > 1 && waves >= 2 * S) waves /= 2;
-        const int mt = j.M <= 16 ? 1 : j.M <= 32 ? 2 : 4;
-        if (j.b_row) {
-            if (mt == 1) launch_few<1, true>(p, waves, stream);
-            else if (mt == 2) launch_few<2, true>(p, waves, stream);
-            else launch_few<4, true>(p, waves, stream);
-        } else {
-            if (mt == 1) launch_few<1, false>(p, waves, stream);
-            else if (mt == 2) launch_few<2, false>(p, waves, stream);
-            else launch_few<4, false>(p, waves, stream);
-        }
+        if (j.b_row) FP4Q_LAUNCH(k_gemm_fp8_few<true>, dim3((unsigned)groups), dim3(waves * kWave), 0, stream, p);
+        else FP4Q_LAUNCH(k_gemm_fp8_few<false>, dim3((unsigned)groups), dim3(waves * kWave), 0, stream, p);
     } else {
-        const int64_t tiles = ((j.M + BM - 1) / BM) * ((j.N + BN - 1) / BN);
-        p.splits = splits_for(j.M, j.N, j.K);
-        if (tiles * p.splits > INT32_MAX) {
+        const bool wide = j.ct == 1;
+        const Choice ch = choose(j.M, j.N, j.K, wide);
+        p.splits = ch.splits;
+        const int64_t groups = ((j.M + ch.tile - 1) / ch.tile) * ((j.N + ch.tile - 1) / ch.tile) * ch.splits;
+        if (groups > INT32_MAX) {
             snprintf(msg, msg_len, "fp8 gemm: %lld x %lld x %lld needs more workgroups than one launch holds",
                      (long long)j.M, (long long)j.N, (long long)j.K);
             return (int)hipErrorInvalidConfiguration;
         }
-        const dim3 grid((unsigned)(tiles * p.splits));
-        const bool wide = j.ct == 1;
-        if (j.b_row && wide) FP4Q_LAUNCH((k_gemm_fp8<true, true>), grid, dim3(kThreads), 0, stream, p);
-        else if (j.b_row) FP4Q_LAUNCH((k_gemm_fp8<true, false>), grid, dim3(kThreads), 0, stream, p);
-        else if (wide) FP4Q_LAUNCH((k_gemm_fp8<false, true>), grid, dim3(kThreads), 0, stream, p);
-        else FP4Q_LAUNCH((k_gemm_fp8<false, false>), grid, dim3(kThreads), 0, stream, p);
+        if (j.b_row && wide) launch_tile<true, true>(p, ch.tile, (unsigned)groups, stream);
+        else if (j.b_row) launch_tile<true, false>(p, ch.tile, (unsigned)groups, stream);
+        else if (wide) launch_tile<false, true>(p, ch.tile, (unsigned)groups, stream);
+        else launch_tile<false, false>(p, ch.tile, (unsigned)groups, stream);
         if (p.splits > 1) launch_splitk_reduce(p.partial, p.splits, j.M * j.N, j.c, j.ct, j.stream);
     }
     const hipError_t e = hipGetLastError();
