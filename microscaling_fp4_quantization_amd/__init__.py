@@ -122,8 +122,17 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(dev) -> int:
+    """torch's current stream on `dev` as a hipStream_t (2 us less than through a
+    torch.cuda.Stream object, a fifth of a small call)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if get is None or dev.index is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return get(dev.index)
+
+
 def _stream(dev) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(dev))
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -156,7 +165,7 @@ def workspace(device) -> torch.Tensor:
     Calls made on one stream share it (stream order keeps them apart); calls
     made on another stream get a workspace of their own."""
     dev = torch.device(device)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    key = (dev.index, _raw_stream(dev))
     ws = _workspaces.get(key)
     if ws is None:
         ws = torch.zeros(workspace_bytes(), dtype=torch.uint8, device=device)
@@ -358,7 +367,7 @@ def gemm_workspace(device, nbytes: int) -> torch.Tensor:
     and current stream and grown on demand (calls on one stream are ordered, so
     they can share it)."""
     dev = torch.device(device)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    key = (dev.index, _raw_stream(dev))
     ws = _gemm_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
@@ -433,6 +442,17 @@ def _b128_scales(rows: int, cols: int, kind: int):
     return (_cdiv(cols, 128), rows) if kind == B128_ROW else (_cdiv(rows, 128), _cdiv(cols, 128))
 
 
+def _b128_outputs(x, rows: int, cols: int, kind: int, codes, scales, what: str, given: bool):
+    """Codes and scales of a rows x cols operand: new ones, or the given ones checked."""
+    shapes = (rows, _cdiv(cols, 16) * 16), _b128_scales(rows, cols, kind)
+    if not given:
+        return (x.new_empty(shapes[0], dtype=torch.float8_e4m3fn), x.new_empty(shapes[1], dtype=torch.float32))
+    for t, shape, dt, name in ((codes, shapes[0], torch.float8_e4m3fn, "codes"), (scales, shapes[1], torch.float32, "scales")):
+        if t is None or t.shape != shape or t.dtype != dt or t.device != x.device or not t.is_contiguous():
+            raise ValueError(f"out.{name}{what} must be a contiguous {dt} tensor of shape {shape} on {x.device}")
+    return codes, scales
+
+
 def fp8_quantize_b128(x: torch.Tensor, kind: int = B128_ROW, *, codes=True, transposed=False,
                       out: Optional[Fp8Quantized] = None) -> Fp8Quantized:
     """E4M3 codes with one float32 scale per 128 elements of a row (B128_ROW) or
@@ -440,31 +460,25 @@ def fp8_quantize_b128(x: torch.Tensor, kind: int = B128_ROW, *, codes=True, tran
     the same pass (``codes=False``: the transpose alone).  ``out``: preallocated
     outputs, laid out as the call returns them; what it lacks is not computed."""
     x = _matrix(x)
-    if kind not in (B128_ROW, B128_TILE):
+    if kind != B128_ROW and kind != B128_TILE:
         raise ValueError(f"kind {kind} is not B128_ROW or B128_TILE")
     rows, cols = x.shape
-    want = {}
-    if codes if out is None else out.codes is not None:
-        want["codes"] = (rows, _cdiv(cols, 16) * 16)
-        want["scales"] = _b128_scales(rows, cols, kind)
-    if transposed if out is None else out.codes_t is not None:
-        want["codes_t"] = (cols, _cdiv(rows, 16) * 16)
-        want["scales_t"] = _b128_scales(cols, rows, kind)
-    if not want:
+    given = out is not None
+    q = Fp8Quantized(None, None, None, None, kind)
+    if out.codes is not None if given else codes:
+        q.codes, q.scales = _b128_outputs(x, rows, cols, kind, given and out.codes, given and out.scales, "", given)
+    if out.codes_t is not None if given else transposed:
+        q.codes_t, q.scales_t = _b128_outputs(x, cols, rows, kind, given and out.codes_t, given and out.scales_t,
+                                              "_t", given)
+    if q.codes is None and q.codes_t is None:
         raise ValueError("nothing is wanted: neither codes nor transposed")
-    got = {}
-    for name, shape in want.items():
-        dt = torch.float8_e4m3fn if name.startswith("codes") else torch.float32
-        t = None if out is None else getattr(out, name)
-        if out is None:
-            t = torch.empty(shape, dtype=dt, device=x.device)
-        elif t is None or t.shape != shape or t.dtype != dt or t.device != x.device or not t.is_contiguous():
-            raise ValueError(f"out.{name} must be a contiguous {dt} tensor of shape {shape} on {x.device}")
-        got[name] = t
-    _check(lib().fp8_quantize_b128(_ptr(x), _dtype_code(x), rows, cols, kind, _ptr(got.get("codes")),
-                                   _ptr(got.get("scales")), _ptr(got.get("codes_t")),
-                                   _ptr(got.get("scales_t")), _stream(x.device)))
-    return Fp8Quantized(got.get("codes"), got.get("scales"), got.get("codes_t"), got.get("scales_t"), kind)
+    rc = lib().fp8_quantize_b128(x.data_ptr(), _dtype_code(x), rows, cols, kind,
+                                 *((None, None) if q.codes is None else (q.codes.data_ptr(), q.scales.data_ptr())),
+                                 *((None, None) if q.codes_t is None else (q.codes_t.data_ptr(), q.scales_t.data_ptr())),
+                                 _raw_stream(x.device))
+    if rc:
+        _check(rc)
+    return q
 
 
 def _b128_operand(codes: torch.Tensor, scales: torch.Tensor, kind: int, what: str):
@@ -472,9 +486,11 @@ def _b128_operand(codes: torch.Tensor, scales: torch.Tensor, kind: int, what: st
     _matrix(scales, what + "_scales")
     if codes.dtype != torch.float8_e4m3fn or scales.dtype != torch.float32:
         raise TypeError(f"{what}: expected float8_e4m3fn codes and float32 scales")
-    want = _b128_scales(codes.shape[0], codes.shape[1], kind)
-    if tuple(scales.shape) != want:
+    rows, cols = codes.shape
+    want = _b128_scales(rows, cols, kind)
+    if scales.shape != want:
         raise ValueError(f"{what}_scales has shape {tuple(scales.shape)}; codes {tuple(codes.shape)} need {want}")
+    return rows, cols
 
 
 def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor,
@@ -483,26 +499,28 @@ def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
                   ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """C = A_hat @ B_hat.T for operands as fp8_quantize_b128 writes them: A with row
     scales, B with the scales that ``b_kind`` names."""
-    if b_kind not in (B128_ROW, B128_TILE):
+    if b_kind != B128_ROW and b_kind != B128_TILE:
         raise ValueError(f"b_kind {b_kind} is not B128_ROW or B128_TILE")
-    _b128_operand(a_codes, a_scales, B128_ROW, "a")
-    _b128_operand(b_codes, b_scales, b_kind, "b")
-    m, k = a_codes.shape
-    n = b_codes.shape[0]
-    if b_codes.shape[1] != k:
-        raise ValueError(f"a_codes has rows of {k}, b_codes of {b_codes.shape[1]}")
+    m, k = _b128_operand(a_codes, a_scales, B128_ROW, "a")
+    n, kb = _b128_operand(b_codes, b_scales, b_kind, "b")
+    if kb != k:
+        raise ValueError(f"a_codes has rows of {k}, b_codes of {kb}")
+    dev = a_codes.device
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=a_codes.device)
-    elif tuple(out.shape) != (m, n) or not out.is_contiguous():
+        out = a_codes.new_empty((m, n), dtype=out_dtype)
+    elif out.shape != (m, n) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous, {m} x {n}")
-    if any(t.device != a_codes.device for t in (a_scales, b_codes, b_scales, out)):
+    if a_scales.device != dev or b_codes.device != dev or b_scales.device != dev or out.device != dev:
         raise ValueError("operands and out must be on one device")
-    need = int(lib().fp8_gemm_b128_workspace_bytes(m, n, k))
+    need = lib().fp8_gemm_b128_workspace_bytes(m, n, k)
     if ws is None and need:
-        ws = gemm_workspace(a_codes.device, need)
-    _check(lib().fp8_gemm_b128(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), b_kind, m, n, k,
-                               _ptr(out), _dtype_code(out), _ptr(ws), 0 if ws is None else ws.numel(),
-                               _stream(a_codes.device)))
+        ws = gemm_workspace(dev, need)
+    rc = lib().fp8_gemm_b128(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
+                             b_kind, m, n, k, out.data_ptr(), _dtype_code(out),
+                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                             _raw_stream(dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -558,7 +576,7 @@ def moe_workspace(device, nbytes: int) -> torch.Tensor:
     """A workspace of at least `nbytes` for moe_layer, zero where it has to be, kept
     per device and current stream and grown on demand."""
     dev = torch.device(device)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    key = (dev.index, _raw_stream(dev))
     ws = _moe_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)

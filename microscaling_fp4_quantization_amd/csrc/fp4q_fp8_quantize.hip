@@ -74,6 +74,19 @@ __device__ __forceinline__ float row16_max(float v) {
     return v;
 }
 
+// Lanes 0 .. 7 of each DPP row, to all of it.
+__device__ __forceinline__ void from_lanes(float (&out)[8], float v) {
+    const int b = __float_as_int(v);
+    out[0] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x150, 0xF, 0xF, true));  // row_newbcast:0
+    out[1] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x151, 0xF, 0xF, true));
+    out[2] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x152, 0xF, 0xF, true));
+    out[3] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x153, 0xF, 0xF, true));
+    out[4] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x154, 0xF, 0xF, true));
+    out[5] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x155, 0xF, 0xF, true));
+    out[6] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x156, 0xF, 0xF, true));
+    out[7] = __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x157, 0xF, 0xF, true));
+}
+
 __device__ __forceinline__ float scale_of(float amax) { return fmaxf(amax / 448.0f, kMinScale); }
 
 __device__ __forceinline__ bool fast_scale(float s) { return s >= kFastLo && s <= kFastHi; }
@@ -115,26 +128,37 @@ __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Fp8Params p) {
     const int n_rows = (int)min((int64_t)kSide, max((int64_t)0, p.rows - row0));
     const int n_cols = (int)min((int64_t)kSide, max((int64_t)0, p.cols - col0));
 
-    // Rows need not start on any boundary past their element's: the 8 elements
-    // are one unaligned wide load (two for binary32), or single loads where the
-    // row ends within them.  What does not exist is +0.
+    // Rows need not start on any boundary past their element's: 8 elements are one
+    // unaligned wide load (two for binary32), or single loads where the row ends
+    // within them.  What does not exist is +0: its loads are of the nearest element
+    // that does (no branch, so that all are in flight together), and dropped.
     struct __attribute__((packed, aligned(sizeof(Bits)))) Eight { Bits e[8]; };
     float v[8][8];
-    const Bits* src = static_cast<const Bits*>(p.x) + row0 * p.cols + col0;
-    if (n_rows == kSide && n_cols == kSide) {
+    if (n_cols == kSide && n_rows > 0) {
         Eight w[8];
 #pragma unroll
-        for (int a = 0; a < 8; ++a) w[a] = *reinterpret_cast<const Eight*>(src + a * p.cols);
+        for (int a = 0; a < 8; ++a)
+            w[a] = *reinterpret_cast<const Eight*>(static_cast<const Bits*>(p.x) + (row0 + min(a, n_rows - 1)) * p.cols + col0);
 #pragma unroll
         for (int a = 0; a < 8; ++a)
 #pragma unroll
-            for (int b = 0; b < 8; ++b) v[a][b] = Elem<XT>::f32(w[a].e[b]);
+            for (int b = 0; b < 8; ++b) v[a][b] = a < n_rows ? Elem<XT>::f32(w[a].e[b]) : 0.0f;
+    } else if (n_cols > 0 && n_rows > 0) {
+#pragma unroll
+        for (int a = 0; a < 8; ++a) {
+            const Bits* src = static_cast<const Bits*>(p.x) + (row0 + min(a, n_rows - 1)) * p.cols + col0;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) v[a][b] = Elem<XT>::f32(src[min(b, n_cols - 1)]);
+        }
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+#pragma unroll
+            for (int b = 0; b < 8; ++b) v[a][b] = a < n_rows && b < n_cols ? v[a][b] : 0.0f;
     } else {
 #pragma unroll
         for (int a = 0; a < 8; ++a)
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-                v[a][b] = a < n_rows && b < n_cols ? Elem<XT>::f32(src[a * p.cols + b]) : 0.0f;
+            for (int b = 0; b < 8; ++b) v[a][b] = 0.0f;
     }
 
     float rm[8], cm[8];
@@ -184,14 +208,13 @@ __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Fp8Params p) {
             if (TOUT) p.scales_t[tile_c * ((p.rows + kTile - 1) / kTile) + tile_r] = sc;
         }
     } else if (OUT) {
+        // Lane j of a row group forms the scale of its row j (mod 8), and hands it out.
+        float m = rm[0];
 #pragma unroll
-        for (int a = 0; a < 8; ++a) {
-            s[a] = scale_of(rm[a]);
-            r[a] = 1.0f / s[a];
-        }
-        float mine = s[0];
-#pragma unroll
-        for (int a = 1; a < 8; ++a) mine = j == a ? s[a] : mine;
+        for (int a = 1; a < 8; ++a) m = j % 8 == a ? rm[a] : m;
+        const float mine = scale_of(m), inv = 1.0f / mine;
+        from_lanes(s, mine);
+        from_lanes(r, inv);
         if (j < n_rows) p.scales[tile_c * p.rows + row0 + j] = mine;
     }
 

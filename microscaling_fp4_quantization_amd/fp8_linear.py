@@ -22,24 +22,27 @@ class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
         need_dx, need_dw = ctx.needs_input_grad
-        xq = fp8_quantize_b128(x, B128_ROW, transposed=need_dw)
-        wq = fp8_quantize_b128(w, B128_TILE, transposed=need_dx)
-        ctx.save_for_backward(wq.codes_t, wq.scales_t, xq.codes_t, xq.scales_t)
-        ctx.dtypes = x.dtype, w.dtype
-        return fp8_gemm_b128(xq.codes, xq.scales, wq.codes, wq.scales, B128_TILE, out_dtype=x.dtype)
+        flat = x.reshape(-1, x.shape[-1]).contiguous()
+        xq = fp8_quantize_b128(flat, B128_ROW, transposed=need_dw)
+        wq = fp8_quantize_b128(w.contiguous(), B128_TILE, transposed=need_dx)
+        if need_dx or need_dw:
+            ctx.save_for_backward(wq.codes_t, wq.scales_t, xq.codes_t, xq.scales_t)
+            ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, w.dtype
+        y = fp8_gemm_b128(xq.codes, xq.scales, wq.codes, wq.scales, B128_TILE, out_dtype=x.dtype)
+        return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         need_dx, need_dw = ctx.needs_input_grad
         wt, swt, xt, sxt = ctx.saved_tensors
-        x_dtype, w_dtype = ctx.dtypes
-        q = fp8_quantize_b128(dy.contiguous(), B128_ROW, codes=need_dx, transposed=need_dw)
+        dy = dy.reshape(-1, dy.shape[-1]).contiguous()
+        q = fp8_quantize_b128(dy, B128_ROW, codes=need_dx, transposed=need_dw)
         dx = dw = None
         if need_dx:
-            dx = fp8_gemm_b128(q.codes, q.scales, wt, swt, B128_TILE, out_dtype=x_dtype)
+            dx = fp8_gemm_b128(q.codes, q.scales, wt, swt, B128_TILE, out_dtype=ctx.x_dtype).view(ctx.x_shape)
         if need_dw:
-            dw = fp8_gemm_b128(q.codes_t, q.scales_t, xt, sxt, B128_ROW, out_dtype=w_dtype)
+            dw = fp8_gemm_b128(q.codes_t, q.scales_t, xt, sxt, B128_ROW, out_dtype=ctx.w_dtype)
         return dx, dw
 
 
@@ -51,5 +54,4 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
         raise ValueError(f"x has shape {tuple(x.shape)}, w {tuple(w.shape)}: the last sizes must agree")
     if x.device != w.device:
         raise ValueError("x and w must be on one device")
-    y = _Fp8Linear.apply(x.reshape(-1, x.shape[-1]).contiguous(), w.contiguous())
-    return y.reshape(*x.shape[:-1], w.shape[0])
+    return _Fp8Linear.apply(x, w)
