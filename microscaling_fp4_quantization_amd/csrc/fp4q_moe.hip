@@ -7,8 +7,9 @@
 //
 // Three launches:
 //  k_moe_route  router logits by 16 experts x 16 tokens x a range of K, on the bf16
-//               matrix cores; the last workgroup of a token tile to finish adds the
-//               ranges and picks its tokens' experts;
+//               matrix cores; the last workgroup to finish adds the ranges, picks the
+//               tokens' experts and lists each expert's tokens (k_moe_plan: the list
+//               alone, for a given routing);
 //  k_moe_up     one workgroup per (expert in use, 16 rows of h): gate and up products
 //               of the expert's tokens, K split over its waves, and silu(g) u;
 //  k_moe_down   one workgroup per 16 rows of y: its waves share out the (expert, K
@@ -65,7 +66,8 @@ struct MoeParams {
     float* wts;        // T x k
     void* y;
     int yt;            // 0 bf16, 1 f32
-    uint32_t* count;   // one per token tile, zero between calls
+    uint32_t* count;   // workgroups of the router that are done, zero between calls
+    struct Plan* plan;
     float* logits;     // ranges x T x E partial sums
     int ranges;        // K ranges of the router product
     uint16_t* h;       // parts x (T k) x I
@@ -245,25 +247,122 @@ __device__ __forceinline__ v4f mma_step(const Frag& w, const Frag (&x)[P], uint3
 }
 
 // ---------------------------------------------------------------------------
+// Which experts are in use, by whom.  Experts in use are numbered in order
+// ("slots"); the tokens of a slot, in order, are the pairs off .. off + n - 1.  An id
+// outside 0 .. E - 1 names none; a token that names an expert twice is one pair under
+// the sum of its weights.
+struct Slot {
+    uint64_t mask;   // its tokens
+    int e, off;
+};
+struct Plan {
+    Slot slot[kMaxExperts];
+    float wt[kMaxPairs];
+    uint8_t tok[kMaxPairs];
+    int slots;
+};
+struct PlanScratch {
+    uint64_t mask[kMaxExperts];  // by expert
+    uint16_t off[kMaxExperts];
+};
+
+// Made by one workgroup from the ids and weights in `ids`, `wts` (T x k; LDS or
+// memory).  GIVEN: a caller's routing, where a token may name an expert twice.
+template <bool GIVEN>
+__device__ __forceinline__ void make_plan(Plan& out, PlanScratch& s, const int* ids, const float* wts, int T, int k, int E) {
+    const int lane = threadIdx.x % kWave, n = T * k;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) s.mask[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int e = ids[i];
+        if (e >= 0 && e < E) atomicOr((unsigned long long*)&s.mask[e], 1ull << (i / k));
+    }
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        int slots = 0, pairs = 0;
+        for (int e0 = 0; e0 < E; e0 += kWave) {
+            const int e = e0 + lane;
+            const uint64_t mask = e < E ? s.mask[e] : 0;
+            const int c = __popcll(mask);
+            const uint64_t below = (1ull << lane) - 1;
+            int before = 0, all = 0;  // pairs of the lanes below, and of all, bit by bit (c is at most 64)
+#pragma unroll
+            for (int bit = 0; bit < 7; ++bit) {
+                const uint64_t with = __builtin_amdgcn_ballot_w64((c >> bit) & 1);
+                before += __popcll(with & below) << bit;
+                all += __popcll(with) << bit;
+            }
+            const uint64_t used = __builtin_amdgcn_ballot_w64(c > 0);
+            if (c > 0) {
+                const int off = pairs + before;
+                s.off[e] = (uint16_t)off;
+                out.slot[slots + __popcll(used & below)] = Slot{mask, e, off};
+            }
+            slots += __popcll(used);
+            pairs += all;
+        }
+        if (lane == 0) out.slots = slots;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int e = ids[i], t = i / k, j = i - t * k;
+        if (e < 0 || e >= E) continue;
+        float w = wts[i];
+        if (GIVEN) {
+            bool first = true;
+            w = 0.0f;
+            for (int o = 0; o < k; ++o)
+                if (ids[t * k + o] == e) {
+                    if (o < j) first = false;
+                    w += wts[t * k + o];
+                }
+            if (!first) continue;
+        }
+        const int at = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1));
+        out.tok[at] = (uint8_t)t;
+        out.wt[at] = w;
+    }
+}
+
+// Given routing.
+__global__ __launch_bounds__(1024) void k_moe_plan(MoeParams p) {
+    __shared__ PlanScratch s;
+    make_plan<true>(*p.plan, s, p.ids, p.wts, p.T, p.k, p.E);
+}
+
+// The i-th token of a mask (i below its count).
+__device__ __forceinline__ int token_of(uint64_t mask, int i) {
+    int at = 0;
+#pragma unroll
+    for (int w = 32; w >= 1; w /= 2) {
+        const int c = __popcll(mask & ((1ull << w) - 1));
+        if (i >= c) i -= c, mask >>= w, at += w;
+    }
+    return at;
+}
+
+// ---------------------------------------------------------------------------
 // The router.
 
 constexpr int kRouteWaves = 16;
+constexpr int kMaxRanges = 8;
 
-// A reduction over the wave: each row of 16 lanes by rotations, then the four rows.
+// A reduction over each row of 16 lanes, by rotations: the same value in all of them.
 template <typename F>
-__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, true));  // row_ror:1, 2, 4, 8
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, true));
     v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, true));
-    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));
-    return f(f((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
-             f((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
+    return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    return wave_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    return row_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+    return row_reduce(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+__device__ __forceinline__ float row_sum(float v) {
+    return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
@@ -282,60 +381,61 @@ __device__ __forceinline__ void load8(Rsrc r, int at, bf16x8_t (&out)[P]) {
     }
 }
 
-// Picks token t's experts: its logits are in the wave's lanes, expert 64 i + lane
-// in v[i].  Each round takes the largest left, the lowest index among equals.
-__device__ void pick(const MoeParams& p, int t, int lane, float (&v)[kMaxExperts / 64]) {
-    constexpr int R = kMaxExperts / 64;
-    uint32_t key[R];
-    float top = 0.0f, total = 0.0f;
+// Picks the experts of four tokens at once, one per row of 16 lanes: lane r of the row
+// holds the logits of experts r, 16 + r, ... in v.  Each round takes the largest left,
+// the lowest index among equals; lane j keeps the j-th.  (A whole wave per token took
+// 6.8 us of 64 tokens' routing where this takes about 1.5: the rounds are chains of
+// short steps, the same for one token as for four.)
+template <int R>
+__device__ __forceinline__ void pick(const MoeParams& p, int t, int r, const float (&v)[R], int* ids, float* wts) {
+    uint32_t key[R];  // ordered as the logits are
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const uint32_t b = __float_as_uint(v[i] + 0.0f);  // -0 and 0 are equal
         const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-        key[i] = 64 * i + lane < p.E ? max(o, 1u) : 0u;  // 0: not there, or taken
+        key[i] = 16 * i + r < p.E ? max(o, 1u) : 0u;  // 0: not there, or taken
     }
-    float mine = 0.0f;
+    uint32_t top = 0, mine = 0;
     int chosen = 0;
     for (int j = 0; j < p.k; ++j) {
-        uint32_t m = 0;
+        uint32_t m = key[0];
 #pragma unroll
-        for (int i = 0; i < R; ++i) m = max(m, key[i]);
-        m = wave_max(m);
-        int e = -1;
-        float l = 0.0f;
+        for (int i = 1; i < R; ++i) m = max(m, key[i]);
+        m = row_max(m);
+        uint32_t e = 0xFFFFFFFFu;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const uint64_t hit = __builtin_amdgcn_ballot_w64(key[i] == m);
-            if (e < 0 && hit) {
-                const int who = __builtin_ctzll(hit);
-                e = 64 * i + who;
-                l = __uint_as_float((uint32_t)__builtin_amdgcn_readlane(__float_as_int(v[i]), who));
-                if (lane == who) key[i] = 0u;
-            }
-        }
-        if (j == 0) top = l;
-        const float w = expf(l - top);
-        total += w;
-        if (lane == j) mine = w, chosen = e;
+        for (int i = R - 1; i >= 0; --i) e = key[i] == m ? 16 * i + r : e;
+        e = row_min(e);
+#pragma unroll
+        for (int i = 0; i < R; ++i) key[i] = e == (uint32_t)(16 * i + r) ? 0u : key[i];
+        if (j == 0) top = m;
+        if (r == j) mine = m, chosen = (int)e;
     }
+    auto logit = [](uint32_t o) { return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o); };
+    const float l0 = logit(top);
+    const float w = r < p.k ? expf(logit(mine) - l0) : 0.0f;
+    float total = w;
     if (!p.renorm) {
         total = 0.0f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) total += 64 * i + lane < p.E ? expf(v[i] - top) : 0.0f;
-        total = wave_sum(total);
+        for (int i = 0; i < R; ++i) total += 16 * i + r < p.E ? expf(v[i] - l0) : 0.0f;
     }
-    if (lane < p.k) {
-        p.ids[t * p.k + lane] = chosen;
-        p.wts[t * p.k + lane] = mine / total;
+    total = row_sum(total);
+    if (r < p.k && t < p.T) {
+        p.ids[t * p.k + r] = ids[t * p.k + r] = chosen;
+        p.wts[t * p.k + r] = wts[t * p.k + r] = w / total;
     }
 }
 
 // PX, PR: bf16 parts of x and of the router's weights (products of parts beyond the
 // third order, below 2^-24 of the whole, are left out).
-template <int PX, int PR>
+template <int PX, int PR, int R>
 __global__ __launch_bounds__(kRouteWaves * kWave) void k_moe_route(MoeParams p) {
     __shared__ float red[kRouteWaves][256];
     __shared__ int last;
+    __shared__ PlanScratch scratch;
+    __shared__ int ids[kMaxPairs];
+    __shared__ float wts[kMaxPairs];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane % 16, q = lane / 16;
@@ -375,91 +475,51 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_moe_route(MoeParams p) 
 #pragma unroll
         for (int w = 0; w < kRouteWaves; ++w) sum += red[w][threadIdx.x];
         if (t < rows_x && e < rows_r) p.logits[((int64_t)range * p.T + t0 + t) * p.E + e0 + e] = sum;
-        __threadfence();
     }
     __syncthreads();
-    // The last workgroup of the token tile sees everyone's sums (none waits).
+    // The last workgroup to get here sees everyone's sums (none waits): the barrier
+    // orders the workgroup's sums before thread 0, which releases and acquires for it.
     if (threadIdx.x == 0) {
-        const uint32_t n = __hip_atomic_fetch_add(&p.count[tile], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        last = n + 1 == (uint32_t)(etiles * p.ranges);
-        if (last) __hip_atomic_store(&p.count[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t n = __hip_atomic_fetch_add(p.count, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        last = n + 1 == gridDim.x;
+        if (last) __hip_atomic_store(p.count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (!last) return;
-    __threadfence();
-    const int t = t0 + wave;  // 16 waves, 16 tokens
-    if (t >= p.T) return;
-    float v[kMaxExperts / 64];
+    // Four tokens per wave: 16 waves take all there can be.
+    static_assert(4 * kRouteWaves >= kMaxTokens, "a row of lanes per token");
+    if (4 * wave < p.T) {
+        const int t = 4 * wave + q;
+        const float* src = p.logits + (int64_t)min(t, p.T - 1) * p.E;
+        float v[R];
+        // A range's sums of all experts are loaded together; where registers allow,
+        // all ranges' (one trip to memory).
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 64; ++i) {
-        v[i] = 0.0f;
-        if (64 * i + lane < p.E)
-            for (int g = 0; g < p.ranges; ++g) v[i] += p.logits[((int64_t)g * p.T + t) * p.E + 64 * i + lane];
-    }
-    pick(p, t, lane, v);
-}
-
-// ---------------------------------------------------------------------------
-// Which experts are in use, by whom: every workgroup works it out from the ids, in
-// LDS.  Experts in use are numbered in order ("slots"); the tokens of a slot, in
-// order, are the pairs off .. off + n - 1.  An id outside 0 .. E - 1 names none; a
-// token that names an expert twice is one pair under the sum of its weights.
-struct Plan {
-    uint64_t mask[kMaxExperts];   // tokens of each expert
-    uint16_t off[kMaxExperts];    // by expert: first pair
-    uint16_t slot_e[kMaxExperts];
-    uint8_t tok[kMaxPairs];
-    float wt[kMaxPairs];
-    int slots;
-};
-
-__device__ __forceinline__ void make_plan(Plan& s, const MoeParams& p) {
-    const int lane = threadIdx.x % kWave, n = p.T * p.k;
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) s.mask[e] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = p.ids[i];
-        if (e >= 0 && e < p.E) atomicOr((unsigned long long*)&s.mask[e], 1ull << (i / p.k));
-    }
-    __syncthreads();
-    if (threadIdx.x < kWave) {
-        int slots = 0, pairs = 0;
-        for (int e0 = 0; e0 < p.E; e0 += kWave) {
-            const int e = e0 + lane;
-            const int c = e < p.E ? __popcll(s.mask[e]) : 0;
-            int before = c;  // inclusive sum over the lanes
+        for (int i = 0; i < R; ++i) v[i] = src[min(16 * i + r, p.E - 1)];
+        if (R <= 8) {
+            float part[kMaxRanges - 1][R <= 8 ? R : 1];
 #pragma unroll
-            for (int d = 1; d < kWave; d *= 2) {
-                const int o = __shfl_up(before, d);
-                if (lane >= d) before += o;
+            for (int g = 1; g < kMaxRanges; ++g)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    part[g - 1][R <= 8 ? i : 0] = src[(int64_t)min(g, p.ranges - 1) * p.T * p.E + min(16 * i + r, p.E - 1)];
+#pragma unroll
+            for (int g = 1; g < kMaxRanges; ++g)
+#pragma unroll
+                for (int i = 0; i < R; ++i) v[i] += g < p.ranges ? part[g - 1][R <= 8 ? i : 0] : 0.0f;
+        } else {
+            for (int g = 1; g < p.ranges; ++g) {
+                float part[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) part[i] = src[(int64_t)g * p.T * p.E + min(16 * i + r, p.E - 1)];
+#pragma unroll
+                for (int i = 0; i < R; ++i) v[i] += part[i];
             }
-            const uint64_t used = __builtin_amdgcn_ballot_w64(c > 0);
-            if (c > 0) {
-                s.off[e] = (uint16_t)(pairs + before - c);
-                s.slot_e[slots + __popcll(used & ((1ull << lane) - 1))] = (uint16_t)e;
-            }
-            slots += __popcll(used);
-            pairs += __shfl(before, kWave - 1);
         }
-        if (lane == 0) s.slots = slots;
+        pick<R>(p, t, r, v, ids, wts);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = p.ids[i], t = i / p.k, j = i % p.k;
-        if (e < 0 || e >= p.E) continue;
-        float w = 0.0f;
-        bool first = true;
-        for (int o = 0; o < p.k; ++o)
-            if (p.ids[t * p.k + o] == e) {
-                if (o < j) first = false;
-                w += p.wts[t * p.k + o];
-            }
-        if (!first) continue;
-        const int at = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1));
-        s.tok[at] = (uint8_t)t;
-        s.wt[at] = w;
-    }
-    __syncthreads();
+    make_plan<false>(*p.plan, scratch, ids, wts, p.T, p.k, p.E);
 }
 
 // ---------------------------------------------------------------------------
@@ -471,15 +531,12 @@ constexpr int kUpWaves = 8;
 template <int FMT, int NT, int PX>
 __global__ __launch_bounds__(kUpWaves * kWave) void k_moe_up(MoeParams p, int parts_h) {
     constexpr int U = FMT == kF8 || PX > 1 ? 2 : 4;  // steps in flight
-    __shared__ Plan plan;
     __shared__ float red[kUpWaves][2][256];
-    make_plan(plan, p);
     const int itiles = p.I / kRows;
     const int slot = (int)(blockIdx.x / itiles), i0 = (int)(blockIdx.x % itiles) * kRows;
-    if (slot >= plan.slots) return;
-    const int e = __builtin_amdgcn_readfirstlane(plan.slot_e[slot]);
-    const int n = __builtin_amdgcn_readfirstlane((int)__popcll(plan.mask[e]));
-    const int off = __builtin_amdgcn_readfirstlane(plan.off[e]);
+    const Slot sl = p.plan->slot[slot];
+    if (slot >= p.plan->slots) return;
+    const int e = sl.e, n = __popcll(sl.mask), off = sl.off;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane % 16, q = lane / 16;
@@ -488,7 +545,7 @@ __global__ __launch_bounds__(kUpWaves * kWave) void k_moe_up(MoeParams p, int pa
     const Rsrc rx = make_rsrc(p.x, (int64_t)p.T * p.D * (PX == 1 ? 2 : 4));
     int src[NT];  // element offset of the lane's token, or none
 #pragma unroll
-    for (int t = 0; t < NT; ++t) src[t] = 16 * t + r < n ? plan.tok[off + 16 * t + r] * p.D : -1;
+    for (int t = 0; t < NT; ++t) src[t] = 16 * t + r < n ? token_of(sl.mask, 16 * t + r) * p.D : -1;
 
     v4f ag[NT], au[NT];
 #pragma unroll
@@ -553,9 +610,11 @@ constexpr int kDownWaves = 16;
 template <int FMT, int NT, int PH>
 __global__ __launch_bounds__(kDownWaves * kWave) void k_moe_down(MoeParams p) {
     constexpr int U = FMT == kF8 ? 2 : 4;
-    __shared__ Plan plan;
+    __shared__ float wt[kMaxPairs];
+    __shared__ uint8_t tok[kMaxPairs];
     extern __shared__ __attribute__((aligned(16))) float ytile[];  // waves x T x 16
-    make_plan(plan, p);
+    for (int i = threadIdx.x; i < p.T * p.k; i += kDownWaves * kWave) wt[i] = p.plan->wt[i], tok[i] = p.plan->tok[i];
+    __syncthreads();
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane % 16, q = lane / 16;
@@ -564,16 +623,15 @@ __global__ __launch_bounds__(kDownWaves * kWave) void k_moe_down(MoeParams p) {
     for (int i = lane; i < p.T * 16; i += kWave) mine[i] = 0.0f;
 
     const int steps = (p.I + kStep - 1) / kStep;
-    const int total = plan.slots * steps;
+    const int total = p.plan->slots * steps;
     int at = total * wave / kDownWaves;
     const int end = total * (wave + 1) / kDownWaves;
     const int64_t plane = (int64_t)p.T * p.k * p.I;
     while (at < end) {
         const int slot = at / steps, c_lo = at % steps, c_hi = min(steps, c_lo + end - at);
         at += c_hi - c_lo;
-        const int e = __builtin_amdgcn_readfirstlane(plan.slot_e[slot]);
-        const int n = __builtin_amdgcn_readfirstlane((int)__popcll(plan.mask[e]));
-        const int off = __builtin_amdgcn_readfirstlane(plan.off[e]);
+        const Slot sl = p.plan->slot[slot];
+        const int e = sl.e, n = __popcll(sl.mask), off = sl.off;
         const Rows<FMT> down(p.w2, (int64_t)e * p.D + d0, p.I);
         Rsrc rh[PH];
 #pragma unroll
@@ -610,8 +668,8 @@ __global__ __launch_bounds__(kDownWaves * kWave) void k_moe_down(MoeParams p) {
         for (int t = 0; t < NT; ++t) {
             // Lane: token 16 t + r of the slot (no token twice), rows 4 q .. 4 q + 3.
             if (16 * t + r >= n) continue;
-            const float w = plan.wt[off + 16 * t + r] * g;
-            v4f* dst = reinterpret_cast<v4f*>(mine + plan.tok[off + 16 * t + r] * 16 + 4 * q);
+            const float w = wt[off + 16 * t + r] * g;
+            v4f* dst = reinterpret_cast<v4f*>(mine + tok[off + 16 * t + r] * 16 + 4 * q);
             v4f v = *dst;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[t][i], w, v[i]);
@@ -652,16 +710,25 @@ void launch_tiles(const MoeParams& p, bool x32, int parts_h, hipStream_t stream)
 // Ranges of K for the router: two steps of 32 per wave keep its loads in flight
 // together, and 8 ranges are as many partial sums as are worth adding.
 int route_ranges(int64_t D) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(8, D / 32 / (2 * kRouteWaves)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRanges, D / 32 / (2 * kRouteWaves)));
 }
 
 constexpr size_t kCountBytes = 256;
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+const size_t kPlanBytes = up256(sizeof(Plan));
+
+template <int PX, int PR>
+void launch_route(const MoeParams& p, hipStream_t stream) {
+    const dim3 grid((unsigned)((p.E + 15) / 16 * p.ranges * ((p.T + 15) / 16))), block(kRouteWaves * kWave);
+    if (p.E <= 64) FP4Q_LAUNCH((k_moe_route<PX, PR, 4>), grid, block, 0, stream, p);
+    else if (p.E <= 128) FP4Q_LAUNCH((k_moe_route<PX, PR, 8>), grid, block, 0, stream, p);
+    else FP4Q_LAUNCH((k_moe_route<PX, PR, kMaxExperts / 16>), grid, block, 0, stream, p);
+}
 
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t I, int64_t E, int64_t k) {
-    return kCountBytes + up256((size_t)(route_ranges(D) * T * E * 4)) + (size_t)(3 * T * k * I * 2);
+    return kCountBytes + kPlanBytes + up256((size_t)(route_ranges(D) * T * E * 4)) + (size_t)(3 * T * k * I * 2);
 }
 
 int launch_moe(const MoeJob& j, char* msg, size_t msg_len) {
@@ -681,14 +748,16 @@ int launch_moe(const MoeJob& j, char* msg, size_t msg_len) {
     p.yt = j.yt;
     p.ranges = route_ranges(j.D);
     p.count = reinterpret_cast<uint32_t*>(ws);
-    p.logits = reinterpret_cast<float*>(ws + kCountBytes);
-    p.h = reinterpret_cast<uint16_t*>(ws + kCountBytes + up256((size_t)(p.ranges * j.T * j.E * 4)));
+    p.plan = reinterpret_cast<Plan*>(ws + kCountBytes);
+    p.logits = reinterpret_cast<float*>(ws + kCountBytes + kPlanBytes);
+    p.h = reinterpret_cast<uint16_t*>(ws + kCountBytes + kPlanBytes + up256((size_t)(p.ranges * j.T * j.E * 4)));
     if (p.router) {
-        const dim3 grid((unsigned)((j.E + 15) / 16 * p.ranges * ((j.T + 15) / 16))), block(kRouteWaves * kWave);
-        if (j.xt == 0 && j.rt == 0) FP4Q_LAUNCH((k_moe_route<1, 1>), grid, block, 0, stream, p);
-        else if (j.xt == 0) FP4Q_LAUNCH((k_moe_route<1, 3>), grid, block, 0, stream, p);
-        else if (j.rt == 0) FP4Q_LAUNCH((k_moe_route<3, 1>), grid, block, 0, stream, p);
-        else FP4Q_LAUNCH((k_moe_route<3, 3>), grid, block, 0, stream, p);
+        if (j.xt == 0 && j.rt == 0) launch_route<1, 1>(p, stream);
+        else if (j.xt == 0) launch_route<1, 3>(p, stream);
+        else if (j.rt == 0) launch_route<3, 1>(p, stream);
+        else launch_route<3, 3>(p, stream);
+    } else {
+        FP4Q_LAUNCH(k_moe_plan, dim3(1), dim3(1024), 0, stream, p);
     }
     const int parts_h = j.yt == 1 ? 3 : 2;
     if (j.fmt == 0) launch_tiles<kMx>(p, j.xt == 1, parts_h, stream);
