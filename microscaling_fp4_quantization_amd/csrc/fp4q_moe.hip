@@ -5,16 +5,15 @@
 //   l = x Wr^T;  the top_k largest of each token, with softmax weights p
 //   h_e = silu(G_e x) * (U_e x);   y = sum_e p_e D_e h_e
 //
-// Three launches:
+// Four launches:
 //  k_moe_route  router logits by 16 experts x 16 tokens x a range of K, on the bf16
 //               matrix cores; the last workgroup to finish adds the ranges, picks the
 //               tokens' experts and lists each expert's tokens (k_moe_plan: the list
 //               alone, for a given routing);
-//  k_moe_up     one workgroup per (expert in use, 16 rows of h): gate and up products
-//               of the expert's tokens, K split over its waves, and silu(g) u;
-//  k_moe_down   one workgroup per 16 rows of y: its waves share out the (expert, K
-//               chunk) pairs in order, each adding into a tile of its own, and the
-//               tiles meet in wave order.
+//  k_moe_up     gate and up products, and silu(g) u; or k_moe_many, which does the same
+//               for more tokens and
+//  k_moe_many   the down products of each (token, expert) pair, by K ranges;
+//  k_moe_combine  their weighted sum.
 // Sums are formed in a fixed order: the same inputs give the same bits.
 //
 // The layer is a pass over the weights of the experts in use.  They go from memory
@@ -58,6 +57,7 @@ struct Weights {
 
 struct MoeParams {
     const void* x;
+    uint16_t* xp;      // x as bf16 parts: x itself, or 3 x T x D made of binary32 x
     int T, D, I, E, k;
     Weights w13, w2;
     const void* router;
@@ -116,36 +116,12 @@ __device__ __forceinline__ void split8(const float (&f)[8], bf16x8_t (&out)[P]) 
     }
 }
 
-// 32 consecutive elements at element offset `at` (kDropped: zeros) of a window of
-// bf16 (P = 1) or binary32 (P = 3) values, as P parts.
-template <int P>
-struct Act;
-template <>
-struct Act<1> {
+// 32 consecutive bf16 values at element offset `at` (negative: zeros) of a window.
+struct Act {
     u32x4_t w[4];
     __device__ __forceinline__ void load(Rsrc r, int at) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = load128(r, at < 0 ? kDropped : at * 2 + 16 * i);
-    }
-    __device__ __forceinline__ void parts(Frag (&f)[1]) const { f[0] = frag_of(w); }
-};
-template <>
-struct Act<3> {
-    u32x4_t w[8];
-    __device__ __forceinline__ void load(Rsrc r, int at) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = load128(r, at < 0 ? kDropped : at * 4 + 16 * i);
-    }
-    __device__ __forceinline__ void parts(Frag (&f)[3]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[2 * i + e / 4][e % 4]);
-            bf16x8_t o[3];
-            split8<3>(v, o);
-            f[0].v[i] = o[0], f[1].v[i] = o[1], f[2].v[i] = o[2];
-        }
     }
 };
 
@@ -187,6 +163,58 @@ struct Rows {
         return o;
     }
 };
+
+// Two steps at once: a lane's row has their 8 (MX) or 16 (NV) scale bytes in one load
+// where rows of scales start on that boundary, instead of four loads of one or two bytes,
+// each of which touches 16 cache lines.
+template <int FMT>
+struct Raw2 {
+    u32x4_t w[2][FMT == kF8 ? 2 : 1];
+    uint32_t s[2][2];
+    __device__ __forceinline__ Raw<FMT> step(int u, int q) const {
+        Raw<FMT> o;
+        o.w[0] = w[u][0];
+        if (FMT == kF8) o.w[FMT == kF8] = w[u][FMT == kF8];
+        if (FMT == kMx) o.s = (s[u][0] >> (8 * q)) & 0xFFu;
+        else if (FMT == kNv) o.s = (q & 2 ? s[u][1] : s[u][0]) >> (16 * (q & 1));
+        else o.s = s[u][0];
+        return o;
+    }
+};
+template <int FMT>
+__device__ __forceinline__ bool whole_scales(const Rows<FMT>& rows, const void* scales) {
+    constexpr int kBytes = FMT == kMx ? 8 : 16;
+    return rows.kb % kBytes == 0 && (uint32_t)(uintptr_t)scales % kBytes == 0;
+}
+// Steps 2 c and 2 c + 1; whole: whole_scales of the matrix.
+template <int FMT>
+__device__ __forceinline__ Raw2<FMT> load2(const Rows<FMT>& rows, int c, int r, int q, bool whole) {
+    Raw2<FMT> o;
+    if (FMT == kF8 || !whole) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const Raw<FMT> x = rows.load(2 * c + u, r, q);
+            o.w[u][0] = x.w[0];
+            if (FMT == kF8) o.w[u][FMT == kF8] = x.w[FMT == kF8];
+            o.s[u][0] = o.s[u][1] = FMT == kF8 ? x.s : x.s << (FMT == kMx ? 8 * q : 16 * (q & 1));
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int k = (2 * c + u) * kStep + 32 * q;
+            o.w[u][0] = load128(rows.codes, k < rows.K ? r * (rows.K / 2) + k / 2 : kDropped);
+        }
+        const bool in = 2 * c * kStep < rows.K;  // K is a multiple of 256 here
+        if (FMT == kMx) {
+            const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(rows.scales, in ? r * rows.kb + 8 * c : kDropped, 0, 0);
+            o.s[0][0] = v[0], o.s[1][0] = v[1], o.s[0][1] = o.s[1][1] = 0;
+        } else {
+            const u32x4_t v = load128(rows.scales, in ? r * rows.kb + 16 * c : kDropped);
+            o.s[0][0] = v[0], o.s[0][1] = v[1], o.s[1][0] = v[2], o.s[1][1] = v[3];
+        }
+    }
+    return o;
+}
 
 __device__ __forceinline__ bf16x8_t join8(bf16x2_t a, bf16x2_t b, bf16x2_t c, bf16x2_t d) {
     return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
@@ -246,25 +274,51 @@ __device__ __forceinline__ v4f mma_step(const Frag& w, const Frag (&x)[P], uint3
     return acc;
 }
 
+// 8 consecutive elements of a row, as bf16 parts.
+template <int P>
+__device__ __forceinline__ void load8(Rsrc r, int at, bf16x8_t (&out)[P]) {
+    if (P == 1) {
+        out[0] = __builtin_bit_cast(bf16x8_t, load128(r, at < 0 ? kDropped : at * 2));
+    } else {
+        const u32x4_t a = load128(r, at < 0 ? kDropped : at * 4), b = load128(r, at < 0 ? kDropped : at * 4 + 16);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(a[e]), f[4 + e] = __uint_as_float(b[e]);
+        split8<P>(f, out);
+    }
+}
+
 // ---------------------------------------------------------------------------
-// Which experts are in use, by whom.  Experts in use are numbered in order
-// ("slots"); the tokens of a slot, in order, are the pairs off .. off + n - 1.  An id
-// outside 0 .. E - 1 names none; a token that names an expert twice is one pair under
-// the sum of its weights.
+// Which experts are in use, by whom: "slots" of an expert and up to 16 of its tokens (a
+// matrix-core fragment), in order of experts and tokens; the tokens of a slot are the
+// pairs off .. off + n - 1.  An id outside 0 .. E - 1 names no expert; a token that names
+// one twice is one pair under the sum of its weights.
+constexpr int kMaxSlots = kMaxExperts + kMaxPairs / 16;
 struct Slot {
     uint64_t mask;   // its tokens
     int e, off;
 };
 struct Plan {
-    Slot slot[kMaxExperts];
-    float wt[kMaxPairs];
-    uint8_t tok[kMaxPairs];
+    Slot slot[kMaxSlots];
+    short pair[kMaxPairs];    // of each token's choices in turn; -1: none
+    float weight[kMaxPairs];  // and their weights
     int slots;
 };
 struct PlanScratch {
     uint64_t mask[kMaxExperts];  // by expert
     uint16_t off[kMaxExperts];
 };
+
+// The i-th token of a mask (i below its count).
+__device__ __forceinline__ int token_of(uint64_t mask, int i) {
+    int at = 0;
+#pragma unroll
+    for (int w = 32; w >= 1; w /= 2) {
+        const int c = __popcll(mask & ((1ull << w) - 1));
+        if (i >= c) i -= c, mask >>= w, at += w;
+    }
+    return at;
+}
 
 // Made by one workgroup from the ids and weights in `ids`, `wts` (T x k; LDS or
 // memory).  GIVEN: a caller's routing, where a token may name an expert twice.
@@ -292,23 +346,37 @@ __device__ __forceinline__ void make_plan(Plan& out, PlanScratch& s, const int* 
                 before += __popcll(with & below) << bit;
                 all += __popcll(with) << bit;
             }
-            const uint64_t used = __builtin_amdgcn_ballot_w64(c > 0);
-            if (c > 0) {
-                const int off = pairs + before;
-                s.off[e] = (uint16_t)off;
-                out.slot[slots + __popcll(used & below)] = Slot{mask, e, off};
+            // Slots of the lanes below, and of all: at most four each.
+            const int ns = (c + 15) / 16;
+            int first = slots;
+#pragma unroll
+            for (int bit = 0; bit < 3; ++bit) {
+                const uint64_t with = __builtin_amdgcn_ballot_w64((ns >> bit) & 1);
+                first += __popcll(with & below) << bit;
+                slots += __popcll(with) << bit;
             }
-            slots += __popcll(used);
+            const int off = pairs + before;
+            if (c > 0) s.off[e] = (uint16_t)off;
+            uint64_t left = mask;
+            for (int i = 0; i < ns; ++i) {
+                const int n = min(16, c - 16 * i);
+                const uint64_t part = n < 16 || c == 16 * (i + 1) ? left : left & ((1ull << token_of(left, 16)) - 1);
+                out.slot[first + i] = Slot{part, e, off + 16 * i};
+                left &= ~part;
+            }
             pairs += all;
         }
         if (lane == 0) out.slots = slots;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = ids[i], t = i / k, j = i - t * k;
+        const int e = ids[i], t = i / k;
+        out.pair[i] = -1;
+        out.weight[i] = 0.0f;
         if (e < 0 || e >= E) continue;
         float w = wts[i];
         if (GIVEN) {
+            const int j = i - t * k;
             bool first = true;
             w = 0.0f;
             for (int o = 0; o < k; ++o)
@@ -319,26 +387,27 @@ __device__ __forceinline__ void make_plan(Plan& out, PlanScratch& s, const int* 
             if (!first) continue;
         }
         const int at = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1));
-        out.tok[at] = (uint8_t)t;
-        out.wt[at] = w;
+        out.pair[i] = (short)at;
+        out.weight[i] = w;
     }
 }
 
-// Given routing.
+// Given routing: the first workgroup lists the experts' tokens, the others make the
+// parts of binary32 x.
 __global__ __launch_bounds__(1024) void k_moe_plan(MoeParams p) {
     __shared__ PlanScratch s;
-    make_plan<true>(*p.plan, s, p.ids, p.wts, p.T, p.k, p.E);
-}
-
-// The i-th token of a mask (i below its count).
-__device__ __forceinline__ int token_of(uint64_t mask, int i) {
-    int at = 0;
+    if (blockIdx.x > 0) {
+        const Rsrc rx = make_rsrc(p.x, (int64_t)p.T * p.D * 4);
+        const int n = p.T * p.D;  // a multiple of 8; at most 2^26
+        for (int at = ((int)(blockIdx.x - 1) * 1024 + (int)threadIdx.x) * 8; at < n; at += (int)(gridDim.x - 1) * 8192) {
+            bf16x8_t part[3];
+            load8<3>(rx, at, part);
 #pragma unroll
-    for (int w = 32; w >= 1; w /= 2) {
-        const int c = __popcll(mask & ((1ull << w) - 1));
-        if (i >= c) i -= c, mask >>= w, at += w;
+            for (int a = 0; a < 3; ++a) *reinterpret_cast<bf16x8_t*>(p.xp + (int64_t)a * n + at) = part[a];
+        }
+        return;
     }
-    return at;
+    make_plan<true>(*p.plan, s, p.ids, p.wts, p.T, p.k, p.E);
 }
 
 // ---------------------------------------------------------------------------
@@ -365,20 +434,6 @@ __device__ __forceinline__ float row_sum(float v) {
     return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
-}
-
-// 8 consecutive elements of a row, as bf16 parts.
-template <int P>
-__device__ __forceinline__ void load8(Rsrc r, int at, bf16x8_t (&out)[P]) {
-    if (P == 1) {
-        out[0] = __builtin_bit_cast(bf16x8_t, load128(r, at < 0 ? kDropped : at * 2));
-    } else {
-        const u32x4_t a = load128(r, at < 0 ? kDropped : at * 4), b = load128(r, at < 0 ? kDropped : at * 4 + 16);
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(a[e]), f[4 + e] = __uint_as_float(b[e]);
-        split8<P>(f, out);
-    }
 }
 
 // Picks the experts of four tokens at once, one per row of 16 lanes: lane r of the row
@@ -458,6 +513,17 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_moe_route(MoeParams p) 
             load8<PX>(rx, s < steps && r < rows_x ? r * p.D + k : -1, x[u]);
             load8<PR>(rr, s < steps && r < rows_r ? r * p.D + k : -1, w[u]);
         }
+        if (PX == 3 && e0 == 0) {
+            // x's parts, for the products: each step is in one wave of these workgroups.
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + u * p.ranges * kRouteWaves;
+                if (s < steps && r < rows_x)
+#pragma unroll
+                    for (int a = 0; a < PX; ++a)
+                        *reinterpret_cast<bf16x8_t*>(p.xp + ((int64_t)a * p.T + t0 + r) * p.D + s * 32 + 8 * q) = x[u][a];
+            }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -523,14 +589,28 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_moe_route(MoeParams p) 
 }
 
 // ---------------------------------------------------------------------------
-// Gate and up.
+// Gate and up, where there are few (slot, rows) pairs to spread over the chip: a
+// workgroup per 16 rows of h, its waves sharing out K, so that one token's few experts
+// still put hundreds of workgroups to work.  Each wave reads its tokens' values from
+// the caches itself.
 
 constexpr int kUpWaves = 8;
 
-// NT: token tiles of 16.  PH: parts of h.
-template <int FMT, int NT, int PX>
-__global__ __launch_bounds__(kUpWaves * kWave) void k_moe_up(MoeParams p, int parts_h) {
-    constexpr int U = FMT == kF8 || PX > 1 ? 2 : 4;  // steps in flight
+// h of a pair's element from the sums of gate and up, as bf16 parts.
+__device__ __forceinline__ void put_h(const MoeParams& p, float sg, float su, int64_t at, int parts_h) {
+    const int64_t plane = (int64_t)p.T * p.k * p.I;
+    float h = sg / (1.0f + expf(-sg)) * su;
+    for (int a = 0; a < parts_h; ++a) {
+        const uint32_t b = to_bf16(h);
+        p.h[at + a * plane] = (uint16_t)b;
+        h = left(h, b << 16);
+    }
+}
+
+// PX: parts of x.
+template <int FMT, int PX>
+__global__ __launch_bounds__(kUpWaves * kWave, 4) void k_moe_up(MoeParams p, int parts_h) {
+    constexpr int U = PX > 1 ? 1 : FMT == kF8 ? 2 : 4;  // steps in flight
     __shared__ float red[kUpWaves][2][256];
     const int itiles = p.I / kRows;
     const int slot = (int)(blockIdx.x / itiles), i0 = (int)(blockIdx.x % itiles) * kRows;
@@ -542,169 +622,227 @@ __global__ __launch_bounds__(kUpWaves * kWave) void k_moe_up(MoeParams p, int pa
     const int r = lane % 16, q = lane / 16;
     const int64_t row = (int64_t)e * 2 * p.I + i0;
     const Rows<FMT> gate(p.w13, row, p.D), up(p.w13, row + p.I, p.D);
-    const Rsrc rx = make_rsrc(p.x, (int64_t)p.T * p.D * (PX == 1 ? 2 : 4));
-    int src[NT];  // element offset of the lane's token, or none
+    Rsrc rx[PX];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) src[t] = 16 * t + r < n ? token_of(sl.mask, 16 * t + r) * p.D : -1;
+    for (int a = 0; a < PX; ++a) rx[a] = make_rsrc(p.xp + (int64_t)a * p.T * p.D, (int64_t)p.T * p.D * 2);
+    const int src = r < n ? token_of(sl.mask, r) * p.D : -1;  // element offset of the lane's token, or none
 
-    v4f ag[NT], au[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) ag[t] = au[t] = v4f{};
+    v4f ag = {}, au = {};
     const int steps = (p.D + kStep - 1) / kStep;
     for (int c0 = wave; c0 < steps; c0 += kUpWaves * U) {
         Raw<FMT> rg[U], ru[U];
+        Act x[U][PX];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * kUpWaves;  // past the last: zeros
+            const int c = c0 + u * kUpWaves, k = c * kStep + 32 * q;  // past the last: zeros
             rg[u] = gate.load(c, r, q);
             ru[u] = up.load(c, r, q);
+#pragma unroll
+            for (int a = 0; a < PX; ++a) x[u][a].load(rx[a], src >= 0 && k < p.D ? src + k : -1);
         }
+        __builtin_amdgcn_sched_barrier(0);  // every load before the first wait
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = (c0 + u * kUpWaves) * kStep + 32 * q;
-            const Frag wg = widen<FMT>(rg[u]), wu = widen<FMT>(ru[u]);
+            Frag f[PX];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (16 * t >= n) break;
-                Act<PX> a;
-                a.load(rx, src[t] >= 0 && k < p.D ? src[t] + k : -1);
-                Frag x[PX];
-                a.parts(x);
-                ag[t] = mma_step<FMT, PX>(wg, x, rg[u].s, ag[t]);
-                au[t] = mma_step<FMT, PX>(wu, x, ru[u].s, au[t]);
-            }
+            for (int a = 0; a < PX; ++a) f[a] = frag_of(x[u][a].w);
+            ag = mma_step<FMT, PX>(widen<FMT>(rg[u]), f, rg[u].s, ag);
+            au = mma_step<FMT, PX>(widen<FMT>(ru[u]), f, ru[u].s, au);
         }
     }
-    const float g = p.w13.g ? p.w13.g[e * p.w13.g_step] : 1.0f;
-    const int64_t plane = (int64_t)p.T * p.k * p.I;
+    // Lane: token r, rows 4 q .. 4 q + 3.
+    *reinterpret_cast<v4f*>(&red[wave][0][r * 16 + 4 * q]) = ag;
+    *reinterpret_cast<v4f*>(&red[wave][1][r * 16 + 4 * q]) = au;
+    __syncthreads();
+    const int m = (int)threadIdx.x / 16;
+    if (threadIdx.x < 256 && m < n) {
+        const float g = p.w13.g ? p.w13.g[e * p.w13.g_step] : 1.0f;
+        float sg = 0.0f, su = 0.0f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        if (16 * t >= n) break;
-        // Lane: token 16 t + r, rows 4 q .. 4 q + 3.
-        *reinterpret_cast<v4f*>(&red[wave][0][r * 16 + 4 * q]) = ag[t];
-        *reinterpret_cast<v4f*>(&red[wave][1][r * 16 + 4 * q]) = au[t];
-        __syncthreads();
-        const int m = 16 * t + (int)threadIdx.x / 16;
-        if (threadIdx.x < 256 && m < n) {
-            float sg = 0.0f, su = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kUpWaves; ++w) sg += red[w][0][threadIdx.x], su += red[w][1][threadIdx.x];
-            sg *= g, su *= g;
-            float h = sg / (1.0f + expf(-sg)) * su;
-            uint16_t* dst = p.h + (int64_t)(off + m) * p.I + i0 + threadIdx.x % 16;
-            for (int a = 0; a < parts_h; ++a) {
-                const uint32_t b = to_bf16(h);
-                dst[a * plane] = (uint16_t)b;
-                h = left(h, b << 16);
-            }
-        }
-        __syncthreads();
+        for (int w = 0; w < kUpWaves; ++w) sg += red[w][0][threadIdx.x], su += red[w][1][threadIdx.x];
+        put_h(p, sg * g, su * g, (int64_t)(off + m) * p.I + i0 + threadIdx.x % 16, parts_h);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Down, and the sum over a token's experts.
+// Down, and gate and up where there are many pairs: a workgroup per slot and 128 rows
+// (64 of gate and the same 64 of up, or 128 of down), four waves of two fragments each.
+// The slot's token values go to LDS once for the 128 rows, a step of 128 elements of
+// each part at a time, by direct loads; two stages, so that the next one's values and
+// weights are on their way while one is multiplied.  (With 16 rows per workgroup the
+// caches deliver the values eight times as often: at 64 tokens the down product took
+// 108 us so, and 63 so.)
+//
+// A stage holds 16 tokens x 256 bytes per part.  The sixteen 16-byte pieces of token
+// t's row sit at slot piece ^ (t + 4) % 16, which spreads the lanes that one
+// ds_read_b128 serves together (0-3, 12-15, 20-23, 24-27, ...; lane l reads piece
+// 4 (l / 16) + i of token l % 16) over all bank groups.
+constexpr int kManyWaves = 4;
+constexpr int kManyRows = 32 * kManyWaves;
+constexpr int kPart = 16 * 256;  // bytes of a stage's part
 
-constexpr int kDownWaves = 16;
-
-template <int FMT, int NT, int PH>
-__global__ __launch_bounds__(kDownWaves * kWave) void k_moe_down(MoeParams p) {
-    constexpr int U = FMT == kF8 ? 2 : 4;
-    __shared__ float wt[kMaxPairs];
-    __shared__ uint8_t tok[kMaxPairs];
-    extern __shared__ __attribute__((aligned(16))) float ytile[];  // waves x T x 16
-    for (int i = threadIdx.x; i < p.T * p.k; i += kDownWaves * kWave) wt[i] = p.plan->wt[i], tok[i] = p.plan->tok[i];
-    __syncthreads();
+// DOWN: this K range's z[pair] = g D_e h in binary32, added up by k_moe_combine; else h.
+template <int FMT, int P, bool DOWN>
+__global__ __launch_bounds__(kManyWaves * kWave) void k_moe_many(MoeParams p, float* z, int ranges, int parts_h) {
+    constexpr int S = 2;  // steps per stage
+    constexpr int kStage = S * P * kPart;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+    const int K = DOWN ? p.I : p.D;
+    const int groups = ((DOWN ? p.D : 2 * p.I) + kManyRows - 1) / kManyRows;
+    const int group = (int)(blockIdx.x % groups), range = (int)(blockIdx.x / groups) % ranges;
+    const int slot = (int)(blockIdx.x / groups) / ranges;
+    const Slot sl = p.plan->slot[slot];
+    if (slot >= p.plan->slots) return;
+    const int e = sl.e, n = __popcll(sl.mask), off = sl.off;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane % 16, q = lane / 16;
-    const int d0 = (int)blockIdx.x * kRows;
-    float* mine = ytile + wave * p.T * 16;
-    for (int i = lane; i < p.T * 16; i += kWave) mine[i] = 0.0f;
+    // The wave's two fragments: rows row and row + 16 of down, or row of gate and of up.
+    // Both sizes are multiples of 32: a wave has both fragments or none.
+    const int row = DOWN ? group * kManyRows + 32 * wave : group * (kManyRows / 2) + 16 * wave;
+    const bool any = row < (DOWN ? p.D : p.I);
+    const int64_t row0 = any ? (DOWN ? (int64_t)e * p.D + row : (int64_t)e * 2 * p.I + row) : 0;
+    const Rows<FMT> w0(DOWN ? p.w2 : p.w13, row0, K), w1(DOWN ? p.w2 : p.w13, any ? row0 + (DOWN ? 16 : p.I) : 0, K);
+    const int stages = (K + S * kStep - 1) / (S * kStep);
+    const int c_lo = stages * range / ranges, c_hi = stages * (range + 1) / ranges;
 
-    const int steps = (p.I + kStep - 1) / kStep;
-    const int total = p.plan->slots * steps;
-    int at = total * wave / kDownWaves;
-    const int end = total * (wave + 1) / kDownWaves;
-    const int64_t plane = (int64_t)p.T * p.k * p.I;
-    while (at < end) {
-        const int slot = at / steps, c_lo = at % steps, c_hi = min(steps, c_lo + end - at);
-        at += c_hi - c_lo;
-        const Slot sl = p.plan->slot[slot];
-        const int e = sl.e, n = __popcll(sl.mask), off = sl.off;
-        const Rows<FMT> down(p.w2, (int64_t)e * p.D + d0, p.I);
-        Rsrc rh[PH];
+    // Direct load `wave` of a part moves tokens 4 wave .. 4 wave + 3, 256 bytes each.
+    const uint16_t* vals = DOWN ? p.h + (int64_t)off * p.I : p.xp;
+    const int64_t part_step = DOWN ? (int64_t)p.T * p.k * p.I : (int64_t)p.T * p.D;
+    const int64_t part_size = (int64_t)(DOWN ? n : p.T) * K * 2;
+    const int m = 4 * wave + lane / 16;
+    const int src = m < n ? (DOWN ? m : token_of(sl.mask, m)) * K : -1;
+    const int piece = (lane % 16) ^ ((m + 4) % 16);
+    auto issue = [&](int c) {
 #pragma unroll
-        for (int a = 0; a < PH; ++a)
-            rh[a] = make_rsrc(p.h + a * plane + (int64_t)off * p.I, (int64_t)n * p.I * 2);
-        v4f acc[NT];
+        for (int u = 0; u < S; ++u) {
+            const int k = (c * S + u) * kStep + 8 * piece;
+            const int at = src >= 0 && k < K ? (src + k) * 2 : kDropped;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] = v4f{};
-        for (int c0 = c_lo; c0 < c_hi; c0 += U) {
-            Raw<FMT> raw[U];
+            for (int a = 0; a < P; ++a)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    make_rsrc(vals + a * part_step, part_size),
+                    (LdsPtr)(lds + (c & 1) * kStage + (u * P + a) * kPart + wave * 1024), 16, at, 0, 0, 0);
+        }
+    };
+
+    v4f acc[2] = {};
+    const bool whole = whole_scales(w0, DOWN ? p.w2.scales : p.w13.scales);
+    issue(c_lo);
+    Raw2<FMT> n0 = load2(w0, c_lo, r, q, whole), n1 = load2(w1, c_lo, r, q, whole);
+    for (int c = c_lo; c < c_hi; ++c) {
+        // Stage c has landed, and no wave still reads stage c - 1.
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+        const Raw2<FMT> now[2] = {n0, n1};
+        issue(c + 1);
+        n0 = load2(w0, c + 1, r, q, whole), n1 = load2(w1, c + 1, r, q, whole);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int u = 0; u < U; ++u) raw[u] = down.load(c0 + u < c_hi ? c0 + u : steps, r, q);
+        for (int u = 0; u < S; ++u) {
+            Frag x[P];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (c0 + u >= c_hi) break;
-                const int k = (c0 + u) * kStep + 32 * q;
-                const Frag w = widen<FMT>(raw[u]);
+            for (int a = 0; a < P; ++a)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (16 * t >= n) break;
-                    Frag x[PH];
+                for (int i = 0; i < 4; ++i)
+                    x[a].v[i] = *reinterpret_cast<const bf16x8_t*>(lds + (c & 1) * kStage + (u * P + a) * kPart + r * 256 +
+                                                                   ((4 * q + i) ^ ((r + 4) % 16)) * 16);
 #pragma unroll
-                    for (int a = 0; a < PH; ++a) {
-                        Act<1> h;
-                        h.load(rh[a], 16 * t + r < n && k < p.I ? (16 * t + r) * p.I + k : -1);
-                        x[a] = frag_of(h.w);
-                    }
-                    acc[t] = mma_step<FMT, PH>(w, x, raw[u].s, acc[t]);
-                }
+            for (int f = 0; f < 2; ++f) {
+                const Raw<FMT> w = now[f].step(u, q);
+                acc[f] = mma_step<FMT, P>(widen<FMT>(w), x, w.s, acc[f]);
             }
         }
-        const float g = p.w2.g ? p.w2.g[e * p.w2.g_step] : 1.0f;
+    }
+    wait_all_barrier();
+    // Lane: token r, rows 4 q .. 4 q + 3 of each fragment.
+    if (!any || r >= n) return;
+    const Weights& w = DOWN ? p.w2 : p.w13;
+    const float g = w.g ? w.g[e * w.g_step] : 1.0f;
+    const int64_t pair = off + r;
+    if (DOWN) {
+        float* dst = z + ((int64_t)range * p.T * p.k + pair) * p.D + row + 4 * q;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            // Lane: token 16 t + r of the slot (no token twice), rows 4 q .. 4 q + 3.
-            if (16 * t + r >= n) continue;
-            const float w = wt[off + 16 * t + r] * g;
-            v4f* dst = reinterpret_cast<v4f*>(mine + tok[off + 16 * t + r] * 16 + 4 * q);
-            v4f v = *dst;
+        for (int f = 0; f < 2; ++f) *reinterpret_cast<v4f*>(dst + 16 * f) = acc[f] * g;
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[t][i], w, v[i]);
-            *dst = v;
+        for (int i = 0; i < 4; ++i) put_h(p, acc[0][i] * g, acc[1][i] * g, pair * p.I + row + 4 * q + i, parts_h);
+    }
+}
+
+// y[t] = sum over the token's choices of weight times z, z by K ranges.  Four columns
+// per thread; the four threads of a quad take the choices in turn and meet in their
+// order, so that a single token still keeps many loads in flight.
+__global__ __launch_bounds__(256) void k_moe_combine(MoeParams p, const float* z, int ranges) {
+    const int cols = p.D / 4, s = threadIdx.x % 4;
+    const int i = (int)blockIdx.x * 64 + (int)threadIdx.x / 4;
+    const int t = min(i / cols, p.T - 1), d = i % cols * 4;  // quads past the last repeat it, unstored
+    const int64_t plane = (int64_t)p.T * p.k * p.D;
+    v4f sum = {};
+    for (int j = s; j < p.k; j += 4) {
+        const int pair = p.plan->pair[t * p.k + j];
+        const float w = p.plan->weight[t * p.k + j];
+        if (pair < 0) continue;
+        const float* src = z + (int64_t)pair * p.D + d;
+        v4f v = {};
+        for (int g0 = 0; g0 < ranges; g0 += 4) {
+            v4f part[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) part[g] = *reinterpret_cast<const v4f*>(src + min(g0 + g, ranges - 1) * plane);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (g0 + g < ranges) v += part[g];
         }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.T * 16; i += kDownWaves * kWave) {
-        float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDownWaves; ++w) sum += ytile[w * p.T * 16 + i];
-        const int64_t o = (int64_t)(i / 16) * p.D + d0 + i % 16;
-        if (p.yt == 1) static_cast<float*>(p.y)[o] = sum;
-        else static_cast<uint16_t*>(p.y)[o] = (uint16_t)to_bf16(sum);
+        for (int c = 0; c < 4; ++c) sum[c] = fmaf(v[c], w, sum[c]);
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        sum[c] += __shfl_xor(sum[c], 1);
+        sum[c] += __shfl_xor(sum[c], 2);
+    }
+    if (s != 0 || i >= p.T * cols) return;
+    const int64_t o = (int64_t)t * p.D + d;
+    if (p.yt == 1) *reinterpret_cast<v4f*>(static_cast<float*>(p.y) + o) = sum;
+    else *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p.y) + o) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
 
 // ---------------------------------------------------------------------------
 
-template <int FMT, int NT>
-void launch_products(const MoeParams& p, bool x32, int parts_h, hipStream_t stream) {
-    const int slots = std::min(p.T * p.k, p.E);
-    const dim3 up((unsigned)(slots * (p.I / kRows))), down((unsigned)(p.D / kRows));
-    if (x32) FP4Q_LAUNCH((k_moe_up<FMT, NT, 3>), up, dim3(kUpWaves * kWave), 0, stream, p, parts_h);
-    else FP4Q_LAUNCH((k_moe_up<FMT, NT, 1>), up, dim3(kUpWaves * kWave), 0, stream, p, parts_h);
-    const unsigned lds = (unsigned)(kDownWaves * p.T * 16 * 4);
-    if (parts_h == 3) FP4Q_LAUNCH((k_moe_down<FMT, NT, 3>), down, dim3(kDownWaves * kWave), lds, stream, p);
-    else FP4Q_LAUNCH((k_moe_down<FMT, NT, 2>), down, dim3(kDownWaves * kWave), lds, stream, p);
+// Slots there may be.
+int64_t max_slots(int64_t T, int64_t E, int64_t k) { return std::min(T * k, E + T * k / 16); }
+
+// K ranges of the down product: as many as fill the chip four workgroups deep, of two
+// steps or more.
+int down_ranges(int64_t T, int64_t D, int64_t I, int64_t E, int64_t k) {
+    const int64_t groups = max_slots(T, E, k) * ((D + kManyRows - 1) / kManyRows);
+    const int64_t stages = (I + 2 * kStep - 1) / (2 * kStep);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(1024 + groups - 1) / groups, stages / 2, 16}));
 }
 
 template <int FMT>
-void launch_tiles(const MoeParams& p, bool x32, int parts_h, hipStream_t stream) {
-    if (p.T <= 16) launch_products<FMT, 1>(p, x32, parts_h, stream);
-    else if (p.T <= 32) launch_products<FMT, 2>(p, x32, parts_h, stream);
-    else launch_products<FMT, 4>(p, x32, parts_h, stream);
+void launch_products(const MoeParams& p, float* z, bool x32, int parts_h, hipStream_t stream) {
+    const int slots = (int)max_slots(p.T, p.E, p.k);
+    const int up_groups = (2 * p.I + kManyRows - 1) / kManyRows, down_groups = (p.D + kManyRows - 1) / kManyRows;
+    const dim3 block(kManyWaves * kWave);
+    // Which form of gate and up: 128 rows per workgroup where that makes enough
+    // workgroups.  Measured (us, 128 rows / 16 rows): 128 workgroups (one token, 8 experts
+    // of 4096 x 1024) 25 / 13, 256 (two tokens) 27 / 22, 448 (one token, 2 of 4096 x 14336)
+    // 34 / 36, 512 (four tokens, NVFP4 2048 x 1024) 20 / 27, 3072 (64 tokens, E4M3) 114 / 157.
+    if (slots * up_groups >= 384) {
+        const dim3 grid((unsigned)(slots * up_groups));
+        if (x32) FP4Q_LAUNCH((k_moe_many<FMT, 3, false>), grid, block, 0, stream, p, z, 1, parts_h);
+        else FP4Q_LAUNCH((k_moe_many<FMT, 1, false>), grid, block, 0, stream, p, z, 1, parts_h);
+    } else {
+        const dim3 grid((unsigned)(slots * (p.I / kRows)));
+        if (x32) FP4Q_LAUNCH((k_moe_up<FMT, 3>), grid, dim3(kUpWaves * kWave), 0, stream, p, parts_h);
+        else FP4Q_LAUNCH((k_moe_up<FMT, 1>), grid, dim3(kUpWaves * kWave), 0, stream, p, parts_h);
+    }
+    const int ranges = down_ranges(p.T, p.D, p.I, p.E, p.k);
+    const dim3 grid((unsigned)(slots * down_groups * ranges));
+    if (parts_h == 3) FP4Q_LAUNCH((k_moe_many<FMT, 3, true>), grid, block, 0, stream, p, z, ranges, parts_h);
+    else FP4Q_LAUNCH((k_moe_many<FMT, 2, true>), grid, block, 0, stream, p, z, ranges, parts_h);
+    FP4Q_LAUNCH(k_moe_combine, dim3((unsigned)((p.T * (p.D / 4) + 63) / 64)), dim3(256), 0, stream, p, (const float*)z, ranges);
 }
 
 // Ranges of K for the router: two steps of 32 per wave keep its loads in flight
@@ -728,7 +866,9 @@ void launch_route(const MoeParams& p, hipStream_t stream) {
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t I, int64_t E, int64_t k) {
-    return kCountBytes + kPlanBytes + up256((size_t)(route_ranges(D) * T * E * 4)) + (size_t)(3 * T * k * I * 2);
+    const size_t logits = up256((size_t)(route_ranges(D) * T * E * 4)), parts = up256((size_t)(3 * T * D * 2));
+    const size_t h = up256((size_t)(3 * T * k * I * 2)), z = (size_t)(down_ranges(T, D, I, E, k) * T * k * D * 4);
+    return kCountBytes + kPlanBytes + logits + parts + h + z;
 }
 
 int launch_moe(const MoeJob& j, char* msg, size_t msg_len) {
@@ -748,21 +888,27 @@ int launch_moe(const MoeJob& j, char* msg, size_t msg_len) {
     p.yt = j.yt;
     p.ranges = route_ranges(j.D);
     p.count = reinterpret_cast<uint32_t*>(ws);
-    p.plan = reinterpret_cast<Plan*>(ws + kCountBytes);
-    p.logits = reinterpret_cast<float*>(ws + kCountBytes + kPlanBytes);
-    p.h = reinterpret_cast<uint16_t*>(ws + kCountBytes + kPlanBytes + up256((size_t)(p.ranges * j.T * j.E * 4)));
+    p.plan = reinterpret_cast<Plan*>(ws += kCountBytes);
+    p.logits = reinterpret_cast<float*>(ws += kPlanBytes);
+    ws += up256((size_t)(p.ranges * j.T * j.E * 4));
+    // Binary32 x in parts; bf16 x is its own.
+    p.xp = j.xt == 1 ? reinterpret_cast<uint16_t*>(ws) : static_cast<uint16_t*>(const_cast<void*>(j.x));
+    p.h = reinterpret_cast<uint16_t*>(ws += up256((size_t)(3 * j.T * j.D * 2)));
+    ws += up256((size_t)(3 * j.T * j.k * j.I * 2));
+    float* z = reinterpret_cast<float*>(ws);
     if (p.router) {
         if (j.xt == 0 && j.rt == 0) launch_route<1, 1>(p, stream);
         else if (j.xt == 0) launch_route<1, 3>(p, stream);
         else if (j.rt == 0) launch_route<3, 1>(p, stream);
         else launch_route<3, 3>(p, stream);
     } else {
-        FP4Q_LAUNCH(k_moe_plan, dim3(1), dim3(1024), 0, stream, p);
+        const int64_t parts = j.xt == 1 ? std::min<int64_t>((j.T * j.D + 8191) / 8192, 256) : 0;
+        FP4Q_LAUNCH(k_moe_plan, dim3((unsigned)(1 + parts)), dim3(1024), 0, stream, p);
     }
     const int parts_h = j.yt == 1 ? 3 : 2;
-    if (j.fmt == 0) launch_tiles<kMx>(p, j.xt == 1, parts_h, stream);
-    else if (j.fmt == 1) launch_tiles<kNv>(p, j.xt == 1, parts_h, stream);
-    else launch_tiles<kF8>(p, j.xt == 1, parts_h, stream);
+    if (j.fmt == 0) launch_products<kMx>(p, z, j.xt == 1, parts_h, stream);
+    else if (j.fmt == 1) launch_products<kNv>(p, z, j.xt == 1, parts_h, stream);
+    else launch_products<kF8>(p, z, j.xt == 1, parts_h, stream);
     const hipError_t e = hipGetLastError();
     if (e == hipSuccess) return 0;
     snprintf(msg, msg_len, "moe kernel launch: %s", hipGetErrorString(e));
