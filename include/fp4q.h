@@ -443,8 +443,8 @@ fp4q_status fp8_quantize_b128(const void* x, int32_t xt, int64_t rows, int64_t c
  *                       2^23; M or N == 0 is a no-op; K == 0 writes zeros
  *   c, ct               device out, M x N row-major, FP4Q_F32 or FP4Q_BF16
  *                       (round to nearest even); aligned to its element
- *   ws, ws_bytes        device scratch of fp8_gemm_b128_workspace_bytes(M, N, K)
- *                       bytes (0 for most shapes; then ws may be NULL), 16-byte
+ *   ws, ws_bytes        device scratch of fp8_gemm_b128_workspace_bytes(M, N, K,
+ *                       ct) bytes (0 for most shapes; then ws may be NULL), 16-byte
  *                       aligned: partial products of K ranges
  * At most 16 rows of A take a kernel that streams B once; others 64 x 64, 128 x 128 or
  * 256 x 256 tiles, by the shape.
@@ -463,8 +463,8 @@ fp4q_status fp8_gemm_b128(const uint8_t* a_codes, const float* a_scales, const u
                           int32_t ct, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes fp8_gemm_b128 needs: 4 * M * N per K range when K is split (a
- * function of M, N and K only); 0 otherwise. */
-size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
+ * function of M, N, K and the output's type only); 0 otherwise. */
+size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t ct);
 
 /* One stacked matrix of a layer's expert weights, (experts * rows) x K, exactly as
  * the quantize calls write it. */

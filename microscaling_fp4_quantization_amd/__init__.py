@@ -89,7 +89,7 @@ def _bind(l):
     l.fp8_quantize_b128.restype = c.c_int
     l.fp8_gemm_b128.argtypes = [P, P, P, P, i32, i64, i64, i64, P, i32, P, sz, P]
     l.fp8_gemm_b128.restype = c.c_int
-    l.fp8_gemm_b128_workspace_bytes.argtypes = [i64, i64, i64]
+    l.fp8_gemm_b128_workspace_bytes.argtypes = [i64, i64, i64, i32]
     l.fp8_gemm_b128_workspace_bytes.restype = sz
     l.moe_layer.argtypes = [P, i32, i64, i64, i64, i32, i32, i32, P, P, P, i32, i32, P, P, P, i32, P, sz, P]
     l.moe_layer.restype = c.c_int
@@ -512,13 +512,14 @@ def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
         raise ValueError(f"out must be contiguous, {m} x {n}")
     if a_scales.device != dev or b_codes.device != dev or b_scales.device != dev or out.device != dev:
         raise ValueError("operands and out must be on one device")
-    need = lib().fp8_gemm_b128_workspace_bytes(m, n, k)
-    if ws is None and need:
-        ws = gemm_workspace(dev, need)
-    rc = lib().fp8_gemm_b128(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
-                             b_kind, m, n, k, out.data_ptr(), _dtype_code(out),
-                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                             _raw_stream(dev))
+    l, ct = lib(), _dtype_code(out)
+    if ws is None and m > 16:  # at most 16 rows take none
+        need = l.fp8_gemm_b128_workspace_bytes(m, n, k, ct)
+        if need:
+            ws = gemm_workspace(dev, need)
+    rc = l.fp8_gemm_b128(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), b_kind,
+                         m, n, k, out.data_ptr(), ct, None if ws is None else ws.data_ptr(),
+                         0 if ws is None else ws.numel(), _raw_stream(dev))
     if rc:
         _check(rc)
     return out
@@ -547,26 +548,29 @@ class MoeOutput:
     topk_weights: torch.Tensor
 
 
+_EXPERT_TYPES = {FMT_MXFP4: (torch.uint8, torch.uint8, 2, 32), FMT_UE4M3: (torch.uint8, torch.uint8, 2, 16),
+                 FMT_E4M3_B128: (torch.float8_e4m3fn, torch.float32, 1, 0)}  # codes, scales, codes per byte, block
+
+
 def _expert_weights(w: ExpertWeights, rows: int, k: int, what: str, device) -> _ExpertWeightsC:
-    codes, scales = _matrix(w.codes, what + " codes"), _matrix(w.scales, what + " scales")
-    if w.fmt == FMT_E4M3_B128:
-        want = (rows, k), _b128_scales(rows, k, B128_TILE)
-        types = torch.float8_e4m3fn, torch.float32
-    elif w.fmt in (FMT_MXFP4, FMT_UE4M3):
-        want = (rows, k // 2), (rows, k // (32 if w.fmt == FMT_MXFP4 else 16))
-        types = torch.uint8, torch.uint8
-    else:
+    codes, scales, g = w.codes, w.scales, w.g
+    if w.fmt not in _EXPERT_TYPES:
         raise ValueError(f"{what}: fmt {w.fmt} is not FMT_MXFP4, FMT_UE4M3 or FMT_E4M3_B128")
-    if (codes.dtype, scales.dtype) != types:
-        raise TypeError(f"{what}: expected {types[0]} codes and {types[1]} scales")
-    if (tuple(codes.shape), tuple(scales.shape)) != want:
+    ct, st, per, block = _EXPERT_TYPES[w.fmt]
+    if codes.dtype != ct or scales.dtype != st:
+        raise TypeError(f"{what}: expected {ct} codes and {st} scales")
+    want = (rows, k // per), (rows, k // block) if block else (_cdiv(rows, 128), _cdiv(k, 128))
+    if codes.shape != want[0] or scales.shape != want[1]:
         raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)}; needed {want[0]} and {want[1]}")
-    if w.g is not None and (w.g.dtype != torch.float32 or not w.g.is_contiguous() or w.g.device != codes.device):
-        raise ValueError(f"{what}: g must be contiguous float32 on the codes' device")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{what}: codes and scales must be contiguous")
     if codes.device != device or scales.device != device:
         raise ValueError(f"{what} must be on x's device")
-    ptr = lambda t: None if t is None else t.data_ptr()
-    return _ExpertWeightsC(ptr(codes), ptr(scales), ptr(w.g), 0 if w.g is None else w.g.numel())
+    if g is None:
+        return _ExpertWeightsC(codes.data_ptr(), scales.data_ptr(), None, 0)
+    if g.dtype != torch.float32 or not g.is_contiguous() or g.device != device:
+        raise ValueError(f"{what}: g must be contiguous float32 on the codes' device")
+    return _ExpertWeightsC(codes.data_ptr(), scales.data_ptr(), g.data_ptr(), g.numel())
 
 
 _moe_workspaces = {}
@@ -575,7 +579,7 @@ _moe_workspaces = {}
 def moe_workspace(device, nbytes: int) -> torch.Tensor:
     """A workspace of at least `nbytes` for moe_layer, zero where it has to be, kept
     per device and current stream and grown on demand."""
-    dev = torch.device(device)
+    dev = device if isinstance(device, torch.device) else torch.device(device)
     key = (dev.index, _raw_stream(dev))
     ws = _moe_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -612,24 +616,30 @@ def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: i
     elif topk_ids is None or topk_weights is None:
         raise ValueError("without a router, topk_ids and topk_weights are needed")
     if topk_ids is None:
-        topk_ids = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
+        topk_ids = x.new_empty((tokens, top_k), dtype=torch.int32)
+    elif topk_ids.shape != (tokens, top_k) or topk_ids.dtype != torch.int32 or not topk_ids.is_contiguous() \
+            or topk_ids.device != x.device:
+        raise ValueError(f"topk_ids must be contiguous int32, {tokens} x {top_k}, on x's device")
     if topk_weights is None:
-        topk_weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
-    for t, dt, name in ((topk_ids, torch.int32, "topk_ids"), (topk_weights, torch.float32, "topk_weights")):
-        if tuple(t.shape) != (tokens, top_k) or t.dtype != dt or not t.is_contiguous() or t.device != x.device:
-            raise ValueError(f"{name} must be contiguous {dt}, {tokens} x {top_k}, on x's device")
+        topk_weights = x.new_empty((tokens, top_k), dtype=torch.float32)
+    elif topk_weights.shape != (tokens, top_k) or topk_weights.dtype != torch.float32 \
+            or not topk_weights.is_contiguous() or topk_weights.device != x.device:
+        raise ValueError(f"topk_weights must be contiguous float32, {tokens} x {top_k}, on x's device")
     if out is None:
-        out = torch.empty((tokens, dim), dtype=out_dtype or x.dtype, device=x.device)
-    elif tuple(out.shape) != (tokens, dim) or not out.is_contiguous() or out.device != x.device:
+        out = x.new_empty((tokens, dim), dtype=out_dtype or x.dtype)
+    elif out.shape != (tokens, dim) or not out.is_contiguous() or out.device != x.device:
         raise ValueError(f"out must be contiguous, {tokens} x {dim}, on x's device")
+    l = lib()
     if ws is None:
-        need = int(lib().moe_layer_workspace_bytes(tokens, dim, inter, experts, top_k))
+        need = l.moe_layer_workspace_bytes(tokens, dim, inter, experts, top_k)
         ws = moe_workspace(x.device, need) if need else None
-    _check(lib().moe_layer(_ptr(x), _dtype_code(x), tokens, dim, inter, experts, top_k, w13.fmt,
-                           ctypes.byref(a), ctypes.byref(b), _ptr(router),
-                           0 if router is None else _dtype_code(router), int(renormalize), _ptr(topk_ids),
-                           _ptr(topk_weights), _ptr(out), _dtype_code(out), _ptr(ws),
-                           0 if ws is None else ws.numel(), _stream(x.device)))
+    rc = l.moe_layer(x.data_ptr(), _dtype_code(x), tokens, dim, inter, experts, top_k, w13.fmt, ctypes.byref(a),
+                     ctypes.byref(b), None if router is None else router.data_ptr(),
+                     0 if router is None else _dtype_code(router), int(renormalize), topk_ids.data_ptr(),
+                     topk_weights.data_ptr(), out.data_ptr(), _dtype_code(out), None if ws is None else ws.data_ptr(),
+                     0 if ws is None else ws.numel(), _raw_stream(x.device))
+    if rc:
+        _check(rc)
     return MoeOutput(out, topk_ids, topk_weights)
 
 

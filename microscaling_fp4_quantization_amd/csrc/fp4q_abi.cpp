@@ -430,7 +430,7 @@ fp4q_status fp8_gemm_b128(const uint8_t* a_codes, const float* a_scales, const u
                 return fail(FP4Q_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
             if (!aligned(a_scales, 4) || !aligned(b_scales, 4))
                 return fail(FP4Q_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
-            const size_t need = fp4q::fp8_gemm_workspace_bytes(M, N, K);
+            const size_t need = fp4q::fp8_gemm_workspace_bytes(M, N, K, ct);
             if (need > 0 && (!ws || ws_bytes < need))
                 return fail(FP4Q_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
                             ws ? ws_bytes : (size_t)0);
@@ -443,9 +443,9 @@ fp4q_status fp8_gemm_b128(const uint8_t* a_codes, const float* a_scales, const u
     return launched(fp4q::launch_fp8_gemm(j, msg, sizeof msg), msg);
 }
 
-size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0 || N <= 0 || K <= 0) return 0;
-    return fp4q::fp8_gemm_workspace_bytes(M, N, K);
+size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t ct) {
+    if (M <= 0 || N <= 0 || K <= 0 || (ct != FP4Q_BF16 && ct != FP4Q_F32)) return 0;
+    return fp4q::fp8_gemm_workspace_bytes(M, N, K, ct);
 }
 
 static fp4q_status moe_weights(const char* fn, const char* what, const fp4q_expert_weights* w, int32_t fmt,

@@ -593,8 +593,8 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_fp8_few(F8Params 
 }
 
 // Which tile, and how many K ranges per tile: the pair that makes the modelled time
-// least.  A function of the shape and the output's type only; the workspace holds
-// either type's ranges.
+// least.  A function of the shape and the output's type only, so that the workspace's
+// size is too.
 constexpr int64_t kMaxPartialBytes = (int64_t)1 << 28;
 
 struct Choice {
@@ -612,6 +612,7 @@ struct TileCost {
 };
 constexpr TileCost kTileCosts[] = {{256, 1, 1.5, 1.5, 3.7, 6.0}, {128, 2, 0.7, 0.53, 0.95, 4.0}, {64, 4, 0.45, 0.22, 0.30, 3.0}};
 constexpr int kCus = 256;
+constexpr int kRanges[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
 
 Choice choose(int64_t M, int64_t N, int64_t K, bool wide) {
     const int64_t S = (K + kBlock - 1) / kBlock;
@@ -621,9 +622,9 @@ Choice choose(int64_t M, int64_t N, int64_t K, bool wide) {
     for (const TileCost& c : kTileCosts) {
         const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
         const double each = wide ? c.each_wide : c.each;
-        for (int64_t sp = 1; sp <= std::min<int64_t>(std::max<int64_t>(S, 1), 64); ++sp) {
+        for (const int sp : kRanges) {
             const int64_t per = (S + sp - 1) / sp;
-            if (sp > 1 && (!may_split || tiles * sp > 4 * kCus || 4 * sp * M * N > kMaxPartialBytes)) break;
+            if (sp > 1 && (sp > S || !may_split || tiles * sp > 4 * kCus || 4 * sp * M * N > kMaxPartialBytes)) break;
             if (sp > 1 && per * (sp - 1) >= S) continue;  // a range would be empty
             // Workgroups on the busiest CU, a full share at a time.
             const int64_t groups = (tiles * sp + kCus - 1) / kCus, full = groups / c.per_cu, rest = groups % c.per_cu;
@@ -631,7 +632,7 @@ Choice choose(int64_t M, int64_t N, int64_t K, bool wide) {
             if (rest) t += (double)per * std::max(c.alone, each * (double)rest) + c.fixed;
             // The partial products' trip through memory, and the launch that adds them.
             if (sp > 1) t += 3.0 + 8.0 * (double)sp * (double)M * (double)N / 8e6;
-            if (t < least) least = t, best = Choice{c.tile, (int)sp};
+            if (t < least) least = t, best = Choice{c.tile, sp};
         }
     }
     return best;
@@ -649,9 +650,9 @@ void launch_tile(const F8Params& p, int tile, unsigned groups, hipStream_t strea
 
 }  // namespace
 
-size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int ct) {
     if (M <= kFewMaxM) return 0;
-    const int sp = std::max(choose(M, N, K, false).splits, choose(M, N, K, true).splits);  // whatever the output's type
+    const int sp = choose(M, N, K, ct == 1).splits;
     return sp > 1 ? (size_t)(4 * sp * M * N) : 0;
 }
 

@@ -139,11 +139,11 @@ struct Fp8GemmJob {
     int64_t M, N, K;
     void* c;
     int ct;            // 0 bf16, 1 f32
-    void* ws;          // fp8_gemm_workspace_bytes(M, N, K) bytes: partial products
+    void* ws;          // fp8_gemm_workspace_bytes(M, N, K, ct) bytes: partial products
     void* stream;
 };
 
-size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int ct);
 
 // Mixture-of-experts layer for a few tokens.
 struct MoeWeights {

@@ -53,13 +53,13 @@ def test_gemm_validation(L):
     assert gemm(L, sa=B + 2) == ALIGN and gemm(L, c=A + 1) == ALIGN
     assert gemm(L, m=0, a=None, sa=None, b=None, sb=None, c=None) == OK
     assert gemm(L, n=0, a=None, sa=None, b=None, sb=None, c=None) == OK
-    need = L.fp8_gemm_b128_workspace_bytes(100, 256, 8192)
+    need = L.fp8_gemm_b128_workspace_bytes(100, 256, 8192, 0)
     assert need > 0 and need % (4 * 100 * 256) == 0
     assert gemm(L, m=100, n=256, k=8192) == WS
     assert gemm(L, m=100, n=256, k=8192, ws=A, wsb=need - 1) == WS
     assert gemm(L, m=100, n=256, k=8192, ws=A + 8, wsb=need) == ALIGN
-    assert L.fp8_gemm_b128_workspace_bytes(16, 256, 8192) == 0
-    assert L.fp8_gemm_b128_workspace_bytes(0, 256, 8192) == 0
+    assert L.fp8_gemm_b128_workspace_bytes(16, 256, 8192, 0) == 0
+    assert L.fp8_gemm_b128_workspace_bytes(0, 256, 8192, 0) == 0
 
 
 def weights(codes=A, scales=B, g=None, n=0):
