@@ -61,6 +61,7 @@ struct F8Params {
     int S;             // K blocks
     void* c;
     int ct;            // 0 bf16, 1 f32
+    bool whole;        // C's rows start on 16 bytes
     int splits;        // K ranges per tile (1: C directly)
     float* partial;    // splits > 1: splits x M x N
 };
@@ -192,9 +193,8 @@ __device__ __forceinline__ void store_pass_any(const uint8_t* lds, int h, Rsrc r
 // wn * WN + 16 i + 4 (l / 16) + e.
 template <int EB>
 __device__ __forceinline__ void store_tile16(const v4f (&acc)[TB][TA], uint8_t* lds, Rsrc rc, int wave, int wm,
-                                             int wn, int lane, int64_t rows_a, int64_t n0, int64_t N) {
+                                             int wn, int lane, int64_t rows_a, int64_t n0, int64_t N, bool whole) {
     typedef EpiPlan<EB> P;
-    const bool whole = ((N * EB) & 15) == 0;
 #pragma unroll
     for (int h = 0; h < P::kPasses; ++h) {
         if (wm * WM / P::kRowsPass == h) {
@@ -366,8 +366,9 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const int ct = splits > 1 ? 1 : p.ct;
     const int eb = ct == 1 ? 4 : 2;
     const Rsrc rc = make_rsrc(static_cast<char*>(c) + m0 * p.N * eb, rows_a * p.N * eb);
-    if (ct == 1) store_tile16<4>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
-    else store_tile16<2>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N);
+    const bool whole = splits > 1 ? (p.N & 3) == 0 : p.whole;
+    if (ct == 1) store_tile16<4>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N, whole);
+    else store_tile16<2>(acc, lds, rc, wave, wm, wn, lane, rows_a, n0, p.N, whole);
 }
 
 // ---------------------------------------------------------------------------
@@ -491,7 +492,7 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_fp8_mid(F8Params
     const int eb = ct == 1 ? 4 : 2;
     const Rsrc rc = make_rsrc(static_cast<char*>(c) + m0 * p.N * eb, (int64_t)rows_a * p.N * eb);
     const int cols = rows_b;  // columns of C in this tile
-    if (((p.N * eb) & 15) == 0) {
+    if (splits > 1 ? (p.N & 3) == 0 : p.whole) {
         const int units = T * eb / 16;  // 16-byte units per row
         for (int u = threadIdx.x; u < rows_a * units; u += 256) {
             const int r = u / units, col = u % units * (16 / eb);
@@ -660,7 +661,8 @@ int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len) {
     if (j.M == 0 || j.N == 0) return 0;
     hipStream_t stream = static_cast<hipStream_t>(j.stream);
     const int S = (int)((j.K + kBlock - 1) / kBlock);
-    F8Params p{j.a_codes, j.a_scales, j.b_codes, j.b_scales, j.M, j.N, j.K, S, j.c, j.ct, 1,
+    const bool whole = j.N * (j.ct == 1 ? 4 : 2) % 16 == 0 && (uintptr_t)j.c % 16 == 0;
+    F8Params p{j.a_codes, j.a_scales, j.b_codes, j.b_scales, j.M, j.N, j.K, S, j.c, j.ct, whole, 1,
                static_cast<float*>(j.ws)};
     if (j.M <= kFewMaxM) {
         // Enough waves to keep memory busy whatever N: 16 per workgroup while

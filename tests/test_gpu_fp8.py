@@ -304,3 +304,37 @@ def test_linear_shapes_and_what_needs_no_gradient():
     assert torch.equal(wg.grad, torch.zeros_like(w))
     with pytest.raises(ValueError, match="last sizes"):
         fq.fp8_linear(x, w[:, :40])
+
+
+@pytest.mark.parametrize("kind", [ROW, TILE])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_gemm_of_many_large_tiles(kind, out_dtype):
+    """More 256 x 256 tiles than the chip holds at once, the last ones cut short in both sizes: sampled rows and
+    columns within the bound."""
+    m, n, k = 4100, 5003, 512
+    a, b = operand(m, k, 14, False), operand(n, k, 15, kind == TILE)
+    got = product(a, b, kind, out_dtype)
+    rows = np.r_[0:5, 255:258, 2047:2050, 4095:4100]
+    cols = np.r_[0:4, 2040:2060, 3500:3600:7, 3830:3850, 4340:4360, 4600:5003:13, 5000:5003]
+    av, bv = ref.value(*a, False)[rows], ref.value(*b, kind == TILE)[cols]
+    want, size = av @ bv.T, np.abs(av) @ np.abs(bv).T
+    bar = (k / 128 + 8) * 2.0 ** -23 * size if out_dtype == torch.float32 else 2.0 ** -14 * size + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(got[np.ix_(rows, cols)] - want) <= bar)
+    # Every element is written: no row or column is left as it was.
+    f8 = lambda c: dev(c).view(torch.float8_e4m3fn)
+    out = torch.full((m, n), float("nan"), dtype=out_dtype, device=DEV)
+    fq.fp8_gemm_b128(f8(a[0]), dev(a[1]), f8(b[0]), dev(b[1]), kind, out=out)
+    assert not torch.isnan(out).any()
+
+
+@pytest.mark.parametrize("m,n", [(3, 24), (100, 24), (300, 520)])
+def test_gemm_writes_where_rows_do_not_start_on_16_bytes(m, n):
+    """An output whose rows are whole 16-byte units apart but start off them."""
+    k = 256
+    a, b = operand(m, k, 16, False), operand(n, k, 17, True)
+    f8 = lambda c: dev(c).view(torch.float8_e4m3fn)
+    flat = torch.zeros(m * n + 9, dtype=torch.bfloat16, device=DEV)
+    out = flat[3:3 + m * n].view(m, n)
+    fq.fp8_gemm_b128(f8(a[0]), dev(a[1]), f8(b[0]), dev(b[1]), TILE, out=out)
+    assert torch.equal(out, fq.fp8_gemm_b128(f8(a[0]), dev(a[1]), f8(b[0]), dev(b[1]), TILE, out_dtype=torch.bfloat16))
+    assert not flat[:3].any() and not flat[3 + m * n:].any()
