@@ -466,6 +466,36 @@ fp4q_status fp8_gemm_b128(const uint8_t* a_codes, const float* a_scales, const u
  * function of M, N, K and the output's type only); 0 otherwise. */
 size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t ct);
 
+/*
+ * A linear layer on these operands, as a training step uses it: y = Qr(x) Qt(w)^T,
+ * dx = Qr(dy) Qt(w), dw = Qr(dy^T) Qr(x^T)^T, where Qr and Qt are the values that
+ * fp8_quantize_b128 gives under row and tile scales.  (The quantizer counts as the
+ * identity in the backward pass: dx and dw are the gradients of the product, with
+ * each product's operands quantized along its own contraction.)  Equal, bit for bit,
+ * to the calls of fp8_quantize_b128 and fp8_gemm_b128 that they stand for; each
+ * tensor is read once.
+ *   x, y, dy, dx  tokens x in and tokens x out, dtype xt; w, dw out x in, dtype wt;
+ *                 contiguous, aligned to their elements
+ *   want_dx, want_dw  which gradients the backward call will be asked for
+ *   saved         device, fp8_linear_saved_bytes() bytes, 256-byte aligned, written
+ *                 by the forward call and read by the backward call, which asks for
+ *                 the same gradients (dx or dw NULL for one that is not wanted)
+ *   ws            device, fp8_linear_workspace_bytes() bytes (enough for either call),
+ *                 256-byte aligned
+ *   tokens, in, out  each below 2^21; an empty matrix is valid (a product over an
+ *                 empty size is zeros)
+ * Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN, FP4Q_ERR_WORKSPACE,
+ * FP4Q_ERR_HIP; nothing is launched on one other than FP4Q_ERR_HIP.
+ */
+fp4q_status fp8_linear_forward(const void* x, int32_t xt, const void* w, int32_t wt, int64_t tokens, int64_t in,
+                               int64_t out, void* y, int32_t want_dx, int32_t want_dw, void* saved,
+                               size_t saved_bytes, void* ws, size_t ws_bytes, void* stream);
+fp4q_status fp8_linear_backward(const void* dy, int32_t xt, int32_t wt, int64_t tokens, int64_t in, int64_t out,
+                                void* dx, void* dw, const void* saved, size_t saved_bytes, void* ws,
+                                size_t ws_bytes, void* stream);
+size_t fp8_linear_saved_bytes(int64_t tokens, int64_t in, int64_t out, int32_t want_dx, int32_t want_dw);
+size_t fp8_linear_workspace_bytes(int64_t tokens, int64_t in, int64_t out, int32_t xt, int32_t wt);
+
 /* One stacked matrix of a layer's expert weights, (experts * rows) x K, exactly as
  * the quantize calls write it. */
 typedef struct {

@@ -40,6 +40,7 @@ EXPORTS = ("mxfp4_quantize", "nvfp4_quantize", "nvfp4_quantize_noalloc", "fp4_qu
            "fp4_block_mse", "hadamard_block_rotate", "fp4_gemm_mxfp4", "fp4_gemm_workspace_bytes",
            "fp4_gemm_nvfp4", "fp4_gemm_nvfp4_workspace_bytes",
            "fp8_quantize_b128", "fp8_gemm_b128", "fp8_gemm_b128_workspace_bytes",
+           "fp8_linear_forward", "fp8_linear_backward", "fp8_linear_saved_bytes", "fp8_linear_workspace_bytes",
            "moe_layer", "moe_layer_workspace_bytes",
            "fp4q_workspace_bytes",
            "fp4q_last_error", "fp4q_abi_version", "fp4q_profile_events", "fp4q_profile_count")
@@ -91,6 +92,12 @@ def _bind(l):
     l.fp8_gemm_b128.restype = c.c_int
     l.fp8_gemm_b128_workspace_bytes.argtypes = [i64, i64, i64, i32]
     l.fp8_gemm_b128_workspace_bytes.restype = sz
+    l.fp8_linear_forward.argtypes = [P, i32, P, i32, i64, i64, i64, P, i32, i32, P, sz, P, sz, P]
+    l.fp8_linear_backward.argtypes = [P, i32, i32, i64, i64, i64, P, P, P, sz, P, sz, P]
+    l.fp8_linear_forward.restype = l.fp8_linear_backward.restype = c.c_int
+    l.fp8_linear_saved_bytes.argtypes = [i64, i64, i64, i32, i32]
+    l.fp8_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    l.fp8_linear_saved_bytes.restype = l.fp8_linear_workspace_bytes.restype = sz
     l.moe_layer.argtypes = [P, i32, i64, i64, i64, i32, i32, i32, P, P, P, i32, i32, P, P, P, i32, P, sz, P]
     l.moe_layer.restype = c.c_int
     l.moe_layer_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]

@@ -448,6 +448,152 @@ size_t fp8_gemm_b128_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t ct
     return fp4q::fp8_gemm_workspace_bytes(M, N, K, ct);
 }
 
+// A linear layer's operands in memory: the parts of `saved` (what the backward pass
+// needs: w's transpose under tile scales, x's under row scales) and of the workspace
+// (what a pass uses itself), each part on a 256-byte boundary.
+namespace {
+
+struct B128Part {
+    uint8_t* codes;
+    float* scales;
+};
+
+struct Carve {
+    char* at;
+    size_t used = 0;
+    void* take(size_t n) {
+        void* p = at ? at + used : nullptr;
+        used += (n + 255) / 256 * 256;
+        return p;
+    }
+    // Codes and scales of a rows x cols operand.
+    B128Part part(int64_t rows, int64_t cols, bool tile) {
+        const int64_t kb = (cols + 127) / 128;
+        B128Part b;
+        b.codes = static_cast<uint8_t*>(take((size_t)(rows * ((cols + 15) / 16 * 16))));
+        b.scales = static_cast<float*>(take((size_t)(4 * kb * (tile ? (rows + 127) / 128 : rows))));
+        return b;
+    }
+};
+
+struct LinearSaved {
+    B128Part wt{}, xt{};
+    size_t bytes;
+    LinearSaved(void* p, int64_t T, int64_t K, int64_t N, bool dx, bool dw) {
+        Carve c{static_cast<char*>(p)};
+        if (dx) wt = c.part(K, N, true);
+        if (dw) xt = c.part(K, T, false);
+        bytes = c.used;
+    }
+};
+
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// Bytes that a product needs for its K ranges, as the library chooses them.
+size_t product_ws(int64_t M, int64_t N, int64_t K, int ct) {
+    return M > 0 && N > 0 && K > 0 ? fp4q::fp8_gemm_workspace_bytes(M, N, K, ct) : 0;
+}
+
+struct LinearForward {
+    B128Part x, w;
+    void* product;
+    size_t bytes;
+    LinearForward(void* p, int64_t T, int64_t K, int64_t N, int xt) {
+        Carve c{static_cast<char*>(p)};
+        x = c.part(T, K, false);
+        w = c.part(N, K, true);
+        product = c.take(product_ws(T, N, up16(K), xt));
+        bytes = c.used;
+    }
+};
+
+struct LinearBackward {
+    B128Part dy{}, dyt{};
+    void* product;
+    size_t bytes;
+    LinearBackward(void* p, int64_t T, int64_t K, int64_t N, int xt, int wt, bool dx, bool dw) {
+        Carve c{static_cast<char*>(p)};
+        if (dx) dy = c.part(T, N, false);
+        if (dw) dyt = c.part(N, T, false);
+        const size_t a = dx ? product_ws(T, K, up16(N), xt) : 0, b = dw ? product_ws(N, K, up16(T), wt) : 0;
+        product = c.take(a > b ? a : b);
+        bytes = c.used;
+    }
+};
+
+fp4q_status linear_shape(const char* fn, int64_t T, int64_t K, int64_t N, int32_t xt, int32_t wt) {
+    TRY(check_dtype(fn, xt));
+    TRY(check_dtype(fn, wt));
+    // Each size is a product's K and another's N (with up to 4 bytes an element).
+    const int64_t most = (int64_t)1 << 21;
+    if (T < 0 || K < 0 || N < 0 || T >= most || K >= most || N >= most)
+        return fail(FP4Q_ERR_SHAPE, "%s: %lld tokens, %lld in, %lld out: each must be below 2^21", fn, (long long)T,
+                    (long long)K, (long long)N);
+    if (T * K > (int64_t)INT32_MAX * 512 || N * K > (int64_t)INT32_MAX * 512 || T * N > (int64_t)INT32_MAX * 512)
+        return fail(FP4Q_ERR_SHAPE, "%s: a matrix exceeds (2^31 - 1) * 512 elements", fn);
+    return FP4Q_OK;
+}
+
+fp4q_status linear_buffer(const char* fn, const char* what, const void* p, size_t have, size_t need) {
+    if (need == 0) return FP4Q_OK;
+    if (!p || have < need) return fail(FP4Q_ERR_WORKSPACE, "%s: needs %s of %zu bytes (got %zu)", fn, what, need, p ? have : (size_t)0);
+    if (!aligned(p, 256)) return fail(FP4Q_ERR_ALIGN, "%s: %s must be 256-byte aligned", fn, what);
+    return FP4Q_OK;
+}
+
+}  // namespace
+
+size_t fp8_linear_saved_bytes(int64_t tokens, int64_t in, int64_t out, int32_t want_dx, int32_t want_dw) {
+    if (linear_shape("fp8_linear_saved_bytes", tokens, in, out, FP4Q_BF16, FP4Q_BF16) != FP4Q_OK) return 0;
+    return LinearSaved(nullptr, tokens, in, out, want_dx != 0, want_dw != 0).bytes;
+}
+
+size_t fp8_linear_workspace_bytes(int64_t tokens, int64_t in, int64_t out, int32_t xt, int32_t wt) {
+    if (linear_shape("fp8_linear_workspace_bytes", tokens, in, out, xt, wt) != FP4Q_OK) return 0;
+    const size_t f = LinearForward(nullptr, tokens, in, out, xt).bytes;
+    const size_t b = LinearBackward(nullptr, tokens, in, out, xt, wt, true, true).bytes;
+    return f > b ? f : b;
+}
+
+fp4q_status fp8_linear_forward(const void* x, int32_t xt, const void* w, int32_t wt, int64_t tokens, int64_t in,
+                               int64_t out, void* y, int32_t want_dx, int32_t want_dw, void* saved,
+                               size_t saved_bytes, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "fp8_linear_forward";
+    TRY(linear_shape(fn, tokens, in, out, xt, wt));
+    if ((tokens > 0 && in > 0 && !x) || (out > 0 && in > 0 && !w) || (tokens > 0 && out > 0 && !y))
+        return fail(FP4Q_ERR_ARG, "%s: x, w and y must not be NULL", fn);
+    if (!aligned(x, xt == FP4Q_F32 ? 4 : 2) || !aligned(w, wt == FP4Q_F32 ? 4 : 2) || !aligned(y, xt == FP4Q_F32 ? 4 : 2))
+        return fail(FP4Q_ERR_ALIGN, "%s: x, w and y must be aligned to their elements", fn);
+    const LinearSaved s(saved, tokens, in, out, want_dx != 0, want_dw != 0);
+    TRY(linear_buffer(fn, "saved", saved, saved_bytes, s.bytes));
+    const LinearForward f(ws, tokens, in, out, xt);
+    TRY(linear_buffer(fn, "a workspace", ws, ws_bytes, f.bytes));
+    char msg[256] = {0};
+    TRY(launched(fp4q::launch_fp8_quantize({x, xt, tokens, in, false, f.x.codes, f.x.scales, s.xt.codes, s.xt.scales, stream}, msg, sizeof msg), msg));
+    TRY(launched(fp4q::launch_fp8_quantize({w, wt, out, in, true, f.w.codes, f.w.scales, s.wt.codes, s.wt.scales, stream}, msg, sizeof msg), msg));
+    return launched(fp4q::launch_fp8_gemm({f.x.codes, f.x.scales, f.w.codes, f.w.scales, false, tokens, out, up16(in), y, xt, f.product, stream}, msg, sizeof msg), msg);
+}
+
+fp4q_status fp8_linear_backward(const void* dy, int32_t xt, int32_t wt, int64_t tokens, int64_t in, int64_t out,
+                                void* dx, void* dw, const void* saved, size_t saved_bytes, void* ws,
+                                size_t ws_bytes, void* stream) {
+    const char* fn = "fp8_linear_backward";
+    TRY(linear_shape(fn, tokens, in, out, xt, wt));
+    if (!dx && !dw) return fail(FP4Q_ERR_ARG, "%s: dx and dw must not both be NULL", fn);
+    if (tokens > 0 && out > 0 && !dy) return fail(FP4Q_ERR_ARG, "%s: dy must not be NULL", fn);
+    if (!aligned(dy, xt == FP4Q_F32 ? 4 : 2) || !aligned(dx, xt == FP4Q_F32 ? 4 : 2) || !aligned(dw, wt == FP4Q_F32 ? 4 : 2))
+        return fail(FP4Q_ERR_ALIGN, "%s: dy, dx and dw must be aligned to their elements", fn);
+    const LinearSaved s(const_cast<void*>(saved), tokens, in, out, dx != nullptr, dw != nullptr);
+    TRY(linear_buffer(fn, "saved", saved, saved_bytes, s.bytes));
+    const LinearBackward b(ws, tokens, in, out, xt, wt, dx != nullptr, dw != nullptr);
+    TRY(linear_buffer(fn, "a workspace", ws, ws_bytes, b.bytes));
+    char msg[256] = {0};
+    TRY(launched(fp4q::launch_fp8_quantize({dy, xt, tokens, out, false, b.dy.codes, b.dy.scales, b.dyt.codes, b.dyt.scales, stream}, msg, sizeof msg), msg));
+    if (dx) TRY(launched(fp4q::launch_fp8_gemm({b.dy.codes, b.dy.scales, s.wt.codes, s.wt.scales, false, tokens, in, up16(out), dx, xt, b.product, stream}, msg, sizeof msg), msg));
+    if (dw) TRY(launched(fp4q::launch_fp8_gemm({b.dyt.codes, b.dyt.scales, s.xt.codes, s.xt.scales, true, out, in, up16(tokens), dw, wt, b.product, stream}, msg, sizeof msg), msg));
+    return ok();
+}
+
 static fp4q_status moe_weights(const char* fn, const char* what, const fp4q_expert_weights* w, int32_t fmt,
                                int64_t experts, fp4q::MoeWeights& out) {
     if (!w) return fail(FP4Q_ERR_ARG, "%s: %s must not be NULL", fn, what);

@@ -9,49 +9,77 @@ The quantizer is taken as the identity in the backward pass (its slope inside th
 range is 1 on average): dx and dw are the exact gradients of the product, with each
 product's operands quantized along its own contraction.  Each tensor is read once:
 x and dy give the row-major and the transposed codes in one pass, and w's tile
-scales serve both products that it is in.
+scales serve both products that it is in.  Each pass is one call of the library: a
+training step's small layers are bound by the host, and call by call the same work
+took it half as long again.
 """
 from __future__ import annotations
 
 import torch
 
-from . import B128_ROW, B128_TILE, fp8_gemm_b128, fp8_quantize_b128
+from . import _check, _dtype_code, _raw_stream, gemm_workspace, lib
 
 
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
-        need_dx, need_dw = ctx.needs_input_grad
-        flat = x.reshape(-1, x.shape[-1]).contiguous()
-        xq = fp8_quantize_b128(flat, B128_ROW, transposed=need_dw)
-        wq = fp8_quantize_b128(w.contiguous(), B128_TILE, transposed=need_dx)
-        if need_dx or need_dw:
-            ctx.save_for_backward(wq.codes_t, wq.scales_t, xq.codes_t, xq.scales_t)
-            ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, w.dtype
-        y = fp8_gemm_b128(xq.codes, xq.scales, wq.codes, wq.scales, B128_TILE, out_dtype=x.dtype)
-        return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
+        want_dx, want_dw = ctx.needs_input_grad
+        l, dev = lib(), x.device
+        out, k = w.shape
+        shape = x.shape
+        if x.dim() != 2:
+            x = x.reshape(-1, k)
+        if not x.is_contiguous():
+            x = x.contiguous()
+        if not w.is_contiguous():
+            w = w.contiguous()
+        tokens = x.shape[0]
+        xt, wt = _dtype_code(x), _dtype_code(w)
+        y = x.new_empty((tokens, out))
+        n = l.fp8_linear_saved_bytes(tokens, k, out, want_dx, want_dw)
+        saved = x.new_empty(n, dtype=torch.uint8) if n else None
+        ws = gemm_workspace(dev, l.fp8_linear_workspace_bytes(tokens, k, out, xt, wt))
+        rc = l.fp8_linear_forward(x.data_ptr(), xt, w.data_ptr(), wt, tokens, k, out, y.data_ptr(), want_dx, want_dw,
+                                  None if saved is None else saved.data_ptr(), n, ws.data_ptr(), ws.numel(),
+                                  _raw_stream(dev))
+        if rc:
+            _check(rc)
+        if want_dx or want_dw:
+            ctx.save_for_backward(saved)
+            ctx.sizes = shape, tokens, k, out, x.dtype, w.dtype
+        return y if len(shape) == 2 else y.view(*shape[:-1], out)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        need_dx, need_dw = ctx.needs_input_grad
-        wt, swt, xt, sxt = ctx.saved_tensors
-        dy = dy.reshape(-1, dy.shape[-1]).contiguous()
-        q = fp8_quantize_b128(dy, B128_ROW, codes=need_dx, transposed=need_dw)
-        dx = dw = None
-        if need_dx:
-            dx = fp8_gemm_b128(q.codes, q.scales, wt, swt, B128_TILE, out_dtype=ctx.x_dtype).view(ctx.x_shape)
-        if need_dw:
-            dw = fp8_gemm_b128(q.codes_t, q.scales_t, xt, sxt, B128_ROW, out_dtype=ctx.w_dtype)
+        want_dx, want_dw = ctx.needs_input_grad
+        shape, tokens, k, out, x_dtype, w_dtype = ctx.sizes
+        saved, = ctx.saved_tensors
+        l, dev = lib(), dy.device
+        if not dy.is_contiguous():
+            dy = dy.contiguous()
+        xt = _dtype_code(dy)
+        wt = xt if w_dtype == x_dtype else 1 - xt
+        dx = dy.new_empty(shape) if want_dx else None
+        dw = dy.new_empty((out, k), dtype=w_dtype) if want_dw else None
+        ws = gemm_workspace(dev, l.fp8_linear_workspace_bytes(tokens, k, out, xt, wt))
+        # An empty gradient has no address of its own: any aligned one stands for it.
+        rc = l.fp8_linear_backward(dy.data_ptr(), xt, wt, tokens, k, out,
+                                   (dx.data_ptr() or ws.data_ptr()) if want_dx else None,
+                                   (dw.data_ptr() or ws.data_ptr()) if want_dw else None,
+                                   None if saved is None else saved.data_ptr(), 0 if saved is None else saved.numel(),
+                                   ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        if rc:
+            _check(rc)
         return dx, dw
 
 
 def fp8_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     """x (... x in-features) times w (out-features x in-features) transposed, both
-    bfloat16 or float32, on 8-bit block-128 operands; differentiable in both.  y
-    and dx have x's dtype, dw has w's."""
+    bfloat16 or float32 on the device, on 8-bit block-128 operands; differentiable in
+    both.  y and dx have x's dtype, dw has w's."""
     if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"x has shape {tuple(x.shape)}, w {tuple(w.shape)}: the last sizes must agree")
-    if x.device != w.device:
+    if x.device != w.device or not x.is_cuda:
         raise ValueError("x and w must be on one device")
     return _Fp8Linear.apply(x, w)

@@ -97,3 +97,30 @@ def test_moe_validation(L):
     assert L.moe_layer(None, 0, 0, 64, 32, 6, 2, 0, None, None, None, 0, 1, None, None, None, 0, None, 0, None) == OK
     assert L.moe_layer(A, 0, 4, 64, 32, 6, 2, 0, None, None, None, 0, 1, C, D, A, 0, A, need, None) == ARG
     assert moe(L, fmt=1, w13=weights(scales=B, g=C, n=1), ws=None) == WS  # past the weights' checks
+
+
+def test_linear_validation(L):
+    T, K, N = 40, 96, 70
+    saved, ws = L.fp8_linear_saved_bytes(T, K, N, 1, 1), L.fp8_linear_workspace_bytes(T, K, N, 0, 0)
+    assert saved > 0 and ws > 0 and saved % 256 == 0
+    assert L.fp8_linear_saved_bytes(T, K, N, 0, 0) == 0 and L.fp8_linear_saved_bytes(-1, K, N, 1, 1) == 0
+    assert L.fp8_linear_saved_bytes(T, K, N, 1, 0) + L.fp8_linear_saved_bytes(T, K, N, 0, 1) == saved
+
+    def fwd(x=A, xt=0, w=B, wt=0, t=T, k=K, n=N, y=C, dx=1, dw=1, s=D, sb=saved, wk=A, wb=ws):
+        return L.fp8_linear_forward(x, xt, w, wt, t, k, n, y, dx, dw, s, sb, wk, wb, None)
+
+    assert fwd(xt=2) == ARG and fwd(wt=-1) == ARG
+    assert fwd(t=-1) == SHAPE and fwd(n=1 << 21) == SHAPE and fwd(t=1 << 20, k=1 << 20) == SHAPE
+    assert fwd(x=None) == ARG and fwd(w=None) == ARG and fwd(y=None) == ARG
+    assert fwd(x=A + 1) == ALIGN and fwd(y=C + 1) == ALIGN and fwd(wt=1, w=B + 2) == ALIGN
+    assert fwd(s=None) == WS and fwd(sb=saved - 1) == WS and "saved" in err(L)
+    assert fwd(s=D + 16) == ALIGN
+    assert fwd(wk=None) == WS and fwd(wb=100) == WS and fwd(wk=A + 16) == ALIGN
+
+    def bwd(dy=A, xt=0, wt=0, t=T, k=K, n=N, dx=B, dw=C, s=D, sb=saved, wk=A, wb=ws):
+        return L.fp8_linear_backward(dy, xt, wt, t, k, n, dx, dw, s, sb, wk, wb, None)
+
+    assert bwd(dx=None, dw=None) == ARG and "both" in err(L)
+    assert bwd(dy=None) == ARG and bwd(xt=3) == ARG and bwd(k=-1) == SHAPE
+    assert bwd(dx=B + 1) == ALIGN and bwd(wt=1, dw=C + 2) == ALIGN
+    assert bwd(s=None) == WS and bwd(sb=saved - 1) == WS and bwd(wk=None) == WS and bwd(wb=1) == WS

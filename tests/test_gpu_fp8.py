@@ -338,3 +338,26 @@ def test_gemm_writes_where_rows_do_not_start_on_16_bytes(m, n):
     fq.fp8_gemm_b128(f8(a[0]), dev(a[1]), f8(b[0]), dev(b[1]), TILE, out=out)
     assert torch.equal(out, fq.fp8_gemm_b128(f8(a[0]), dev(a[1]), f8(b[0]), dev(b[1]), TILE, out_dtype=torch.bfloat16))
     assert not flat[:3].any() and not flat[3 + m * n:].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("t,n,k", [(5, 40, 33), (200, 300, 260), (70, 1000, 4100)])
+def test_linear_is_the_calls_that_it_stands_for(t, n, k, dtype):
+    rng = np.random.default_rng([18, t, n, k])
+    mk = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dtype).to(DEV)
+    x, w, dy = mk(t, k).requires_grad_(), mk(n, k).requires_grad_(), mk(t, n)
+    y = fq.fp8_linear(x, w)
+    y.backward(dy)
+    xq, wq = fq.fp8_quantize_b128(x.detach(), ROW, transposed=True), fq.fp8_quantize_b128(w.detach(), TILE, transposed=True)
+    dq = fq.fp8_quantize_b128(dy, ROW, transposed=True)
+    assert torch.equal(y, fq.fp8_gemm_b128(xq.codes, xq.scales, wq.codes, wq.scales, TILE, dtype))
+    assert torch.equal(x.grad, fq.fp8_gemm_b128(dq.codes, dq.scales, wq.codes_t, wq.scales_t, TILE, dtype))
+    assert torch.equal(w.grad, fq.fp8_gemm_b128(dq.codes_t, dq.scales_t, xq.codes_t, xq.scales_t, ROW, dtype))
+
+
+def test_linear_of_mixed_types():
+    x = torch.randn(9, 64, device=DEV, dtype=torch.bfloat16, requires_grad=True)
+    w = torch.randn(20, 64, device=DEV, requires_grad=True)
+    y = fq.fp8_linear(x, w)
+    y.sum().backward()
+    assert y.dtype == x.grad.dtype == torch.bfloat16 and w.grad.dtype == torch.float32
