@@ -137,20 +137,20 @@ struct Raw {
 template <int FMT>
 struct Rows {
     Rsrc codes, scales;
-    int K, kb;
+    int K, kb, end;     // `end`: no element from here on is read
     const float* tile;  // kF8: the tile scales of these rows, one per step
-    __device__ __forceinline__ Rows(const Weights& w, int64_t row0, int K_) : K(K_) {
+    __device__ __forceinline__ Rows(const Weights& w, int64_t row0, int K_, int end_) : K(K_), end(end_) {
         const int rowb = FMT == kF8 ? K : K / 2;
         kb = FMT == kMx ? K / 32 : FMT == kNv ? K / 16 : (K + kStep - 1) / kStep;
         codes = make_rsrc(w.codes + row0 * rowb, (int64_t)kRows * rowb);
         if (FMT == kF8) tile = static_cast<const float*>(w.scales) + row0 / 128 * kb;
         else scales = make_rsrc(static_cast<const uint8_t*>(w.scales) + row0 * kb, (int64_t)kRows * kb);
     }
-    // Step c of the lane of row r, quarter q; past K: zeros.
+    // Step c of the lane of row r, quarter q; from `end` on: zeros.
     __device__ __forceinline__ Raw<FMT> load(int c, int r, int q) const {
         Raw<FMT> o;
         const int k = c * kStep + 32 * q;
-        const bool in = k < K;
+        const bool in = k < end;
         if (FMT == kF8) {
             o.w[0] = load128(codes, in ? r * K + k : kDropped);
             o.w[FMT == kF8] = load128(codes, in ? r * K + k + 16 : kDropped);
@@ -202,9 +202,9 @@ __device__ __forceinline__ Raw2<FMT> load2(const Rows<FMT>& rows, int c, int r, 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int k = (2 * c + u) * kStep + 32 * q;
-            o.w[u][0] = load128(rows.codes, k < rows.K ? r * (rows.K / 2) + k / 2 : kDropped);
+            o.w[u][0] = load128(rows.codes, k < rows.end ? r * (rows.K / 2) + k / 2 : kDropped);
         }
-        const bool in = 2 * c * kStep < rows.K;  // K is a multiple of 256 here
+        const bool in = 2 * c * kStep < rows.end;  // K is a multiple of 256 here
         if (FMT == kMx) {
             const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(rows.scales, in ? r * rows.kb + 8 * c : kDropped, 0, 0);
             o.s[0][0] = v[0], o.s[1][0] = v[1], o.s[0][1] = o.s[1][1] = 0;
@@ -621,7 +621,7 @@ __global__ __launch_bounds__(kUpWaves * kWave, 4) void k_moe_up(MoeParams p, int
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane % 16, q = lane / 16;
     const int64_t row = (int64_t)e * 2 * p.I + i0;
-    const Rows<FMT> gate(p.w13, row, p.D), up(p.w13, row + p.I, p.D);
+    const Rows<FMT> gate(p.w13, row, p.D, p.D), up(p.w13, row + p.I, p.D, p.D);
     Rsrc rx[PX];
 #pragma unroll
     for (int a = 0; a < PX; ++a) rx[a] = make_rsrc(p.xp + (int64_t)a * p.T * p.D, (int64_t)p.T * p.D * 2);
@@ -702,9 +702,10 @@ __global__ __launch_bounds__(kManyWaves * kWave) void k_moe_many(MoeParams p, fl
     const int row = DOWN ? group * kManyRows + 32 * wave : group * (kManyRows / 2) + 16 * wave;
     const bool any = row < (DOWN ? p.D : p.I);
     const int64_t row0 = any ? (DOWN ? (int64_t)e * p.D + row : (int64_t)e * 2 * p.I + row) : 0;
-    const Rows<FMT> w0(DOWN ? p.w2 : p.w13, row0, K), w1(DOWN ? p.w2 : p.w13, any ? row0 + (DOWN ? 16 : p.I) : 0, K);
     const int stages = (K + S * kStep - 1) / (S * kStep);
     const int c_lo = stages * range / ranges, c_hi = stages * (range + 1) / ranges;
+    const int end = min(K, c_hi * S * kStep);  // the last stage's early loads go no further
+    const Rows<FMT> w0(DOWN ? p.w2 : p.w13, row0, K, end), w1(DOWN ? p.w2 : p.w13, any ? row0 + (DOWN ? 16 : p.I) : 0, K, end);
 
     // Direct load `wave` of a part moves tokens 4 wave .. 4 wave + 3, 256 bytes each.
     const uint16_t* vals = DOWN ? p.h + (int64_t)off * p.I : p.xp;
@@ -717,7 +718,7 @@ __global__ __launch_bounds__(kManyWaves * kWave) void k_moe_many(MoeParams p, fl
 #pragma unroll
         for (int u = 0; u < S; ++u) {
             const int k = (c * S + u) * kStep + 8 * piece;
-            const int at = src >= 0 && k < K ? (src + k) * 2 : kDropped;
+            const int at = src >= 0 && k < end ? (src + k) * 2 : kDropped;
 #pragma unroll
             for (int a = 0; a < P; ++a)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(

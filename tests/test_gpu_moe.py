@@ -195,6 +195,36 @@ def test_an_infinity_stays_with_its_token(fmt):
     assert int(ids.min()) >= 0 and int(ids.max()) < 6
 
 
+def test_mx_scales_over_the_whole_exponent_range():
+    # E8M0 bytes from 2^-127 up to where 6 * 2^(b - 127) is still a binary32 number.  A sum whose
+    # terms reach below 2^-126 is rounded to multiples of 2^-149 at each of them.
+    t, d, i = 3, 64, 96
+    m = Layer(t, d, i, 1, 1, "mxfp4", torch.float32, 8)
+    old = m.w2.scales.cpu().numpy().astype(np.int64)
+    new = np.resize(np.array([0, 1, 2, 60, 127, 200, 245]), d)[:, None] + np.zeros_like(old)
+    m.v2 = m.v2 * 2.0 ** np.repeat(new - old, 32, axis=1)
+    m.w2.scales = dev(new.astype(np.uint8))
+    ids, p, dp = m.routing()
+    y, dy = m.reference(ids, p, dp, True)
+    err = np.abs(m.run().y.double().cpu().numpy() - y)
+    assert np.all(err <= dy + (3 * i + 24) * 2.0 ** -149)
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_a_nan_weight_stays_in_its_row(fmt):
+    m = Layer(5, 64, 96, 4, 2, fmt, torch.bfloat16, 9)
+    clean = m.run()
+    e, row = int(clean.topk_ids[1, 0]), 37
+    if fmt == "fp8":
+        m.w2.codes.view(torch.uint8)[e * 64 + row, 11] = 0x7F
+    else:
+        m.w2.scales[e * 64 + row, 1] = 255 if fmt == "mxfp4" else 0x7F
+    y = m.run().y
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[(clean.topk_ids == e).any(1), row] = True
+    assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], clean.y[~hit])
+
+
 def test_same_bits_again_in_a_graph_and_on_another_stream():
     m = Layer(20, 256, 96, 16, 4, "nvfp4", torch.bfloat16, 7)
     x, wr = m.x.to(DEV), m.wr.to(DEV)
