@@ -21,9 +21,9 @@
 // Kernels:
 //  k_gemm_fp8        a workgroup of 8 waves computes a 256 x 256 tile of C, as
 //                    the FP4 kernels do, one K block of 128 bytes per row (a
-//                    cache line) per stage, through two LDS stages;
+//                    cache line) per stage, through two LDS stages; a bf16 C;
 //  k_gemm_fp8_mid    the same in 128 x 128 or 64 x 64 tiles, for products that the
-//                    large tile leaves the chip idle with;
+//                    large tile leaves the chip idle with, and for a binary32 C;
 //  k_gemm_fp8_few    at most 16 rows of A: one pass over B, 16 rows of B per
 //                    workgroup, K blocks dealt to its waves in turn; bound by the
 //                    read of B, so always on the bf16 form.
@@ -213,10 +213,9 @@ __device__ __forceinline__ void store_tile16(const v4f (&acc)[TB][TA], uint8_t* 
     }
 }
 
-template <bool BROW, bool WIDE>
+template <bool BROW>
 __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
-    typedef Operand<WIDE> Op;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave >> 2, wn = wave & 3;  // 2 x 4 waves of 128 x 64
@@ -272,26 +271,25 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
 #pragma unroll
         for (int j = 0; j < TA; ++j) acc[i][j] = v4f{};
 
-    // Groups of products: NI fragments of B against fragment j of A.  While a
-    // group's products run, the previous group's are scaled into the sums, the next
+    // Groups of products: the fragments of B against fragment j of A.  While a group's
+    // products run, the previous group's are scaled into the sums, the next
     // fragment of A is read and loads of the next stage go out, kEarly per group: early
     // enough to land within the stage, without a burst that fills the load queue.
-    // Where registers allow (kCarry), the last group's products of a stage are
+    // With one scale of B for all (kCarry), the last group's products of a stage are
     // scaled in the next one, while its first operands are on their way from LDS.
-    constexpr int NI = WIDE ? 2 : TB, kPasses = TB / NI, kGroups = kPasses * TA;
-    constexpr bool kCarry = !BROW && !WIDE;
+    constexpr bool kCarry = !BROW;
     constexpr int kEarly = 2;
-    v4f t[2][NI];
+    v4f t[2][TB];
     float f_old = 0.0f, sb_old = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) t[1][i] = v4f{};
+    for (int i = 0; i < TB; ++i) t[1][i] = v4f{};
     const int a_row = wm * WM + lane % kF16;  // within the tile
     const int b_row = wn * WN + lane % kF16;
     const int a_lo = op_offset(a_row, lane, 0), a_hi = op_offset(a_row, lane, 1);
     const int b_lo = BM * kRowStage + op_offset(b_row, lane, 0), b_hi = BM * kRowStage + op_offset(b_row, lane, 1);
-    auto scale_in = [&](int i0, int i, int j, const v4f& d, float f, const v4f& sb) {
+    auto scale_in = [&](int i, int j, const v4f& d, float f, const v4f& sb) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i0 + i][j][e] = fmaf(BROW ? d[e] * sb[e] : d[e], f, acc[i0 + i][j][e]);
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(BROW ? d[e] * sb[e] : d[e], f, acc[i][j][e]);
     };
     if (s_lo < s_hi) {  // K = 0 has no operands to read
 #pragma unroll
@@ -306,59 +304,53 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
         __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
         asm volatile("s_barrier" ::: "memory");
         v8i a_next = read_op(here + a_lo, here + a_hi, 0);
-        float f_next, sb_tile;
+        v8i b[TB];
+        v4f sb[BROW ? TB : 1];
 #pragma unroll
-        for (int g = 0; g < kPasses; ++g) {
-            typename Op::T b[NI];
-            v4f sb[BROW ? NI : 1];
+        for (int i = 0; i < TB; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // the first products wait for as few reads as can be
+            b[i] = read_op(here + b_lo, here + b_hi, i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float f_next = fa[0];
+        const float sb_tile = BROW ? 1.0f : fb[0];
+        if (BROW) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                __builtin_amdgcn_sched_barrier(0);  // the first products wait for as few reads as can be
-                b[i] = Op::of(read_op(here + b_lo, here + b_hi, g * NI + i));
+            for (int i = 0; i < TB; ++i) sb[BROW ? i : 0] = *reinterpret_cast<const v4f*>(fb + i * kF16 + 4 * (lane / kF16));
+        }
+#pragma unroll
+        for (int j = 0; j < TA; ++j) {
+            const v8i a = a_next;
+            const float f = f_next;
+            if (j + 1 < TA) {
+                a_next = read_op(here + a_lo, here + a_hi, j + 1);
+                f_next = fa[(j + 1) * kF16];
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (g == 0) f_next = fa[0], sb_tile = BROW ? 1.0f : fb[0];
+            const float scale = BROW ? f_old : f_old * sb_old;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                if (BROW) sb[i] = *reinterpret_cast<const v4f*>(fb + (g * NI + i) * kF16 + 4 * (lane / kF16));
-            }
-#pragma unroll
-            for (int j = 0; j < TA; ++j) {
-                const int n = g * TA + j;
-                const typename Op::T a = Op::of(a_next);
-                const float f = f_next;
-                if (n + 1 < kGroups) {
-                    a_next = read_op(here + a_lo, here + a_hi, (n + 1) % TA);
-                    f_next = fa[(n + 1) % TA * kF16];
-                }
+            for (int i = 0; i < TB; ++i) {
+                t[j % 2][i] = mma16(b[i], a);
+                if (kCarry || j > 0) scale_in(i, (j + TA - 1) % TA, t[(j + 1) % 2][i], scale, sb[BROW ? i : 0]);
                 __builtin_amdgcn_sched_barrier(0);
-                const float scale = BROW ? f_old : f_old * sb_old;
+                if (i == 0) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    t[n % 2][i] = mma16(b[i], a);
-                    if (kCarry || j > 0)
-                        scale_in(g * NI, i, (j + TA - 1) % TA, t[(n + 1) % 2][i], scale, sb[BROW ? i : 0]);
+                    for (int e = 0; e < kEarly; ++e)
+                        if (j * kEarly + e <= kLoads) issue(s + 1, j * kEarly + e);
                     __builtin_amdgcn_sched_barrier(0);
-                    if (i == 0) {
-#pragma unroll
-                        for (int e = 0; e < kEarly; ++e)
-                            if (n * kEarly + e <= kLoads) issue(s + 1, n * kEarly + e);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
                 }
-                f_old = f;
-                if (j == 0) sb_old = sb_tile;
             }
-            if (!kCarry) {
-                const float scale = BROW ? f_old : f_old * sb_old;
+            f_old = f;
+            if (j == 0) sb_old = sb_tile;
+        }
+        if (!kCarry) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) scale_in(g * NI, i, TA - 1, t[1][i], scale, sb[BROW ? i : 0]);
-            }
+            for (int i = 0; i < TB; ++i) scale_in(i, TA - 1, t[1][i], f_old, sb[BROW ? i : 0]);
         }
     }
     if (kCarry) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) scale_in(0, i, TA - 1, t[1][i], f_old * sb_old, v4f{});
+        for (int i = 0; i < TB; ++i) scale_in(i, TA - 1, t[1][i], f_old * sb_old, v4f{});
     }
     wait_all_barrier();  // LDS is reused below
 
@@ -606,21 +598,24 @@ struct Choice {
 // Costs in microseconds, fitted to measured products (100 x 3584 x 3584 to 14336 x
 // 4096 x 4096): a K block of one workgroup while its CU is shared (`each`, on the 8-bit
 // and on the bf16 cores) and its latency when it is not (`alone`), a workgroup's start and
-// epilogue, and how many share a CU.
+// epilogue, and how many share a CU.  A binary32 C takes the smaller tiles alone: on the
+// bf16 cores the large one gained 4% at best (4096 x 4096 x 14336: 392 us against 407) and
+// lost 10% where K is short (8192 x 8192 x 512: 105 against 95).
 struct TileCost {
     int tile, per_cu;
     double alone, each, each_wide, fixed;
 };
-constexpr TileCost kTileCosts[] = {{256, 1, 1.5, 1.5, 3.7, 6.0}, {128, 2, 0.7, 0.53, 0.95, 4.0}, {64, 4, 0.45, 0.22, 0.30, 3.0}};
+constexpr TileCost kTileCosts[] = {{256, 1, 1.5, 1.5, 0.0, 6.0}, {128, 2, 0.7, 0.53, 0.95, 4.0}, {64, 4, 0.45, 0.22, 0.30, 3.0}};
 constexpr int kCus = 256;
 constexpr int kRanges[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
 
 Choice choose(int64_t M, int64_t N, int64_t K, bool wide) {
     const int64_t S = (K + kBlock - 1) / kBlock;
     const bool may_split = N * 4 < ((int64_t)1 << 23);
-    Choice best{256, 1};
+    Choice best{128, 1};
     double least = 1e300;
     for (const TileCost& c : kTileCosts) {
+        if (wide && c.each_wide == 0.0) continue;
         const int64_t tiles = ((M + c.tile - 1) / c.tile) * ((N + c.tile - 1) / c.tile);
         const double each = wide ? c.each_wide : c.each;
         for (const int sp : kRanges) {
@@ -641,8 +636,8 @@ Choice choose(int64_t M, int64_t N, int64_t K, bool wide) {
 
 template <bool BROW, bool WIDE>
 void launch_tile(const F8Params& p, int tile, unsigned groups, hipStream_t stream) {
-    if (tile == 256)
-        FP4Q_LAUNCH((k_gemm_fp8<BROW, WIDE>), dim3(groups), dim3(kThreads), 0, stream, p);
+    if (!WIDE && tile == 256)
+        FP4Q_LAUNCH(k_gemm_fp8<BROW>, dim3(groups), dim3(kThreads), 0, stream, p);
     else if (tile == 128)
         FP4Q_LAUNCH((k_gemm_fp8_mid<128, BROW, WIDE>), dim3(groups), dim3(256), MidPlan<128>::kLds, stream, p);
     else
