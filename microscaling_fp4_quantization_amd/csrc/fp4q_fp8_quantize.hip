@@ -17,7 +17,10 @@
 // the 16 threads of a row group; column maxima cross the workgroup through LDS.
 //
 // Memory-bound: 2 or 4 bytes in and 1 or 2 out per element, against about 8
-// vector instructions (12 with both outputs).
+// vector instructions (12 with both outputs).  Measured: 8192 x 3584 bf16, row
+// scales, both outputs, 119 MB in 22.8 us (5.2 TB/s, where a large copy reached 4.7);
+// 4861 x 5000 binary32, tile scales, both, 146 MB in 28 us (5.2 TB/s); 7 x 896 in
+// 5.1 us, the time of any launch that waits for memory twice.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stdio.h>

@@ -26,6 +26,13 @@
 // as a sum of bf16 parts, each the rounding of what the ones before it leave: 3 for
 // binary32 x (24 bits, all of it); h as 2 parts (16 bits: rounding it to one would
 // add an error as large as a bf16 output's own) or 3 for a binary32 output.
+//
+// Measured: 64 tokens, 64 experts of 4096 x 1024 in E4M3 (805 MB) 190 us, its two
+// products at 4.7 TB/s; 11 tokens, 8 experts of 4096 x 14336 in NVFP4 (793 MB) 198 us;
+// one token on 8 of 64 experts of 4096 x 1024 in MXFP4 (53 MB) 31 us, of which the
+// products 12.5 and 7.3, router 7.7 and combine 4.4: four launches of work too short to
+// fill memory.  (The combine inside the down kernel, by the last workgroup of each 128
+// rows, saved the launch but took 37 us: each workgroup's release writes back its L2.)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
