@@ -374,10 +374,14 @@ def gemm_workspace(device, nbytes: int) -> torch.Tensor:
     and current stream and grown on demand (calls on one stream are ordered, so
     they can share it)."""
     dev = torch.device(device)
-    key = (dev.index, _raw_stream(dev))
+    return _stream_workspace(dev, _raw_stream(dev), nbytes)
+
+
+def _stream_workspace(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor:
+    key = (dev.index, stream)
     ws = _gemm_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
         _gemm_workspaces[key] = ws
     return ws
 

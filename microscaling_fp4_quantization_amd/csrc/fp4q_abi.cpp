@@ -569,8 +569,9 @@ fp4q_status fp8_linear_forward(const void* x, int32_t xt, const void* w, int32_t
     const LinearForward f(ws, tokens, in, out, xt);
     TRY(linear_buffer(fn, "a workspace", ws, ws_bytes, f.bytes));
     char msg[256] = {0};
-    TRY(launched(fp4q::launch_fp8_quantize({x, xt, tokens, in, false, f.x.codes, f.x.scales, s.xt.codes, s.xt.scales, stream}, msg, sizeof msg), msg));
-    TRY(launched(fp4q::launch_fp8_quantize({w, wt, out, in, true, f.w.codes, f.w.scales, s.wt.codes, s.wt.scales, stream}, msg, sizeof msg), msg));
+    TRY(launched(fp4q::launch_fp8_quantize_two({x, xt, tokens, in, false, f.x.codes, f.x.scales, s.xt.codes, s.xt.scales, stream},
+                                               {w, wt, out, in, true, f.w.codes, f.w.scales, s.wt.codes, s.wt.scales, stream},
+                                               msg, sizeof msg), msg));
     return launched(fp4q::launch_fp8_gemm({f.x.codes, f.x.scales, f.w.codes, f.w.scales, false, tokens, out, up16(in), y, xt, f.product, stream}, msg, sizeof msg), msg);
 }
 

@@ -210,6 +210,8 @@ int launch_rotate(const RotateJob& j, char* msg, size_t msg_len);
 int launch_gemm(const GemmJob& j, char* msg, size_t msg_len);
 int launch_gemm_nvfp4(const GemmNvJob& j, char* msg, size_t msg_len);
 int launch_fp8_quantize(const Fp8QuantJob& j, char* msg, size_t msg_len);
+// x under row scales and w under tile scales: one launch where both outputs of both are wanted.
+int launch_fp8_quantize_two(const Fp8QuantJob& x, const Fp8QuantJob& w, char* msg, size_t msg_len);
 int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len);
 int launch_moe(const MoeJob& j, char* msg, size_t msg_len);
 

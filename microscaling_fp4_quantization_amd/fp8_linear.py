@@ -15,16 +15,26 @@ took it half as long again.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
-from . import _check, _dtype_code, _raw_stream, gemm_workspace, lib
+from . import _check, _dtype_code, _raw_stream, _stream_workspace, lib
+
+
+@functools.lru_cache(maxsize=4096)
+def _sizes(tokens, k, out, xt, wt, want_dx, want_dw):
+    """Bytes of (what the forward call saves, either call's workspace)."""
+    l = lib()
+    return (l.fp8_linear_saved_bytes(tokens, k, out, want_dx, want_dw),
+            l.fp8_linear_workspace_bytes(tokens, k, out, xt, wt))
 
 
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
         want_dx, want_dw = ctx.needs_input_grad
-        l, dev = lib(), x.device
+        dev = x.device
         out, k = w.shape
         shape = x.shape
         if x.dim() != 2:
@@ -36,39 +46,38 @@ class _Fp8Linear(torch.autograd.Function):
         tokens = x.shape[0]
         xt, wt = _dtype_code(x), _dtype_code(w)
         y = x.new_empty((tokens, out))
-        n = l.fp8_linear_saved_bytes(tokens, k, out, want_dx, want_dw)
+        n, need = _sizes(tokens, k, out, xt, wt, want_dx, want_dw)
         saved = x.new_empty(n, dtype=torch.uint8) if n else None
-        ws = gemm_workspace(dev, l.fp8_linear_workspace_bytes(tokens, k, out, xt, wt))
-        rc = l.fp8_linear_forward(x.data_ptr(), xt, w.data_ptr(), wt, tokens, k, out, y.data_ptr(), want_dx, want_dw,
-                                  None if saved is None else saved.data_ptr(), n, ws.data_ptr(), ws.numel(),
-                                  _raw_stream(dev))
+        stream = _raw_stream(dev)
+        ws = _stream_workspace(dev, stream, need)
+        rc = lib().fp8_linear_forward(x.data_ptr(), xt, w.data_ptr(), wt, tokens, k, out, y.data_ptr(), want_dx, want_dw,
+                                      None if saved is None else saved.data_ptr(), n, ws.data_ptr(), ws.numel(), stream)
         if rc:
             _check(rc)
         if want_dx or want_dw:
             ctx.save_for_backward(saved)
-            ctx.sizes = shape, tokens, k, out, x.dtype, w.dtype
+            ctx.sizes = shape, tokens, k, out, xt, wt, w.dtype, need
         return y if len(shape) == 2 else y.view(*shape[:-1], out)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         want_dx, want_dw = ctx.needs_input_grad
-        shape, tokens, k, out, x_dtype, w_dtype = ctx.sizes
+        shape, tokens, k, out, xt, wt, w_dtype, need = ctx.sizes
         saved, = ctx.saved_tensors
-        l, dev = lib(), dy.device
+        dev = dy.device
         if not dy.is_contiguous():
             dy = dy.contiguous()
-        xt = _dtype_code(dy)
-        wt = xt if w_dtype == x_dtype else 1 - xt
         dx = dy.new_empty(shape) if want_dx else None
         dw = dy.new_empty((out, k), dtype=w_dtype) if want_dw else None
-        ws = gemm_workspace(dev, l.fp8_linear_workspace_bytes(tokens, k, out, xt, wt))
+        stream = _raw_stream(dev)
+        ws = _stream_workspace(dev, stream, need)
         # An empty gradient has no address of its own: any aligned one stands for it.
-        rc = l.fp8_linear_backward(dy.data_ptr(), xt, wt, tokens, k, out,
-                                   (dx.data_ptr() or ws.data_ptr()) if want_dx else None,
-                                   (dw.data_ptr() or ws.data_ptr()) if want_dw else None,
-                                   None if saved is None else saved.data_ptr(), 0 if saved is None else saved.numel(),
-                                   ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        rc = lib().fp8_linear_backward(dy.data_ptr(), xt, wt, tokens, k, out,
+                                       (dx.data_ptr() or ws.data_ptr()) if want_dx else None,
+                                       (dw.data_ptr() or ws.data_ptr()) if want_dw else None,
+                                       None if saved is None else saved.data_ptr(), 0 if saved is None else saved.numel(),
+                                       ws.data_ptr(), ws.numel(), stream)
         if rc:
             _check(rc)
         return dx, dw
