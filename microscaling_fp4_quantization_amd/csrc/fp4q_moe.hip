@@ -834,10 +834,16 @@ void launch_products(const MoeParams& p, float* z, bool x32, int parts_h, hipStr
     const int up_groups = (2 * p.I + kManyRows - 1) / kManyRows, down_groups = (p.D + kManyRows - 1) / kManyRows;
     const dim3 block(kManyWaves * kWave);
     // Which form of gate and up: 128 rows per workgroup where that makes enough
-    // workgroups.  Measured (us, 128 rows / 16 rows): 128 workgroups (one token, 8 experts
-    // of 4096 x 1024) 25 / 13, 256 (two tokens) 27 / 22, 448 (one token, 2 of 4096 x 14336)
-    // 34 / 36, 512 (four tokens, NVFP4 2048 x 1024) 20 / 27, 3072 (64 tokens, E4M3) 114 / 157.
-    if (slots * up_groups >= 384) {
+    // workgroups, fewer of them where slots are at least half full, since 16 rows per
+    // workgroup fetch a slot's values eight times as often.  Measured (us, 128 rows / 16
+    // rows; the product alone, and the whole layer where said): 128 workgroups (one token, 8
+    // experts of 4096 x 1024) 25 / 13, 256 (two tokens) 27 / 22, 448 (one token, 2 of 4096 x
+    // 14336) 34 / 36, 512 (four tokens, NVFP4 2048 x 1024) 20 / 27, 3072 (64 tokens, E4M3)
+    // 114 / 157; layers with half-full slots: 174 workgroups (29 tokens, 15 of 864 x 352)
+    // 27.6 / 26.2, 238 (49 tokens, 5 of 1920 x 896, binary32) 50 / 55, 256 (64 tokens, 8 of
+    // 2048 x 1024) 34 / 36, binary32 42 / 49.
+    const bool full = p.T * p.k >= 8 * slots;
+    if (slots * up_groups >= (full ? 224 : 384)) {
         const dim3 grid((unsigned)(slots * up_groups));
         if (x32) FP4Q_LAUNCH((k_moe_many<FMT, 3, false>), grid, block, 0, stream, p, z, 1, parts_h);
         else FP4Q_LAUNCH((k_moe_many<FMT, 1, false>), grid, block, 0, stream, p, z, 1, parts_h);
@@ -853,10 +859,16 @@ void launch_products(const MoeParams& p, float* z, bool x32, int parts_h, hipStr
     FP4Q_LAUNCH(k_moe_combine, dim3((unsigned)((p.T * (p.D / 4) + 63) / 64)), dim3(256), 0, stream, p, (const float*)z, ranges);
 }
 
-// Ranges of K for the router: two steps of 32 per wave keep its loads in flight
-// together, and 8 ranges are as many partial sums as are worth adding.
-int route_ranges(int64_t D) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRanges, D / 32 / (2 * kRouteWaves)));
+// Ranges of K for the router: as many as make 64 workgroups, with no less than half a step of
+// 32 per wave; 32 where over 128 experts make the last workgroup add one range after the
+// other.  Measured (us, so / with two steps per wave whatever the tiles): 49 tokens,
+// 5 experts of 1920, binary32, 10.9 / 17.6 (32 workgroups / 4); one token, 64 of 4096, 7.7 /
+// 8.3 (32 / 16); 64 tokens, 64 of 4096, 11.0 (64); 64 tokens, 500 of 4096, binary32,
+// 46.9 / 54.2 (128 / 512); 16 tokens, 200 of 2048, 15.8 (26; 17.3 with 52).
+int route_ranges(int64_t T, int64_t D, int64_t E) {
+    const int64_t tiles = (E + 15) / 16 * ((T + 15) / 16), steps = D / 32;
+    const int64_t most = std::min<int64_t>(kMaxRanges, (2 * steps + kRouteWaves - 1) / kRouteWaves);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(most, (E <= 128 ? 64 : 32) / tiles));
 }
 
 constexpr size_t kCountBytes = 256;
@@ -874,7 +886,7 @@ void launch_route(const MoeParams& p, hipStream_t stream) {
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t I, int64_t E, int64_t k) {
-    const size_t logits = up256((size_t)(route_ranges(D) * T * E * 4)), parts = up256((size_t)(3 * T * D * 2));
+    const size_t logits = up256((size_t)(route_ranges(T, D, E) * T * E * 4)), parts = up256((size_t)(3 * T * D * 2));
     const size_t h = up256((size_t)(3 * T * k * I * 2)), z = (size_t)(down_ranges(T, D, I, E, k) * T * k * D * 4);
     return kCountBytes + kPlanBytes + logits + parts + h + z;
 }
@@ -894,7 +906,7 @@ int launch_moe(const MoeJob& j, char* msg, size_t msg_len) {
     p.wts = j.wts;
     p.y = j.y;
     p.yt = j.yt;
-    p.ranges = route_ranges(j.D);
+    p.ranges = route_ranges(j.T, j.D, j.E);
     p.count = reinterpret_cast<uint32_t*>(ws);
     p.plan = reinterpret_cast<Plan*>(ws += kCountBytes);
     p.logits = reinterpret_cast<float*>(ws += kPlanBytes);
