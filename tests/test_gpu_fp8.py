@@ -340,6 +340,25 @@ def test_gemm_writes_where_rows_do_not_start_on_16_bytes(m, n):
     assert not flat[:3].any() and not flat[3 + m * n:].any()
 
 
+@pytest.mark.parametrize("kind", [ROW, TILE])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n", [(5, 131), (40, 131), (300, 1033), (2304, 3601), (2305, 3606)])
+def test_gemm_of_odd_rows_is_that_of_whole_ones(m, n, dtype, kind):
+    """One K block, so that every tile size forms the same sums: C with rows that end inside 16 bytes equals the
+    columns of a wider one, and nothing around it is written."""
+    k, wide = 128, (n + 127) // 128 * 128
+    a, b = operand(m, k, 18, False), operand(n, k, 19, kind == TILE)
+    f8 = lambda c: dev(c).view(torch.float8_e4m3fn)
+    more = np.zeros((wide - n, b[0].shape[1]), np.uint8)
+    scales = b[1] if kind == TILE else np.concatenate([b[1], np.ones((1, wide - n), np.float32)], 1)
+    want = fq.fp8_gemm_b128(f8(a[0]), dev(a[1]), f8(np.concatenate([b[0], more])), dev(scales), kind, out_dtype=dtype)
+    flat = torch.zeros(m * n + 32, dtype=dtype, device=DEV)
+    out = flat[16:16 + m * n].view(m, n)
+    fq.fp8_gemm_b128(f8(a[0]), dev(a[1]), f8(b[0]), dev(b[1]), kind, out=out)
+    assert torch.equal(out, want[:, :n])
+    assert not flat[:16].any() and not flat[16 + m * n:].any()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("t,n,k", [(5, 40, 33), (200, 300, 260), (70, 1000, 4100)])
 def test_linear_is_the_calls_that_it_stands_for(t, n, k, dtype):
