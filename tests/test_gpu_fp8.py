@@ -380,3 +380,29 @@ def test_linear_of_mixed_types():
     y = fq.fp8_linear(x, w)
     y.sum().backward()
     assert y.dtype == x.grad.dtype == torch.bfloat16 and w.grad.dtype == torch.float32
+
+
+def test_quantize_past_32_bits():
+    """Elements and codes beyond 2^31: the last rows are those of the rows alone."""
+    rows, cols = 270001, 8000
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    tail = torch.randn(257, cols, dtype=torch.bfloat16, device=DEV)
+    x[-257:] = tail
+    q, want = fq.fp8_quantize_b128(x), fq.fp8_quantize_b128(tail)
+    assert torch.equal(q.codes[-257:].view(torch.uint8), want.codes.view(torch.uint8))
+    assert torch.equal(q.scales[:, -257:], want.scales)
+
+
+@pytest.mark.parametrize("m", [2, 40])
+def test_gemm_past_32_bits(m):
+    """B beyond 2^31 bytes, sums exact on whole numbers: the last columns are those of B's last rows alone."""
+    n, k = 262400, 8320
+    g = torch.Generator(device=DEV).manual_seed(3)
+    small = lambda r: torch.randint(-2, 3, (r, k), generator=g, device=DEV).to(torch.float8_e4m3fn)
+    a, tail = small(m), small(256)
+    b = torch.zeros(n, k, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    b[-256:].view(torch.uint8).copy_(tail.view(torch.uint8))
+    one = lambda *shape: torch.ones(*shape, device=DEV)
+    got = fq.fp8_gemm_b128(a, one(k // 128, m), b, one(n // 128, k // 128))
+    want = a.double() @ tail.double().T
+    assert torch.equal(got[:, -256:].double(), want) and not got[:, :-256].any()

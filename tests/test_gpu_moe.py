@@ -285,3 +285,24 @@ def test_no_tokens_and_refusals():
         call(w13=fq.ExpertWeights(fq.FMT_MXFP4, m.w13.codes, m.w13.scales, torch.ones(1, device=DEV)))
     with pytest.raises(fq.Fp4qError, match="workspace"):
         call(ws=torch.zeros(256, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_weights_past_32_bits(fmt):
+    """Stacked weights of over 2^31 bytes: the last expert gives what it gives alone."""
+    d, i = 4096, 2048
+    m = Layer(3, d, i, 1, 1, fmt, torch.bfloat16, 10)
+    per = m.w13.codes.numel()
+    e = (1 << 31) // per + 2
+    def stack(w):
+        codes = torch.zeros(e * w.codes.shape[0], w.codes.shape[1], dtype=torch.uint8, device=DEV)
+        codes[-w.codes.shape[0]:] = w.codes.view(torch.uint8)
+        scales = w.scales.new_zeros(e * w.scales.shape[0], w.scales.shape[1])
+        scales[-w.scales.shape[0]:] = w.scales
+        return fq.ExpertWeights(w.fmt, codes.view(w.codes.dtype), scales, w.g)
+    ids = torch.full((3, 1), e - 1, dtype=torch.int32, device=DEV)
+    wts = torch.ones(3, 1, device=DEV)
+    got = fq.moe_layer(m.x.to(DEV), stack(m.w13), stack(m.w2), e, 1, topk_ids=ids, topk_weights=wts).y
+    ids0 = torch.zeros_like(ids)
+    want = fq.moe_layer(m.x.to(DEV), m.w13, m.w2, 1, 1, topk_ids=ids0, topk_weights=wts).y
+    assert (got.float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max() and got.any()
