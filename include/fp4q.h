@@ -536,7 +536,9 @@ typedef struct {
  *   y, yt       device out, tokens x dim
  *   ws          moe_layer_workspace_bytes() bytes, 256-byte aligned, its first 256
  *               bytes zero before the first call; calls leave them zero.  Calls
- *               that overlap need distinct workspaces.
+ *               that overlap need distinct workspaces: on two streams, from two
+ *               host threads (whose launches may mix on one stream), or in a graph
+ *               whose replay may overlap a call.
  * Activations meet the weights' exact values; sums are binary32.  Binary32 x goes
  * through whole; h = silu(G x) * (U x) is held to 16 bits (24 for a binary32 y).
  * Against the exact layer y differs by rounding of order 2^-16 (binary32 y: that of

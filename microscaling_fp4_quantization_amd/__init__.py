@@ -584,19 +584,27 @@ def _expert_weights(w: ExpertWeights, rows: int, k: int, what: str, device) -> _
     return _ExpertWeightsC(codes.data_ptr(), scales.data_ptr(), g.data_ptr(), g.numel())
 
 
-_moe_workspaces = {}
+def _capturing(dev: torch.device) -> bool:
+    """Whether torch's current stream on `dev` is being captured into a graph."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(dev):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def moe_workspace(device, nbytes: int) -> torch.Tensor:
-    """A workspace of at least `nbytes` for moe_layer, zero where it has to be, kept
-    per device and current stream and grown on demand."""
-    dev = device if isinstance(device, torch.device) else torch.device(device)
-    key = (dev.index, _raw_stream(dev))
-    ws = _moe_workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _moe_workspaces[key] = ws
+    """A new workspace of `nbytes` for moe_layer, zero where it has to be before the
+    first call (the fill is on torch's current stream)."""
+    ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
     return ws
+
+
+# Workspaces of moe_layer that no call is issuing launches through, by device and stream.
+# Their first 256 bytes are zero once the stream has got there.  A call takes one out while
+# it launches, so that calls from several threads, whose launches may mix, have one each;
+# list.pop and list.append are atomic.
+_moe_free = {}
 
 
 def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: int, top_k: int, *,
@@ -610,7 +618,9 @@ def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: i
     ``w13``: (experts * 2 * inter) x dim, gate rows then up rows per expert; ``w2``:
     (experts * dim) x inter.  ``router``: experts x dim; or None, with the routing in
     ``topk_ids`` (int32) and ``topk_weights`` (float32), tokens x top_k.  y has x's
-    dtype unless ``out_dtype`` or ``out`` says otherwise."""
+    dtype unless ``out_dtype`` or ``out`` says otherwise.  ``ws``: a moe_workspace that
+    no other call uses at the same time; a captured call without one gets its own, and
+    clears its counter at each replay."""
     x = _matrix(x)
     tokens, dim = x.shape
     if w13.fmt != w2.fmt:
@@ -641,16 +651,31 @@ def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: i
     elif out.shape != (tokens, dim) or not out.is_contiguous() or out.device != x.device:
         raise ValueError(f"out must be contiguous, {tokens} x {dim}, on x's device")
     l = lib()
+    stream = _raw_stream(x.device)
+    free = None
     if ws is None:
         need = l.moe_layer_workspace_bytes(tokens, dim, inter, experts, top_k)
-        ws = moe_workspace(x.device, need) if need else None
+        if need and _capturing(x.device):
+            # The graph's own, its counter cleared at each replay: a fill in a capture is only
+            # recorded, and a graph keeps its buffer's address whatever eager calls do later.
+            ws = moe_workspace(x.device, need)
+        elif need:
+            free = _moe_free.setdefault((x.device.index, stream), [])
+            try:
+                ws = free.pop()
+            except IndexError:
+                pass
+            if ws is None or ws.numel() < need:
+                ws = moe_workspace(x.device, need)
     rc = l.moe_layer(x.data_ptr(), _dtype_code(x), tokens, dim, inter, experts, top_k, w13.fmt, ctypes.byref(a),
                      ctypes.byref(b), None if router is None else router.data_ptr(),
                      0 if router is None else _dtype_code(router), int(renormalize), topk_ids.data_ptr(),
                      topk_weights.data_ptr(), out.data_ptr(), _dtype_code(out), None if ws is None else ws.data_ptr(),
-                     0 if ws is None else ws.numel(), _raw_stream(x.device))
+                     0 if ws is None else ws.numel(), stream)
     if rc:
         _check(rc)
+    if free is not None:
+        free.append(ws)
     return MoeOutput(out, topk_ids, topk_weights)
 
 

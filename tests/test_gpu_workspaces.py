@@ -1,0 +1,99 @@
+"""Calls without a workspace of the caller's: in graphs, beside each other and from
+several threads, each gives the bits that it gives alone."""
+import threading
+
+import pytest
+import torch
+
+import microscaling_fp4_quantization_amd as fq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def moe_case(tokens, dim, inter, experts, top_k, seed):
+    """A layer in 8 bits and a call of it."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda r, c: torch.randn(r, c, generator=g, device=DEV) * c ** -0.5
+    q = lambda w: fq.fp8_quantize_b128(w, fq.B128_TILE)
+    w13, w2 = q(rnd(experts * 2 * inter, dim)), q(rnd(experts * dim, inter))
+    w13, w2 = (fq.ExpertWeights(fq.FMT_E4M3_B128, w.codes, w.scales) for w in (w13, w2))
+    router, x = rnd(experts, dim) * 4, rnd(tokens, dim) * dim ** 0.5
+    return lambda **kw: fq.moe_layer(x, w13, w2, experts, top_k, router=router, **kw)
+
+
+def test_graphs_of_several_sizes_on_a_stream_that_nothing_warmed_up():
+    """Captured largest first, replayed smallest first, before anything else ran on their stream."""
+    cases = [moe_case(t, 256, 96, 16, 4, t) for t in (40, 9, 1)]
+    want = [c().y for c in cases]
+    outs = [torch.zeros_like(w) for w in want]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs = []
+    for case, out in zip(cases, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            case(out=out)
+    for _ in range(3):
+        for i in (2, 1, 0, 1):
+            outs[i].zero_()
+            graphs[i].replay()
+            cases[i]()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], want[i])
+    with torch.cuda.stream(side):  # an eager call on the stream that captured
+        assert torch.equal(cases[1]().y, want[1])
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[1], want[1])
+
+
+def test_a_graph_outlives_a_larger_call_on_its_stream():
+    small, large = moe_case(3, 256, 96, 16, 4, 1), moe_case(64, 2048, 512, 16, 4, 2)
+    want, want_large = small().y, large().y
+    out = torch.zeros_like(want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        small()
+        graph = torch.cuda.CUDAGraph()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            small(out=out)
+        large()
+        held = [torch.full((1 << 20,), 0x55, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            assert torch.equal(large().y, want_large)
+            assert torch.equal(out, want)
+    assert all(bool((h == 0x55).all()) for h in held)
+
+
+def test_experts_from_two_threads_on_one_stream():
+    cases = [moe_case(t, 512, 128, 32, 4, 10 + t) for t in (1, 24)]
+    want = [c().y for c in cases]
+    torch.cuda.synchronize()
+    run_threads([(lambda c=c: c().y) for c in cases], want)
+
+
+def run_threads(calls, want, rounds=200):
+    """Each call over and over from a thread of its own, all on the current stream."""
+    stream, bad = torch.cuda.current_stream(), []
+    start = threading.Barrier(len(calls))
+
+    def work(i):
+        try:
+            with torch.cuda.stream(stream):
+                start.wait()
+                got = [calls[i]() for _ in range(rounds)]
+                bad.extend(i for g in got if not torch.equal(g, want[i]))
+        except Exception as e:  # noqa: BLE001 (told to the main thread)
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:3]
