@@ -366,24 +366,12 @@ def fp4_quantize_search(x: torch.Tensor, fmt: int = FMT_UE4M3, block: int = 16,
     return Quantized(codes, scales, block_mse, stats, g)
 
 
-_gemm_workspaces = {}
-
-
 def gemm_workspace(device, nbytes: int) -> torch.Tensor:
-    """A device workspace of at least `nbytes` for the GEMMs, kept per device
-    and current stream and grown on demand (calls on one stream are ordered, so
-    they can share it)."""
-    dev = torch.device(device)
-    return _stream_workspace(dev, _raw_stream(dev), nbytes)
-
-
-def _stream_workspace(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor:
-    key = (dev.index, stream)
-    ws = _gemm_workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
-        _gemm_workspaces[key] = ws
-    return ws
+    """A new device workspace of `nbytes` (at least 256, so that it has an address) for the
+    GEMMs and the linear layer.  Calls without one of the caller's take theirs here: torch's
+    allocator hands a freed one to the next call on its stream, never to a call whose launches
+    may mix with this one's, and a captured call's stays its graph's."""
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def fp4_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor,

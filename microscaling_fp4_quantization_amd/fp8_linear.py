@@ -19,7 +19,7 @@ import functools
 
 import torch
 
-from . import _check, _dtype_code, _raw_stream, _stream_workspace, lib
+from . import _check, _dtype_code, _raw_stream, gemm_workspace, lib
 
 
 @functools.lru_cache(maxsize=4096)
@@ -49,7 +49,7 @@ class _Fp8Linear(torch.autograd.Function):
         n, need = _sizes(tokens, k, out, xt, wt, want_dx, want_dw)
         saved = x.new_empty(n, dtype=torch.uint8) if n else None
         stream = _raw_stream(dev)
-        ws = _stream_workspace(dev, stream, need)
+        ws = gemm_workspace(dev, need)
         rc = lib().fp8_linear_forward(x.data_ptr(), xt, w.data_ptr(), wt, tokens, k, out, y.data_ptr(), want_dx, want_dw,
                                       None if saved is None else saved.data_ptr(), n, ws.data_ptr(), ws.numel(), stream)
         if rc:
@@ -71,7 +71,7 @@ class _Fp8Linear(torch.autograd.Function):
         dx = dy.new_empty(shape) if want_dx else None
         dw = dy.new_empty((out, k), dtype=w_dtype) if want_dw else None
         stream = _raw_stream(dev)
-        ws = _stream_workspace(dev, stream, need)
+        ws = gemm_workspace(dev, need)
         # An empty gradient has no address of its own: any aligned one stands for it.
         rc = lib().fp8_linear_backward(dy.data_ptr(), xt, wt, tokens, k, out,
                                        (dx.data_ptr() or ws.data_ptr()) if want_dx else None,

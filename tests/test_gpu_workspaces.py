@@ -77,6 +77,72 @@ def test_experts_from_two_threads_on_one_stream():
     run_threads([(lambda c=c: c().y) for c in cases], want)
 
 
+def linear_case(tokens, n, k, seed):
+    """A training step of a layer: y, dx and dw in one tensor."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    x, w, dy = rnd(tokens, k), rnd(n, k), rnd(tokens, n)
+
+    def call():
+        a, b = x.detach().requires_grad_(), w.detach().requires_grad_()
+        y = fq.fp8_linear(a, b)
+        return torch.cat([t.flatten() for t in (y.detach(), *torch.autograd.grad(y, (a, b), dy))])
+
+    return call
+
+
+def gemm_cases():
+    """Products that split K, so that they need a workspace: 8-bit, MXFP4 and NVFP4."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    rnd = lambda m, k: torch.randn(m, k, generator=g, device=DEV)
+    a, b = rnd(100, 8192), rnd(256, 8192)
+    qa, qb = fq.fp8_quantize_b128(a), fq.fp8_quantize_b128(b, fq.B128_TILE)
+    ma, mb = fq.mxfp4_quantize(a), fq.mxfp4_quantize(b)
+    na, nb = fq.nvfp4_quantize(a), fq.nvfp4_quantize(b)
+    assert fq.lib().fp8_gemm_b128_workspace_bytes(100, 256, 8192, fq.F32) > 0
+    assert fq.lib().fp4_gemm_workspace_bytes(100, 256, 8192) > 0
+    assert fq.lib().fp4_gemm_nvfp4_workspace_bytes(100, 256, 8192) > 0
+    return [lambda: fq.fp8_gemm_b128(qa.codes, qa.scales, qb.codes, qb.scales),
+            lambda: fq.fp4_gemm_mxfp4(ma.codes, ma.scales, mb.codes, mb.scales),
+            lambda: fq.fp4_gemm_nvfp4(na.codes, na.scales, na.g, nb.codes, nb.scales, nb.g)]
+
+
+def test_linear_layers_from_two_threads_on_one_stream():
+    cases = [linear_case(70, 1000, 600, 3), linear_case(300, 200, 500, 4)]
+    want = [c() for c in cases]
+    torch.cuda.synchronize()
+    run_threads(cases, want, 100)
+
+
+def test_products_from_three_threads_on_one_stream():
+    cases = gemm_cases()
+    want = [c() for c in cases]
+    torch.cuda.synchronize()
+    run_threads(cases, want)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_a_captured_product_outlives_a_larger_one(which):
+    case, step = gemm_cases()[which], linear_case(4096, 1024, 4096, 6)
+    want = case()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        case()
+        graph = torch.cuda.CUDAGraph()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            out = case()
+        step()
+        held = [torch.full((1 << 20,), 0x55, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            step()
+            assert torch.equal(out, want)
+    assert all(bool((h == 0x55).all()) for h in held)
+
+
 def run_threads(calls, want, rounds=200):
     """Each call over and over from a thread of its own, all on the current stream."""
     stream, bad = torch.cuda.current_stream(), []
