@@ -18,6 +18,7 @@ Layouts (row-major, blocks of b consecutive elements along a row):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -160,24 +161,26 @@ def _matrix(x: torch.Tensor, what: str = "x") -> torch.Tensor:
     return x
 
 
-_workspaces = {}
-
-
 def workspace_bytes(rows: int = 0, cols: int = 0, block: int = 32) -> int:
     return int(lib().fp4q_workspace_bytes(rows, cols, block))
 
 
 def workspace(device) -> torch.Tensor:
-    """A zero-filled workspace for `device` and torch's current stream on it.
-    Calls made on one stream share it (stream order keeps them apart); calls
-    made on another stream get a workspace of their own."""
-    dev = torch.device(device)
-    key = (dev.index, _raw_stream(dev))
-    ws = _workspaces.get(key)
-    if ws is None:
-        ws = torch.zeros(workspace_bytes(), dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
-    return ws
+    """A zero-filled workspace for `device` (calls take any contents).  One serves any
+    number of calls in stream order, issued by one thread."""
+    return torch.zeros(workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+@functools.lru_cache(maxsize=None)
+def _workspace_size() -> int:
+    return workspace_bytes()
+
+
+def _scratch(x: torch.Tensor) -> torch.Tensor:
+    """The workspace of a call without one of the caller's: from torch's allocator, so that
+    it is no other call's whose launches may mix with this one's, and a captured call's
+    stays its graph's."""
+    return x.new_empty(_workspace_size(), dtype=torch.uint8)
 
 
 def new_stats(device) -> torch.Tensor:
@@ -229,7 +232,7 @@ def mxfp4_quantize(x: torch.Tensor, rotate: int = 0, *, codes=None, scales=None,
     """
     x = _matrix(x)
     codes, scales, block_mse, stats = _outputs(x, 32, codes, scales, block_mse, stats)
-    ws = ws if ws is not None else (workspace(x.device) if stats is not None else None)
+    ws = ws if ws is not None else (_scratch(x) if stats is not None else None)
     _check(lib().mxfp4_quantize(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], rotate,
                                 _ptr(codes), _ptr(scales), _ptr(block_mse), mse_kind,
                                 _ptr(stats), _ptr(ws), 0 if ws is None else ws.numel(),
@@ -252,7 +255,7 @@ def nvfp4_quantize(x: torch.Tensor, block: int = 16, scale_fmt: int = FMT_UE4M3,
     if gmode != G_NONE and g is None:
         g = torch.empty(x.shape[0] if gmode == G_ROW else 1, dtype=torch.float32, device=x.device)
     need_ws = stats is not None or gmode == G_DYNAMIC
-    ws = ws if ws is not None else (workspace(x.device) if need_ws else None)
+    ws = ws if ws is not None else (_scratch(x) if need_ws else None)
     _check(lib().nvfp4_quantize(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], block,
                                 scale_fmt, gmode, _ptr(g), rotate, _ptr(codes), _ptr(scales),
                                 _ptr(block_mse), mse_kind, _ptr(stats), _ptr(ws),
@@ -294,7 +297,7 @@ def fp4_quantize_mx_nv(x: torch.Tensor, nv_block: int = 16, *, mse_kind: int = M
                  nv.get("stats", stats))
     if g is None:
         g = torch.empty(1, dtype=torch.float32, device=x.device)
-    ws = ws if ws is not None else workspace(x.device)
+    ws = ws if ws is not None else _scratch(x)
     _check(lib().fp4_quantize_mx_nv(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1],
                                     _ptr(m[0]), _ptr(m[1]), _ptr(m[2]), _ptr(m[3]), nv_block, _ptr(g),
                                     _ptr(v[0]), _ptr(v[1]), _ptr(v[2]), _ptr(v[3]), mse_kind,
@@ -339,7 +342,7 @@ def fp4_quantize_mx_nv_batch(xs, nv_block: int = 16, *, mse_kind: int = MSE_ABS,
         arr[i] = MxNvTensor(ptr(x), x.shape[0], x.shape[1], ptr(m[0]), ptr(m[1]), ptr(m[2]), ptr(m[3]),
                             ptr(g), ptr(v[0]), ptr(v[1]), ptr(v[2]), ptr(v[3]))
         res.append((Quantized(*m, None), Quantized(*v, g)))
-    ws = ws if ws is not None else workspace(xs[0].device)
+    ws = ws if ws is not None else _scratch(xs[0])
     _check(lib().fp4_quantize_mx_nv_batch(arr, len(xs), _dtype_code(xs[0]), nv_block, mse_kind,
                                           _ptr(ws), ws.numel(), _stream(xs[0].device)))
     return res
@@ -358,7 +361,7 @@ def fp4_quantize_search(x: torch.Tensor, fmt: int = FMT_UE4M3, block: int = 16,
     if gmode != G_NONE and g is None:
         g = torch.empty(1, dtype=torch.float32, device=x.device)
     need_ws = stats is not None or gmode == G_DYNAMIC
-    ws = ws if ws is not None else (workspace(x.device) if need_ws else None)
+    ws = ws if ws is not None else (_scratch(x) if need_ws else None)
     _check(lib().fp4_quantize_search(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], fmt, block,
                                      gmode, _ptr(g), rotate, radius, _ptr(codes), _ptr(scales),
                                      _ptr(block_mse), mse_kind, _ptr(stats), _ptr(ws),
@@ -691,7 +694,7 @@ def fp4_block_mse(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fm
     """Error split of stored codes against x; returns (block_mse, stats)."""
     x = _matrix(x)
     _, _, block_mse, stats = _outputs(x, block, codes, scales, block_mse, stats)
-    ws = ws if ws is not None else (workspace(x.device) if stats is not None else None)
+    ws = ws if ws is not None else (_scratch(x) if stats is not None else None)
     _check(lib().fp4_block_mse(_ptr(x), _dtype_code(x), _ptr(codes), _ptr(scales), fmt, block,
                                _ptr(g), x.shape[0], x.shape[1], rotate, _ptr(block_mse),
                                mse_kind, _ptr(stats), _ptr(ws), 0 if ws is None else ws.numel(),

@@ -143,6 +143,45 @@ def test_a_captured_product_outlives_a_larger_one(which):
     assert all(bool((h == 0x55).all()) for h in held)
 
 
+def quantize_cases():
+    """Calls whose later launches read what the earlier ones left in their workspace: the
+    per-tensor scale and the error sums."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    xs = [torch.randn(m, 4096, generator=g, device=DEV) * s for m, s in ((64, 1.0), (300, 50.0))]
+
+    def call(x):
+        q = fq.nvfp4_quantize(x)
+        m, n = fq.fp4_quantize_mx_nv(x)
+        return torch.cat([q.g, n.g, q.stats.float(), m.stats.float(), n.stats.float(), q.codes.flatten().float()])
+
+    return [lambda x=x: call(x) for x in xs]
+
+
+def test_quantizers_from_two_threads_on_one_stream():
+    cases = quantize_cases()
+    want = [c() for c in cases]
+    torch.cuda.synchronize()
+    run_threads(cases, want)
+
+
+def test_captured_quantizers_beside_eager_ones():
+    """A graph on one stream, eager calls of another tensor on the stream that captured it."""
+    small, large = quantize_cases()
+    want, want_large = small(), large()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = small()
+    for _ in range(20):
+        with torch.cuda.stream(other):
+            graph.replay()
+        with torch.cuda.stream(side):
+            got = large()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(got, want_large)
+
+
 def run_threads(calls, want, rounds=200):
     """Each call over and over from a thread of its own, all on the current stream."""
     stream, bad = torch.cuda.current_stream(), []
