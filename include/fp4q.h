@@ -453,8 +453,9 @@ fp4q_status fp8_quantize_b128(const void* x, int32_t xt, int64_t rows, int64_t c
  * binary64.  A binary32 C differs from the exact product by rounding of order
  * (K / 128 + 8) * 2^-23 of sum |a_hat| |b_hat|.  A bf16 C of more than 16 rows is
  * computed on the 8-bit matrix cores, whose sums hold about 16 bits (2^-15.5 of sum
- * |a_hat| |b_hat|), and rounded.  Scale products below 2^-126 lose their low bits.
- * The same on every run for a given shape.
+ * |a_hat| |b_hat|), and rounded.  Scale products below 2^-126 lose their low bits;
+ * where one is 2^128 or more, the two go one after the other (slowly), so that only
+ * sums past binary32's range are infinite.  The same on every run for a given shape.
  * A NaN code or scale gives NaN in the rows or columns that it belongs to.
  * Errors as for fp4_gemm_nvfp4.
  */

@@ -9,7 +9,11 @@
 // multiply-add under the product of the two scales.  A's scales go by row of A,
 // which is a lane of the result; B's are one number per 128 x 128 ("tile"), so
 // that the factor is one per lane and fragment, or one per row of B ("row"),
-// which costs a multiplication more per element.
+// which costs a multiplication more per element.  Where the product of two scales
+// passes binary32's range they go one after the other (d sb, then the sum with sa:
+// both are at least 1 there, so that d sb overflows only where d sa sb does).  No K
+// loop tests for that: an infinite factor leaves an infinity or NaN in its sum, whatever
+// follows, and a wave that finds one in its sums forms them again (sums_again).
 //
 // The matrix cores' 8-bit form keeps a product only to about 2^-17 of the largest
 // that it adds (measured over 128 Normal products: 1.4e-5 of the result, 2^-15.5 of
@@ -45,6 +49,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4q_gemm_tile.h"
 #include "fp4q_launch.h"
@@ -135,6 +140,76 @@ __device__ __forceinline__ int op_offset(int row, int lane, int half) {
 __device__ __forceinline__ v8i read_op(const uint8_t* lo, const uint8_t* hi, int frag) {
     return join(*reinterpret_cast<const v4i*>(lo + frag * kF16 * kRowStage),
                 *reinterpret_cast<const v4i*>(hi + frag * kF16 * kRowStage));
+}
+
+constexpr float kInf = __builtin_inff();
+
+// acc + d sa sb, under the scales' product or, where that is infinite, one after the other.
+__device__ __forceinline__ float scaled_sum(float d, float sa, float sb, float acc) {
+    const float f = sa * sb;
+    const bool over = fabsf(f) == kInf;
+    return fmaf(over ? d * sb : d, over ? sa : f, acc);
+}
+
+// Whether one of a wave's sums is infinite or NaN.
+template <int NA, int NB>
+__device__ __forceinline__ bool not_finite(const v4f (&acc)[NB][NA]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < NA; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = __builtin_elementwise_maximum(m, fabsf(acc[i][j][e]));  // keeps a NaN
+    return __builtin_amdgcn_ballot_w64(!(m < kInf)) != 0;
+}
+
+// A wave's sums formed again, for scales whose product passes binary32's range: operands and
+// scales straight from memory, no LDS and no barrier.  FA and FB fragments of 16 rows from
+// row a0 and b0 of the tile (whose first rows are m0 and n0), K blocks s_lo .. s_hi - 1.
+template <bool BROW, bool WIDE, int NA, int NB>
+__device__ __forceinline__ void sums_again(v4f (&acc)[NB][NA], const F8Params& p, Rsrc ra, Rsrc rb, int64_t m0, int64_t n0, int rows_a,
+                           int rows_b, int a0, int b0, int s_lo, int s_hi, int lane) {
+    const int K = (int)p.K, r = lane % kF16, q = lane / kF16;
+    const Rsrc rst = make_rsrc(p.sb + n0 / kBlock * p.S, (int64_t)((rows_b + kBlock - 1) / kBlock) * p.S * 4);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < NA; ++j) acc[i][j] = v4f{};
+    auto codes = [&](Rsrc w, int row, int s) {
+        u32x4_t half[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pos = s * kBlock + h * 64 + q * 16;
+            half[h] = __builtin_amdgcn_raw_buffer_load_b128(w, pos < K ? row * K + pos : kDropped, 0, 0);
+        }
+        return Operand<WIDE>::of(join(__builtin_bit_cast(v4i, half[0]), __builtin_bit_cast(v4i, half[1])));
+    };
+    auto scale = [](Rsrc w, int at) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w, at * 4, 0, 0)); };
+    for (int s = s_lo; s < s_hi; ++s) {
+        const Rsrc rsa = make_rsrc(p.sa + s * p.M + m0, rows_a * 4);
+        const Rsrc rsb = make_rsrc(BROW ? p.sb + s * p.N + n0 : p.sb, rows_b * 4);
+        for (int i = 0; i < NB; ++i) {
+            const typename Operand<WIDE>::T b = codes(rb, b0 + i * kF16 + r, s);
+            float sb[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = b0 + i * kF16 + 4 * q + e;
+                sb[e] = BROW ? scale(rsb, row) : scale(rst, row / kBlock * p.S + s);
+            }
+#pragma unroll
+            for (int j = 0; j < NA; ++j) {
+                const int row = a0 + j * kF16 + r;
+                const v4f d = mma16(b, codes(ra, row, s));
+                const float sa = scale(rsa, row);
+#pragma unroll
+                for (int k = 0; k < NB; ++k)  // (registers have no run-time index)
+                    if (k == i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[k][j][e] = scaled_sum(d[e], sa, sb[e], acc[k][j][e]);
+            }
+        }
+    }
 }
 
 // The epilogue of the FP4 kernels (store_tile) for these fragments.  It is written
@@ -300,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const int b_lo = BM * kRowStage + op_offset(b_row, lane, 0), b_hi = BM * kRowStage + op_offset(b_row, lane, 1);
     auto scale_in = [&](int i, int j, const v4f& d, float f, const v4f& sb) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(BROW ? d[e] * sb[e] : d[e], f, acc[i][j][e]);
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], BROW ? sb[e] * f : f, acc[i][j][e]);
     };
     if (s_lo < s_hi) {  // K = 0 has no operands to read
 #pragma unroll
@@ -363,6 +438,8 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
 #pragma unroll
         for (int i = 0; i < TB; ++i) scale_in(i, TA - 1, t[1][i], f_old * sb_old, v4f{});
     }
+    if (__builtin_expect(not_finite(acc), 0))
+        sums_again<BROW, false>(acc, p, ra, rb, m0, n0, (int)rows_a, (int)rows_b, wm * WM, wn * WN, s_lo, s_hi, lane);
     wait_all_barrier();  // LDS is reused below
 
     void* c = splits > 1 ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.c;
@@ -479,9 +556,11 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_fp8_mid(F8Params
 #pragma unroll
             for (int i = 0; i < F; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(BROW ? t[i][e] * sb[i][e] : t[i][e], f, acc[i][j][e]);
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(t[i][e], BROW ? sb[i][e] * f : f, acc[i][j][e]);
         }
     }
+    if (__builtin_expect(not_finite(acc), 0))
+        sums_again<BROW, WIDE>(acc, p, ra, rb, m0, n0, rows_a, rows_b, wm * (T / 2), wn * (T / 2), s_lo, s_hi, lane);
     wait_all_barrier();  // LDS is reused below
 
     // The tile as binary32 in LDS, then whole row segments to memory.
@@ -544,42 +623,52 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_fp8_few(F8Params 
     const Rsrc rsa = make_rsrc(p.sa, (int64_t)S * M * 4);
     const float* sb_tile = p.sb + n0 / kBlock * S;
 
-    v4f acc = {};
-    for (int s0 = wave; s0 < S; s0 += waves * U) {
-        u32x4_t b[U][2], a[U][2];
-        float sa[U], sb[U][4];
+    v4f acc[1][1] = {};
+    auto sums = [&](auto careful) {
+        constexpr bool CAREFUL = decltype(careful)::value;
+        for (int s0 = wave; s0 < S; s0 += waves * U) {
+            u32x4_t b[U][2], a[U][2];
+            float sa[U], sb[U][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * waves;
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + u * waves;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int pos = s * kBlock + h * 64 + q * 16;
-                const int off = s < S && pos < K ? r * K + pos : kDropped;
-                b[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, off, 0, 0);
-                a[u][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, off, 0, 0);
+                for (int h = 0; h < 2; ++h) {
+                    const int pos = s * kBlock + h * 64 + q * 16;
+                    const int off = s < S && pos < K ? r * K + pos : kDropped;
+                    b[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, off, 0, 0);
+                    a[u][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, off, 0, 0);
+                }
+                sa[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsa, s < S ? (s * M + r) * 4 : kDropped, 0, 0));
+                if (BROW) {
+                    const Rsrc rs = make_rsrc(p.sb + (int64_t)(s < S ? s : 0) * p.N + n0, rows_b * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sb[u][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (4 * q + e) * 4, 0, 0));
+                } else {
+                    sb[u][0] = sb_tile[s < S ? s : 0];
+                }
             }
-            sa[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsa, s < S ? (s * M + r) * 4 : kDropped, 0, 0));
-            if (BROW) {
-                const Rsrc rs = make_rsrc(p.sb + (int64_t)(s < S ? s : 0) * p.N + n0, rows_b * 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sb[u][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (4 * q + e) * 4, 0, 0));
-            } else {
-                sb[u][0] = sb_tile[s < S ? s : 0];
+            for (int u = 0; u < U; ++u) {
+                const Wide bw = widen(join(__builtin_bit_cast(v4i, b[u][0]), __builtin_bit_cast(v4i, b[u][1])));
+                const Wide aw = widen(join(__builtin_bit_cast(v4i, a[u][0]), __builtin_bit_cast(v4i, a[u][1])));
+                const v4f d = mma16(bw, aw);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float t = sb[u][BROW ? e : 0];
+                    acc[0][0][e] = CAREFUL ? scaled_sum(d[e], sa[u], t, acc[0][0][e]) : fmaf(d[e], sa[u] * t, acc[0][0][e]);
+                }
             }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const Wide bw = widen(join(__builtin_bit_cast(v4i, b[u][0]), __builtin_bit_cast(v4i, b[u][1])));
-            const Wide aw = widen(join(__builtin_bit_cast(v4i, a[u][0]), __builtin_bit_cast(v4i, a[u][1])));
-            const v4f d = mma16(bw, aw);
-            const float f = BROW ? sa[u] : sa[u] * sb[u][0];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = fmaf(BROW ? d[e] * sb[u][e] : d[e], f, acc[e]);
-        }
+    };
+    sums(std::false_type{});
+    if (__builtin_expect(not_finite(acc), 0)) {
+        acc[0][0] = v4f{};
+        sums(std::true_type{});
     }
     // Register e of lane l: row of A l % 16, row of B 4 (l / 16) + e.
-    *reinterpret_cast<v4f*>(red + (wave * 16 + r) * 16 + 4 * q) = acc;
+    *reinterpret_cast<v4f*>(red + (wave * 16 + r) * 16 + 4 * q) = acc[0][0];
     __syncthreads();
     for (int e = threadIdx.x; e < 256; e += blockDim.x) {
         double sum = 0.0;
