@@ -79,6 +79,7 @@ struct F8Params {
     bool whole;        // C's rows start on 16 bytes
     int splits;        // K ranges per tile (1: C directly)
     float* partial;    // splits > 1: splits x M x N
+    unsigned first;    // this launch's first workgroup (of tiles times K ranges)
 };
 
 // 16 x 16 x 128 products.  Lane l supplies 32 bytes of row l % 16 of each operand,
@@ -306,9 +307,11 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave >> 2, wn = wave & 3;  // 2 x 4 waves of 128 x 64
     const int64_t tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
-    const int splits = p.splits, split = (int)(blockIdx.x % splits);
+    const int splits = p.splits;
+    const unsigned group = p.first + blockIdx.x;
+    const int split = (int)(group % splits);
     int64_t tm, tn;
-    tile_of(blockIdx.x / splits, tiles_m, tiles_n, tm, tn);
+    tile_of(group / splits, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = tm * BM, n0 = tn * BN;
     const int64_t rows_a = p.M - m0 < BM ? p.M - m0 : BM;
     const int64_t rows_b = p.N - n0 < BN ? p.N - n0 : BN;
@@ -481,9 +484,11 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_fp8_mid(F8Params
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / 2, wn = wave % 2;
     const int64_t tiles_m = (p.M + T - 1) / T, tiles_n = (p.N + T - 1) / T;
-    const int splits = p.splits, split = (int)(blockIdx.x % splits);
+    const int splits = p.splits;
+    const unsigned group = p.first + blockIdx.x;
+    const int split = (int)(group % splits);
     int64_t tm, tn;
-    tile_of(blockIdx.x / splits, tiles_m, tiles_n, tm, tn);
+    tile_of(group / splits, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = tm * T, n0 = tn * T;
     const int rows_a = (int)(p.M - m0 < T ? p.M - m0 : T), rows_b = (int)(p.N - n0 < T ? p.N - n0 : T);
     const int K = (int)p.K, S = p.S;
@@ -732,13 +737,17 @@ Choice choose(int64_t M, int64_t N, int64_t K, bool wide) {
 }
 
 template <bool BROW, bool WIDE>
-void launch_tile(const F8Params& p, int tile, unsigned groups, hipStream_t stream) {
-    if (!WIDE && tile == 256)
-        FP4Q_LAUNCH(k_gemm_fp8<BROW>, dim3(groups), dim3(kThreads), 0, stream, p);
-    else if (tile == 128)
-        FP4Q_LAUNCH((k_gemm_fp8_mid<128, BROW, WIDE>), dim3(groups), dim3(256), MidPlan<128>::kLds, stream, p);
-    else
-        FP4Q_LAUNCH((k_gemm_fp8_mid<64, BROW, WIDE>), dim3(groups), dim3(256), MidPlan<64>::kLds, stream, p);
+void launch_tile(F8Params p, int tile, int64_t groups, hipStream_t stream) {
+    for (int64_t first = 0; first < groups; first += kMaxGrid) {
+        const dim3 grid((unsigned)std::min(groups - first, kMaxGrid));
+        p.first = (unsigned)first;
+        if (!WIDE && tile == 256)
+            FP4Q_LAUNCH(k_gemm_fp8<BROW>, grid, dim3(kThreads), 0, stream, p);
+        else if (tile == 128)
+            FP4Q_LAUNCH((k_gemm_fp8_mid<128, BROW, WIDE>), grid, dim3(256), MidPlan<128>::kLds, stream, p);
+        else
+            FP4Q_LAUNCH((k_gemm_fp8_mid<64, BROW, WIDE>), grid, dim3(256), MidPlan<64>::kLds, stream, p);
+    }
 }
 
 }  // namespace
@@ -755,7 +764,7 @@ int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len) {
     const int S = (int)((j.K + kBlock - 1) / kBlock);
     const bool whole = j.N * (j.ct == 1 ? 4 : 2) % 16 == 0 && (uintptr_t)j.c % 16 == 0;
     F8Params p{j.a_codes, j.a_scales, j.b_codes, j.b_scales, j.M, j.N, j.K, S, j.c, j.ct, whole, 1,
-               static_cast<float*>(j.ws)};
+               static_cast<float*>(j.ws), 0};
     if (j.M <= kFewMaxM) {
         // Enough waves to keep memory busy whatever N: 16 per workgroup while
         // there are fewer workgroups than CUs.
@@ -774,10 +783,10 @@ int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len) {
                      (long long)j.M, (long long)j.N, (long long)j.K);
             return (int)hipErrorInvalidConfiguration;
         }
-        if (j.b_row && wide) launch_tile<true, true>(p, ch.tile, (unsigned)groups, stream);
-        else if (j.b_row) launch_tile<true, false>(p, ch.tile, (unsigned)groups, stream);
-        else if (wide) launch_tile<false, true>(p, ch.tile, (unsigned)groups, stream);
-        else launch_tile<false, false>(p, ch.tile, (unsigned)groups, stream);
+        if (j.b_row && wide) launch_tile<true, true>(p, ch.tile, groups, stream);
+        else if (j.b_row) launch_tile<true, false>(p, ch.tile, groups, stream);
+        else if (wide) launch_tile<false, true>(p, ch.tile, groups, stream);
+        else launch_tile<false, false>(p, ch.tile, groups, stream);
         if (p.splits > 1) launch_splitk_reduce(p.partial, p.splits, j.M * j.N, j.c, j.ct, j.stream);
     }
     const hipError_t e = hipGetLastError();

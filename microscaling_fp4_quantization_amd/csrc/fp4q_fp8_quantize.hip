@@ -45,6 +45,7 @@ struct Fp8Params {
     int64_t rows, cols;
     int64_t ld, ld_t;        // bytes per row of codes and of codes_t
     int64_t tiles_c;         // tiles along the columns
+    unsigned first;          // this launch's first tile
     uint8_t* codes;          // NULL: not wanted
     float* scales;
     uint8_t* codes_t;        // NULL: not wanted
@@ -281,7 +282,7 @@ template <int XT, bool TILE, bool OUT, bool TOUT>
 __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Fp8Params p) {
     __shared__ Fp8Lds lds;
     __shared__ __attribute__((aligned(16))) uint8_t flip[TOUT ? kTile * kPitch : 16];
-    quantize_tile<XT, TILE, OUT, TOUT>(p, blockIdx.x, lds, flip);
+    quantize_tile<XT, TILE, OUT, TOUT>(p, p.first + blockIdx.x, lds, flip);
 }
 
 // A linear layer's input (row scales) and weight (tile scales), both outputs of each, in
@@ -334,7 +335,7 @@ int launch_fp8_quantize_two(const Fp8QuantJob& x, const Fp8QuantJob& w, char* ms
                      w.codes && w.codes_t;
     const Fp8Params px = params_of(x), pw = params_of(w);
     const int64_t tx = tiles_of(px), tiles = tx + tiles_of(pw);
-    if (!all || tiles > INT32_MAX) {
+    if (!all || tiles > kMaxGrid) {
         const int rc = launch_fp8_quantize(x, msg, msg_len);
         return rc ? rc : launch_fp8_quantize(w, msg, msg_len);
     }
@@ -350,20 +351,23 @@ int launch_fp8_quantize_two(const Fp8QuantJob& x, const Fp8QuantJob& w, char* ms
 
 int launch_fp8_quantize(const Fp8QuantJob& j, char* msg, size_t msg_len) {
     if (j.rows == 0 || j.cols == 0) return 0;
-    const Fp8Params p = params_of(j);
+    Fp8Params p = params_of(j);
     const int64_t tiles = tiles_of(p);
     if (tiles > INT32_MAX) {
         snprintf(msg, msg_len, "fp8 quantize: %lld x %lld needs more workgroups than one launch holds",
                  (long long)j.rows, (long long)j.cols);
         return (int)hipErrorInvalidConfiguration;
     }
-    const unsigned grid = (unsigned)tiles;
-    if (j.xt == 0) {
-        if (j.tile) launch_outs<0, true>(p, grid, j.stream);
-        else launch_outs<0, false>(p, grid, j.stream);
-    } else {
-        if (j.tile) launch_outs<1, true>(p, grid, j.stream);
-        else launch_outs<1, false>(p, grid, j.stream);
+    for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+        const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
+        p.first = (unsigned)first;
+        if (j.xt == 0) {
+            if (j.tile) launch_outs<0, true>(p, grid, j.stream);
+            else launch_outs<0, false>(p, grid, j.stream);
+        } else {
+            if (j.tile) launch_outs<1, true>(p, grid, j.stream);
+            else launch_outs<1, false>(p, grid, j.stream);
+        }
     }
     return launch_status(msg, msg_len);
 }

@@ -188,6 +188,11 @@ void profile_after(void* stream);
         ::fp4q::profile_after(stream);                                             \
     } while (0)
 
+// A grid holds fewer than 2^32 threads: more workgroups (of up to 512 threads) than this go out
+// in several launches, each told its first one.  (A second grid dimension needs a test for the
+// workgroups past the last, which cost small products 3%.)
+constexpr int64_t kMaxGrid = 1 << 22;
+
 // The library's static device scratch for the allocation-free entry point:
 // its device address on the current device (looked up once per device) and
 // its size (kWsBytes).  Returns 0, else a HIP error code with `msg` set.

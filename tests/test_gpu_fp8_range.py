@@ -73,3 +73,34 @@ def test_row_scales_of_opposite_ends(m):
         f8 = lambda x: x.to(torch.float8_e4m3fn)
         got = fq.fp8_gemm_b128(f8(a), sa, f8(b), sb, ROW)
         assert torch.equal(got.double(), a.double() @ b.double().t().contiguous())
+
+
+def test_quantize_takes_more_workgroups_than_a_grid_holds():
+    """2^31 + 300 elements in one row, and in one column: 2^24 workgroups and some."""
+    n = (1 << 31) + 300
+    x = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    tail = torch.randn(300, device=DEV).to(torch.bfloat16)
+    x[-300:] = tail
+    want = fq.fp8_quantize_b128(tail.view(1, -1))
+    q = fq.fp8_quantize_b128(x.view(1, -1))
+    assert q.codes.shape == (1, n + 4)
+    assert torch.equal(q.codes.view(torch.uint8)[:, -304:], want.codes.view(torch.uint8)) and torch.equal(q.scales[-3:], want.scales)
+    assert not q.codes.view(torch.uint8)[:, :-304].any()
+    del q
+    q = fq.fp8_quantize_b128(x.view(-1, 1), codes=False, transposed=True)
+    assert torch.equal(q.codes_t.view(torch.uint8)[:, -304:], want.codes.view(torch.uint8))
+    assert torch.equal(q.scales_t[-3:], want.scales) and not q.codes_t.view(torch.uint8)[:, :-304].any()
+
+
+def test_gemm_takes_more_workgroups_than_a_grid_holds():
+    """2^30 + 70 rows of A: 2^24 + 2 tiles of 64.  Whole numbers: the last rows are exact."""
+    m, n, k = (1 << 30) + 70, 8, 16
+    g = torch.Generator(device=DEV).manual_seed(5)
+    small = lambda r: torch.randint(-8, 9, (r, k), generator=g, device=DEV).float()
+    tail, b = small(70), small(n)
+    a = torch.zeros(m, k, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    a[-70:].view(torch.uint8).copy_(tail.to(torch.float8_e4m3fn).view(torch.uint8))
+    one = lambda *s: torch.ones(*s, device=DEV)
+    got = fq.fp8_gemm_b128(a, one(1, m), b.to(torch.float8_e4m3fn), one(1, 1))
+    assert torch.equal(got[-70:].double(), tail.double() @ b.double().t().contiguous())
+    assert not got[:-70].any()
