@@ -16,6 +16,7 @@ took it half as long again.
 from __future__ import annotations
 
 import functools
+import math
 
 import torch
 
@@ -38,7 +39,7 @@ class _Fp8Linear(torch.autograd.Function):
         out, k = w.shape
         shape = x.shape
         if x.dim() != 2:
-            x = x.reshape(-1, k)
+            x = x.reshape(math.prod(shape[:-1]), k)
         if not x.is_contiguous():
             x = x.contiguous()
         if not w.is_contiguous():
