@@ -422,6 +422,9 @@ typedef enum { FP4Q_B128_ROW = 0, FP4Q_B128_TILE = 1 } fp4q_b128_kind;
  *               cols; TILE ceil(cols / 128) x ceil(rows / 128)
  * Any rows and cols (rows * cols <= (2^31 - 1) * 512; an empty matrix is a
  * no-op); no workspace.  Equal to calling twice, on x and on its transpose.
+ * A NaN of x is a NaN code (0x7F or 0xFF) and leaves the rest of its block as if it
+ * were 0.  An infinity makes its block's scale infinite, its own code NaN and the
+ * block's finite elements codes of 0: on use the whole block is NaN.
  * Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN, FP4Q_ERR_HIP.
  */
 fp4q_status fp8_quantize_b128(const void* x, int32_t xt, int64_t rows, int64_t cols, int32_t kind,

@@ -21,3 +21,62 @@ def test_linear_of_empty_inputs(shape):
     y.backward(torch.ones_like(y))
     assert x.grad.shape == shape and w.grad.shape == w.shape and not x.grad.any() and not w.grad.any()
     assert fq.fp8_linear(x, w[:0]).shape == (*shape[:-1], 0)
+
+
+def same_but_nan(got, want):
+    """Equal codes, with either sign of NaN."""
+    nan = (want & 0x7F) == 0x7F
+    np.testing.assert_array_equal((got & 0x7F) == 0x7F, nan)
+    np.testing.assert_array_equal(got[~nan], want[~nan])
+
+
+def reference(x, tile):
+    """fp8_ref's codes and scales with each NaN taken as 0 first, then a NaN code; blocks of an infinity by hand."""
+    nan, inf = np.isnan(x), np.isinf(x)
+    codes, scales = ref.quantize(np.where(nan | inf, 0, x).astype(np.float32), tile)
+    step = 128 if tile else 1
+    s = scales if tile else scales.T
+    for r, c in np.argwhere(inf):
+        block = (slice(r // step * step, r // step * step + step), slice(c // 128 * 128, min(x.shape[1], c // 128 * 128 + 128)))
+        codes[block] = np.where(inf[block], 0x7F, np.where(np.signbit(x[block]), 0x80, 0))
+        s[r // step, c // 128] = np.inf
+    codes[:, :x.shape[1]][nan] = 0x7F
+    return codes, scales
+
+
+@pytest.mark.parametrize("kind", [ROW, TILE])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_keeps_what_is_not_finite_in_its_block(dtype, kind):
+    rng = np.random.default_rng(21)
+    t = torch.from_numpy(rng.standard_normal((300, 290)).astype(np.float32)).to(dtype)
+    for r, c, v in ((3, 5, "nan"), (3, 200, "-nan"), (140, 7, "inf"), (299, 289, "-inf"), (260, 131, "nan"), (9, 250, "nan")):
+        t[r, c] = float(v)
+    t[200] = float("nan")
+    x = t.float().numpy()
+    q = fq.fp8_quantize_b128(t.to(DEV), kind, transposed=True)
+    for codes, scales, src in ((q.codes, q.scales, x), (q.codes_t, q.scales_t, x.T)):
+        c, s = reference(src, kind == TILE)
+        np.testing.assert_array_equal(scales.cpu().numpy(), s)
+        same_but_nan(codes.view(torch.uint8).cpu().numpy(), c)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_linear_shows_what_is_not_finite(value):
+    """One such element of x: its row of y and its column of dw are NaN; of dy: its row of dx and of dw."""
+    x, w, dy = torch.randn(40, 96, device=DEV), torch.randn(56, 96, device=DEV), torch.randn(40, 56, device=DEV)
+    for at in ("x", "dy"):
+        a, g = x.clone(), dy.clone()
+        (a if at == "x" else g)[7, 11] = value
+        a, b = a.requires_grad_(), w.clone().requires_grad_()
+        y = fq.fp8_linear(a, b)
+        y.backward(g)
+        rows = torch.arange(40, device=DEV) == 7
+        assert torch.equal(torch.isnan(y).all(1), rows & (at == "x"))
+        assert torch.equal(torch.isnan(y).any(1), rows & (at == "x"))
+        assert torch.equal(torch.isnan(a.grad).any(1), rows & (at == "dy"))
+        hit = torch.zeros(56, 96, dtype=torch.bool, device=DEV)
+        if at == "x":
+            hit[:, 11] = True
+        else:
+            hit[11] = True
+        assert torch.equal(torch.isnan(b.grad), hit)
