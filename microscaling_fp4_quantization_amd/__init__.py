@@ -455,6 +455,22 @@ def _b128_outputs(x, rows: int, cols: int, kind: int, codes, scales, what: str, 
     return codes, scales
 
 
+class _NoGradient(torch.autograd.Function):
+    """The outputs of a call that has no gradient, for inputs that require one: a backward
+    pass that gets there says so, where detached outputs would lose it silently.  Outputs are
+    given as detached views, so that a caller's own buffer gathers no history."""
+
+    @staticmethod
+    def forward(ctx, name, n, *tensors):
+        ctx.name = name
+        ctx.mark_dirty(*tensors[:n])
+        return tensors[0] if n == 1 else tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError(f"{ctx.name} has no gradient: call it under torch.no_grad() or on detached tensors")
+
+
 def fp8_quantize_b128(x: torch.Tensor, kind: int = B128_ROW, *, codes=True, transposed=False,
                       out: Optional[Fp8Quantized] = None) -> Fp8Quantized:
     """E4M3 codes with one float32 scale per 128 elements of a row (B128_ROW) or
@@ -500,7 +516,8 @@ def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
                   out: Optional[torch.Tensor] = None,
                   ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """C = A_hat @ B_hat.T for operands as fp8_quantize_b128 writes them: A with row
-    scales, B with the scales that ``b_kind`` names."""
+    scales, B with the scales that ``b_kind`` names.  It has no gradient (fp8_linear
+    has): a backward pass through scales that require one raises."""
     if b_kind != B128_ROW and b_kind != B128_TILE:
         raise ValueError(f"b_kind {b_kind} is not B128_ROW or B128_TILE")
     m, k = _b128_operand(a_codes, a_scales, B128_ROW, "a")
@@ -524,6 +541,8 @@ def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
                          0 if ws is None else ws.numel(), _raw_stream(dev))
     if rc:
         _check(rc)
+    if (a_scales.requires_grad or b_scales.requires_grad) and torch.is_grad_enabled():
+        return _NoGradient.apply("fp8_gemm_b128", 1, out.detach(), a_scales, b_scales)
     return out
 
 
@@ -611,7 +630,8 @@ def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: i
     ``topk_ids`` (int32) and ``topk_weights`` (float32), tokens x top_k.  y has x's
     dtype unless ``out_dtype`` or ``out`` says otherwise.  ``ws``: a moe_workspace that
     no other call uses at the same time; a captured call without one gets its own, and
-    clears its counter at each replay."""
+    clears its counter at each replay.  It has no gradient: a backward pass through it
+    raises, where x, the router or the given weights require one."""
     x = _matrix(x)
     tokens, dim = x.shape
     if w13.fmt != w2.fmt:
@@ -667,6 +687,11 @@ def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: i
         _check(rc)
     if free is not None:
         free.append(ws)
+    if torch.is_grad_enabled() and (x.requires_grad or (router is not None and router.requires_grad)
+                                    or topk_weights.requires_grad):
+        if router is None:  # topk_weights is an input
+            return MoeOutput(_NoGradient.apply("moe_layer", 1, out.detach(), x, topk_weights), topk_ids, topk_weights)
+        out, topk_weights = _NoGradient.apply("moe_layer", 2, out.detach(), topk_weights.detach(), x, router)
     return MoeOutput(out, topk_ids, topk_weights)
 
 

@@ -80,3 +80,37 @@ def test_linear_shows_what_is_not_finite(value):
         else:
             hit[11] = True
         assert torch.equal(torch.isnan(b.grad), hit)
+
+
+def test_a_backward_pass_through_calls_without_a_gradient_raises():
+    a, b = fq.fp8_quantize_b128(torch.randn(20, 64, device=DEV)), fq.fp8_quantize_b128(torch.randn(30, 64, device=DEV), TILE)
+    want = fq.fp8_gemm_b128(a.codes, a.scales, b.codes, b.scales)
+    s = b.scales.clone().requires_grad_()
+    for out in (None, torch.empty_like(want)):
+        y = fq.fp8_gemm_b128(a.codes, a.scales, b.codes, s, out=out)
+        assert torch.equal(y, want)
+        assert out is None or (y.data_ptr() == out.data_ptr() and not out.requires_grad)
+        with pytest.raises(NotImplementedError, match="fp8_gemm_b128"):
+            y.sum().backward()
+    with torch.no_grad():
+        assert not fq.fp8_gemm_b128(a.codes, a.scales, b.codes, s).requires_grad
+
+    e, d, i, k, t = 4, 64, 32, 2, 3
+    quant = lambda r, c: fq.fp8_quantize_b128(torch.randn(r, c, device=DEV), TILE)
+    w13, w2 = (fq.ExpertWeights(fq.FMT_E4M3_B128, q.codes, q.scales) for q in (quant(e * 2 * i, d), quant(e * d, i)))
+    x, wr = torch.randn(t, d, device=DEV), torch.randn(e, d, device=DEV)
+    want = fq.moe_layer(x, w13, w2, e, k, router=wr)
+    assert not want.y.requires_grad
+    for xg, rg in ((True, False), (False, True)):
+        r = fq.moe_layer(x.clone().requires_grad_(xg), w13, w2, e, k, router=wr.clone().requires_grad_(rg))
+        assert torch.equal(r.y, want.y) and torch.equal(r.topk_weights, want.topk_weights)
+        for v in (r.y, r.topk_weights):
+            with pytest.raises(NotImplementedError, match="moe_layer"):
+                v.sum().backward(retain_graph=True)
+    w = want.topk_weights.clone().requires_grad_()
+    r = fq.moe_layer(x, w13, w2, e, k, topk_ids=want.topk_ids, topk_weights=w)
+    assert torch.equal(r.y, want.y)
+    with pytest.raises(NotImplementedError, match="moe_layer"):
+        r.y.sum().backward()
+    with torch.no_grad():
+        assert not fq.moe_layer(x.clone().requires_grad_(), w13, w2, e, k, router=wr).y.requires_grad
