@@ -100,13 +100,16 @@ __device__ __forceinline__ Frag frag_of(const u32x4_t (&w)[4]) {
 }
 
 // Binary32 as bf16 parts: what is left after a part is exact, so three parts hold
-// all 24 bits of a value whose last bits do not fall below the smallest number.
-// (An infinity or NaN leaves nothing.)
+// all 24 bits of a value whose last bits do not fall below the smallest number.  The
+// first part stops at bf16's largest number, which the largest binary32 ones would round
+// past; what is left of an infinity or NaN is itself, and of its own part nothing.
+__device__ __forceinline__ float first_part(float f) { return __builtin_amdgcn_fmed3f(f, -0x1.FEp127f, 0x1.FEp127f); }
 __device__ __forceinline__ float left(float f, uint32_t part) {
     return (part & 0x7F800000u) == 0x7F800000u ? 0.0f : f - __uint_as_float(part);
 }
 template <int P>
 __device__ __forceinline__ void split8(const float (&f)[8], bf16x8_t (&out)[P]) {
+    static_assert(P > 1, "an infinity is in the second part");
     float rest[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) rest[e] = f[e];
@@ -115,7 +118,8 @@ __device__ __forceinline__ void split8(const float (&f)[8], bf16x8_t (&out)[P]) 
         u32x4_t w;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            w[q] = pack_bf16x2(rest[2 * q], rest[2 * q + 1]);
+            w[q] = p == 0 ? pack_bf16x2(first_part(rest[2 * q]), first_part(rest[2 * q + 1]))
+                          : pack_bf16x2(rest[2 * q], rest[2 * q + 1]);
             rest[2 * q] = left(rest[2 * q], w[q] << 16);
             rest[2 * q + 1] = left(rest[2 * q + 1], w[q] & 0xFFFF0000u);
         }
@@ -284,7 +288,7 @@ __device__ __forceinline__ v4f mma_step(const Frag& w, const Frag (&x)[P], uint3
 // 8 consecutive elements of a row, as bf16 parts.
 template <int P>
 __device__ __forceinline__ void load8(Rsrc r, int at, bf16x8_t (&out)[P]) {
-    if (P == 1) {
+    if constexpr (P == 1) {
         out[0] = __builtin_bit_cast(bf16x8_t, load128(r, at < 0 ? kDropped : at * 2));
     } else {
         const u32x4_t a = load128(r, at < 0 ? kDropped : at * 4), b = load128(r, at < 0 ? kDropped : at * 4 + 16);
@@ -608,7 +612,7 @@ __device__ __forceinline__ void put_h(const MoeParams& p, float sg, float su, in
     const int64_t plane = (int64_t)p.T * p.k * p.I;
     float h = sg / (1.0f + expf(-sg)) * su;
     for (int a = 0; a < parts_h; ++a) {
-        const uint32_t b = to_bf16(h);
+        const uint32_t b = pack_bf16x2(a == 0 ? first_part(h) : h, 0.0f) & 0xFFFFu;
         p.h[at + a * plane] = (uint16_t)b;
         h = left(h, b << 16);
     }
