@@ -814,9 +814,12 @@ __global__ __launch_bounds__(256) void k_moe_combine(MoeParams p, const float* z
         sum[c] += __shfl_xor(sum[c], 2);
     }
     if (s != 0 || i >= p.T * cols) return;
+    // y need not start on more than its element's boundary.
+    typedef float Four __attribute__((ext_vector_type(4), aligned(4)));
+    typedef uint32_t Two __attribute__((ext_vector_type(2), aligned(2)));
     const int64_t o = (int64_t)t * p.D + d;
-    if (p.yt == 1) *reinterpret_cast<v4f*>(static_cast<float*>(p.y) + o) = sum;
-    else *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p.y) + o) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+    if (p.yt == 1) *reinterpret_cast<Four*>(static_cast<float*>(p.y) + o) = sum;
+    else *reinterpret_cast<Two*>(static_cast<uint16_t*>(p.y) + o) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
 
 // ---------------------------------------------------------------------------
