@@ -553,9 +553,10 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_moe_route(MoeParams p) 
         for (int w = 0; w < kRouteWaves; ++w) sum += red[w][threadIdx.x];
         if (t < rows_x && e < rows_r) p.logits[((int64_t)range * p.T + t0 + t) * p.E + e0 + e] = sum;
     }
+    // The last workgroup to get here sees everyone's sums (none waits): each wave waits for
+    // its own stores (the barrier does not), then thread 0 releases and acquires for all.
+    wait_vm<0>();
     __syncthreads();
-    // The last workgroup to get here sees everyone's sums (none waits): the barrier
-    // orders the workgroup's sums before thread 0, which releases and acquires for it.
     if (threadIdx.x == 0) {
         const uint32_t n = __hip_atomic_fetch_add(p.count, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
         last = n + 1 == gridDim.x;
