@@ -127,20 +127,21 @@ def _check(rc: int):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# torch's own shorter ways to what torch.cuda gives, where this torch has them: a small call is
+# bound by the host, and these are a fifth of its time.
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _raw_stream(dev) -> int:
-    """torch's current stream on `dev` as a hipStream_t (2 us less than through a
-    torch.cuda.Stream object, a fifth of a small call)."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if get is None or dev.index is None:
+    """torch's current stream on `dev` as a hipStream_t."""
+    if _get_raw_stream is None or dev.index is None:
         return torch.cuda.current_stream(dev).cuda_stream
-    return get(dev.index)
-
-
-def _stream(dev) -> ctypes.c_void_p:
-    return ctypes.c_void_p(_raw_stream(dev))
+    return _get_raw_stream(dev.index)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -161,6 +162,38 @@ def _matrix(x: torch.Tensor, what: str = "x") -> torch.Tensor:
     return x
 
 
+def _capturing(dev: torch.device) -> bool:
+    """Whether torch's current stream on `dev` is being captured into a graph."""
+    if dev.index == _get_device():
+        return _is_capturing()
+    with torch.cuda.device(dev):
+        return _is_capturing()
+
+
+# Workspaces of calls that were given none, by (device, stream): those that no call is issuing
+# its launches through.  A call takes one out while it launches: calls on one stream share it in
+# stream order, and calls from several threads, whose launches may mix, have one each (list.pop
+# and list.append are atomic).
+_free_workspaces, _free_moe_workspaces = {}, {}
+
+
+def _borrow(pool: dict, make, dev: torch.device, stream: int, nbytes: int):
+    """A workspace from `pool`, or a new one from make(dev, nbytes), and the list to append it
+    to after the call.  Under capture a new one and None: it is the graph's own, which neither
+    eager calls write nor larger ones free, and what `make` fills is filled at each replay."""
+    if _capturing(dev):
+        return make(dev, nbytes), None
+    key = dev.index, stream
+    try:
+        free = pool[key]
+        ws = free.pop()
+        if ws.numel() >= nbytes:
+            return ws, free
+    except (KeyError, IndexError):
+        free = pool.setdefault(key, [])
+    return make(dev, max(nbytes, 1 << 20)), free
+
+
 def workspace_bytes(rows: int = 0, cols: int = 0, block: int = 32) -> int:
     return int(lib().fp4q_workspace_bytes(rows, cols, block))
 
@@ -176,11 +209,9 @@ def _workspace_size() -> int:
     return workspace_bytes()
 
 
-def _scratch(x: torch.Tensor) -> torch.Tensor:
-    """The workspace of a call without one of the caller's: from torch's allocator, so that
-    it is no other call's whose launches may mix with this one's, and a captured call's
-    stays its graph's."""
-    return x.new_empty(_workspace_size(), dtype=torch.uint8)
+def _scratch(x: torch.Tensor, stream: int):
+    """The workspace of a quantize call that was given none (see _borrow)."""
+    return _borrow(_free_workspaces, gemm_workspace, x.device, stream, _workspace_size())
 
 
 def new_stats(device) -> torch.Tensor:
@@ -232,11 +263,15 @@ def mxfp4_quantize(x: torch.Tensor, rotate: int = 0, *, codes=None, scales=None,
     """
     x = _matrix(x)
     codes, scales, block_mse, stats = _outputs(x, 32, codes, scales, block_mse, stats)
-    ws = ws if ws is not None else (_scratch(x) if stats is not None else None)
+    stream, free = _raw_stream(x.device), None
+    if ws is None and stats is not None:
+        ws, free = _scratch(x, stream)
     _check(lib().mxfp4_quantize(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], rotate,
                                 _ptr(codes), _ptr(scales), _ptr(block_mse), mse_kind,
                                 _ptr(stats), _ptr(ws), 0 if ws is None else ws.numel(),
-                                _stream(x.device)))
+                                stream))
+    if free is not None:
+        free.append(ws)
     return Quantized(codes, scales, block_mse, stats, None)
 
 
@@ -255,11 +290,15 @@ def nvfp4_quantize(x: torch.Tensor, block: int = 16, scale_fmt: int = FMT_UE4M3,
     if gmode != G_NONE and g is None:
         g = torch.empty(x.shape[0] if gmode == G_ROW else 1, dtype=torch.float32, device=x.device)
     need_ws = stats is not None or gmode == G_DYNAMIC
-    ws = ws if ws is not None else (_scratch(x) if need_ws else None)
+    stream, free = _raw_stream(x.device), None
+    if ws is None and need_ws:
+        ws, free = _scratch(x, stream)
     _check(lib().nvfp4_quantize(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], block,
                                 scale_fmt, gmode, _ptr(g), rotate, _ptr(codes), _ptr(scales),
                                 _ptr(block_mse), mse_kind, _ptr(stats), _ptr(ws),
-                                0 if ws is None else ws.numel(), _stream(x.device)))
+                                0 if ws is None else ws.numel(), stream))
+    if free is not None:
+        free.append(ws)
     return Quantized(codes, scales, block_mse, stats, g)
 
 
@@ -276,7 +315,7 @@ def nvfp4_quantize_noalloc(x: torch.Tensor, block: int = 16, scale_fmt: int = FM
         g = torch.empty(x.shape[0] if gmode == G_ROW else 1, dtype=torch.float32, device=x.device)
     _check(lib().nvfp4_quantize_noalloc(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], block,
                                         scale_fmt, gmode, _ptr(g), rotate, _ptr(codes), _ptr(scales),
-                                        _ptr(block_mse), mse_kind, _ptr(stats), _stream(x.device)))
+                                        _ptr(block_mse), mse_kind, _ptr(stats), _raw_stream(x.device)))
     return Quantized(codes, scales, block_mse, stats, g)
 
 
@@ -297,11 +336,15 @@ def fp4_quantize_mx_nv(x: torch.Tensor, nv_block: int = 16, *, mse_kind: int = M
                  nv.get("stats", stats))
     if g is None:
         g = torch.empty(1, dtype=torch.float32, device=x.device)
-    ws = ws if ws is not None else _scratch(x)
+    stream, free = _raw_stream(x.device), None
+    if ws is None:
+        ws, free = _scratch(x, stream)
     _check(lib().fp4_quantize_mx_nv(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1],
                                     _ptr(m[0]), _ptr(m[1]), _ptr(m[2]), _ptr(m[3]), nv_block, _ptr(g),
                                     _ptr(v[0]), _ptr(v[1]), _ptr(v[2]), _ptr(v[3]), mse_kind,
-                                    _ptr(ws), ws.numel(), _stream(x.device)))
+                                    _ptr(ws), ws.numel(), stream))
+    if free is not None:
+        free.append(ws)
     return Quantized(*m, None), Quantized(*v, g)
 
 
@@ -342,9 +385,13 @@ def fp4_quantize_mx_nv_batch(xs, nv_block: int = 16, *, mse_kind: int = MSE_ABS,
         arr[i] = MxNvTensor(ptr(x), x.shape[0], x.shape[1], ptr(m[0]), ptr(m[1]), ptr(m[2]), ptr(m[3]),
                             ptr(g), ptr(v[0]), ptr(v[1]), ptr(v[2]), ptr(v[3]))
         res.append((Quantized(*m, None), Quantized(*v, g)))
-    ws = ws if ws is not None else _scratch(xs[0])
+    stream, free = _raw_stream(xs[0].device), None
+    if ws is None:
+        ws, free = _scratch(xs[0], stream)
     _check(lib().fp4_quantize_mx_nv_batch(arr, len(xs), _dtype_code(xs[0]), nv_block, mse_kind,
-                                          _ptr(ws), ws.numel(), _stream(xs[0].device)))
+                                          _ptr(ws), ws.numel(), stream))
+    if free is not None:
+        free.append(ws)
     return res
 
 
@@ -361,19 +408,20 @@ def fp4_quantize_search(x: torch.Tensor, fmt: int = FMT_UE4M3, block: int = 16,
     if gmode != G_NONE and g is None:
         g = torch.empty(1, dtype=torch.float32, device=x.device)
     need_ws = stats is not None or gmode == G_DYNAMIC
-    ws = ws if ws is not None else (_scratch(x) if need_ws else None)
+    stream, free = _raw_stream(x.device), None
+    if ws is None and need_ws:
+        ws, free = _scratch(x, stream)
     _check(lib().fp4_quantize_search(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], fmt, block,
                                      gmode, _ptr(g), rotate, radius, _ptr(codes), _ptr(scales),
                                      _ptr(block_mse), mse_kind, _ptr(stats), _ptr(ws),
-                                     0 if ws is None else ws.numel(), _stream(x.device)))
+                                     0 if ws is None else ws.numel(), stream))
+    if free is not None:
+        free.append(ws)
     return Quantized(codes, scales, block_mse, stats, g)
 
 
 def gemm_workspace(device, nbytes: int) -> torch.Tensor:
-    """A new device workspace of `nbytes` (at least 256, so that it has an address) for the
-    GEMMs and the linear layer.  Calls without one of the caller's take theirs here: torch's
-    allocator hands a freed one to the next call on its stream, never to a call whose launches
-    may mix with this one's, and a captured call's stays its graph's."""
+    """A new device workspace of at least `nbytes` for the GEMMs."""
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
@@ -392,11 +440,14 @@ def fp4_gemm_mxfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=a_codes.device)
     need = int(lib().fp4_gemm_workspace_bytes(m, n, k))
+    stream, free = _raw_stream(a_codes.device), None
     if ws is None and need:
-        ws = gemm_workspace(a_codes.device, need)
+        ws, free = _borrow(_free_workspaces, gemm_workspace, a_codes.device, stream, need)
     _check(lib().fp4_gemm_mxfp4(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), m, n,
                                 k, _ptr(out), _dtype_code(out), _ptr(ws),
-                                0 if ws is None else ws.numel(), _stream(a_codes.device)))
+                                0 if ws is None else ws.numel(), stream))
+    if free is not None:
+        free.append(ws)
     return out
 
 
@@ -417,12 +468,14 @@ def fp4_gemm_nvfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, a_g: Optional[
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=a_codes.device)
     need = int(lib().fp4_gemm_nvfp4_workspace_bytes(m, n, k))
+    stream, free = _raw_stream(a_codes.device), None
     if ws is None and need:
-        ws = gemm_workspace(a_codes.device, need)
+        ws, free = _borrow(_free_workspaces, gemm_workspace, a_codes.device, stream, need)
     _check(lib().fp4_gemm_nvfp4(_ptr(a_codes), _ptr(a_scales), _ptr(a_g), _ptr(b_codes),
                                 _ptr(b_scales), _ptr(b_g), m, n, k, _ptr(out), _dtype_code(out),
-                                _ptr(ws), 0 if ws is None else ws.numel(),
-                                _stream(a_codes.device)))
+                                _ptr(ws), 0 if ws is None else ws.numel(), stream))
+    if free is not None:
+        free.append(ws)
     return out
 
 
@@ -532,15 +585,18 @@ def fp8_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
     if a_scales.device != dev or b_codes.device != dev or b_scales.device != dev or out.device != dev:
         raise ValueError("operands and out must be on one device")
     l, ct = lib(), _dtype_code(out)
+    stream, free = _raw_stream(dev), None
     if ws is None and m > 16:  # at most 16 rows take none
         need = l.fp8_gemm_b128_workspace_bytes(m, n, k, ct)
         if need:
-            ws = gemm_workspace(dev, need)
+            ws, free = _borrow(_free_workspaces, gemm_workspace, dev, stream, need)
     rc = l.fp8_gemm_b128(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), b_kind,
                          m, n, k, out.data_ptr(), ct, None if ws is None else ws.data_ptr(),
-                         0 if ws is None else ws.numel(), _raw_stream(dev))
+                         0 if ws is None else ws.numel(), stream)
     if rc:
         _check(rc)
+    if free is not None:
+        free.append(ws)
     if (a_scales.requires_grad or b_scales.requires_grad) and torch.is_grad_enabled():
         return _NoGradient.apply("fp8_gemm_b128", 1, out.detach(), a_scales, b_scales)
     return out
@@ -594,27 +650,12 @@ def _expert_weights(w: ExpertWeights, rows: int, k: int, what: str, device) -> _
     return _ExpertWeightsC(codes.data_ptr(), scales.data_ptr(), g.data_ptr(), g.numel())
 
 
-def _capturing(dev: torch.device) -> bool:
-    """Whether torch's current stream on `dev` is being captured into a graph."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.device(dev):
-        return torch.cuda.is_current_stream_capturing()
-
-
 def moe_workspace(device, nbytes: int) -> torch.Tensor:
     """A new workspace of `nbytes` for moe_layer, zero where it has to be before the
     first call (the fill is on torch's current stream)."""
-    ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
-
-
-# Workspaces of moe_layer that no call is issuing launches through, by device and stream.
-# Their first 256 bytes are zero once the stream has got there.  A call takes one out while
-# it launches, so that calls from several threads, whose launches may mix, have one each;
-# list.pop and list.append are atomic.
-_moe_free = {}
 
 
 def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: int, top_k: int, *,
@@ -662,22 +703,11 @@ def moe_layer(x: torch.Tensor, w13: ExpertWeights, w2: ExpertWeights, experts: i
     elif out.shape != (tokens, dim) or not out.is_contiguous() or out.device != x.device:
         raise ValueError(f"out must be contiguous, {tokens} x {dim}, on x's device")
     l = lib()
-    stream = _raw_stream(x.device)
-    free = None
+    stream, free = _raw_stream(x.device), None
     if ws is None:
         need = l.moe_layer_workspace_bytes(tokens, dim, inter, experts, top_k)
-        if need and _capturing(x.device):
-            # The graph's own, its counter cleared at each replay: a fill in a capture is only
-            # recorded, and a graph keeps its buffer's address whatever eager calls do later.
-            ws = moe_workspace(x.device, need)
-        elif need:
-            free = _moe_free.setdefault((x.device.index, stream), [])
-            try:
-                ws = free.pop()
-            except IndexError:
-                pass
-            if ws is None or ws.numel() < need:
-                ws = moe_workspace(x.device, need)
+        if need:
+            ws, free = _borrow(_free_moe_workspaces, moe_workspace, x.device, stream, need)
     rc = l.moe_layer(x.data_ptr(), _dtype_code(x), tokens, dim, inter, experts, top_k, w13.fmt, ctypes.byref(a),
                      ctypes.byref(b), None if router is None else router.data_ptr(),
                      0 if router is None else _dtype_code(router), int(renormalize), topk_ids.data_ptr(),
@@ -708,7 +738,7 @@ def fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: int, block: i
     if out is None:
         out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device)
     _check(lib().fp4_dequantize(_ptr(codes), _ptr(scales), fmt, block, _ptr(g), rows, cols,
-                                rotate, _ptr(out), _dtype_code(out), _stream(codes.device)))
+                                rotate, _ptr(out), _dtype_code(out), _raw_stream(codes.device)))
     return out
 
 
@@ -719,11 +749,15 @@ def fp4_block_mse(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fm
     """Error split of stored codes against x; returns (block_mse, stats)."""
     x = _matrix(x)
     _, _, block_mse, stats = _outputs(x, block, codes, scales, block_mse, stats)
-    ws = ws if ws is not None else (_scratch(x) if stats is not None else None)
+    stream, free = _raw_stream(x.device), None
+    if ws is None and stats is not None:
+        ws, free = _scratch(x, stream)
     _check(lib().fp4_block_mse(_ptr(x), _dtype_code(x), _ptr(codes), _ptr(scales), fmt, block,
                                _ptr(g), x.shape[0], x.shape[1], rotate, _ptr(block_mse),
                                mse_kind, _ptr(stats), _ptr(ws), 0 if ws is None else ws.numel(),
-                               _stream(x.device)))
+                               stream))
+    if free is not None:
+        free.append(ws)
     return block_mse, stats
 
 
@@ -734,7 +768,7 @@ def hadamard_block_rotate(x: torch.Tensor, n: int, out: Optional[torch.Tensor] =
     if out is None:
         out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
     _check(lib().hadamard_block_rotate(_ptr(x), _dtype_code(x), x.shape[0], x.shape[1], n,
-                                       _ptr(out), _stream(x.device)))
+                                       _ptr(out), _raw_stream(x.device)))
     return out
 
 

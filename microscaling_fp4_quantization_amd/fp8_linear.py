@@ -20,7 +20,7 @@ import math
 
 import torch
 
-from . import _check, _dtype_code, _raw_stream, gemm_workspace, lib
+from . import _borrow, _check, _dtype_code, _free_workspaces, _raw_stream, gemm_workspace, lib
 
 
 @functools.lru_cache(maxsize=4096)
@@ -50,11 +50,13 @@ class _Fp8Linear(torch.autograd.Function):
         n, need = _sizes(tokens, k, out, xt, wt, want_dx, want_dw)
         saved = x.new_empty(n, dtype=torch.uint8) if n else None
         stream = _raw_stream(dev)
-        ws = gemm_workspace(dev, need)
+        ws, free = _borrow(_free_workspaces, gemm_workspace, dev, stream, need)
         rc = lib().fp8_linear_forward(x.data_ptr(), xt, w.data_ptr(), wt, tokens, k, out, y.data_ptr(), want_dx, want_dw,
                                       None if saved is None else saved.data_ptr(), n, ws.data_ptr(), ws.numel(), stream)
         if rc:
             _check(rc)
+        if free is not None:
+            free.append(ws)
         if want_dx or want_dw:
             ctx.save_for_backward(saved)
             ctx.sizes = shape, tokens, k, out, xt, wt, w.dtype, need
@@ -72,7 +74,7 @@ class _Fp8Linear(torch.autograd.Function):
         dx = dy.new_empty(shape) if want_dx else None
         dw = dy.new_empty((out, k), dtype=w_dtype) if want_dw else None
         stream = _raw_stream(dev)
-        ws = gemm_workspace(dev, need)
+        ws, free = _borrow(_free_workspaces, gemm_workspace, dev, stream, need)
         # An empty gradient has no address of its own: any aligned one stands for it.
         rc = lib().fp8_linear_backward(dy.data_ptr(), xt, wt, tokens, k, out,
                                        (dx.data_ptr() or ws.data_ptr()) if want_dx else None,
@@ -81,6 +83,8 @@ class _Fp8Linear(torch.autograd.Function):
                                        ws.data_ptr(), ws.numel(), stream)
         if rc:
             _check(rc)
+        if free is not None:
+            free.append(ws)
         return dx, dw
 
 
