@@ -32,9 +32,11 @@
 //                    workgroup, K blocks dealt to its waves in turn; bound by the
 //                    read of B, so always on the bf16 form.
 //
-// Measured: 8192 x 18944 x 3584 bf16 486 us (2.29 PFLOP/s; the library's product under
-// one scale per tensor 411), 4096 x 4096 x 14336 186 us (2.59); binary32 C 8192 x 3584
-// x 3584 188 us (1.12 PFLOP/s on the bf16 cores); 1 x 3584 x 18944 14 us (4.9 TB/s of B).
+// Measured: 8192 x 18944 x 3584 bf16 475 to 494 us (2.25 to 2.34 PFLOP/s; 515 on inputs
+// that change from pass to pass, where the library's product under one scale per tensor
+// took 424), 4096 x 4096 x 14336 186 us (2.59), with row scales 14336 x 4096 x 4096 251
+// (1.92); binary32 C 4096 x 14336 x 4096 430 us (1.12 PFLOP/s on the bf16 cores); 1 x 3584
+// x 18944 13.8 us (4.9 TB/s of B).
 // What bounds the large tile: at 4096 x 4096 x 14336, one tile per CU, its cycles are
 // half as many again as the matrix cores need.  Timing copies of it took 143 us without
 // the direct loads into LDS, 147 without the reads of LDS, about 170 with half of either,

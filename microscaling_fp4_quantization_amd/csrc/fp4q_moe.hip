@@ -28,8 +28,10 @@
 // add an error as large as a bf16 output's own) or 3 for a binary32 output.
 //
 // Measured: 64 tokens, 64 experts of 4096 x 1024 in E4M3 (805 MB) 190 us, its two
-// products at 4.7 TB/s; 11 tokens, 8 experts of 4096 x 14336 in NVFP4 (793 MB) 198 us;
-// one token on 8 of 64 experts of 4096 x 1024 in MXFP4 (53 MB) 31 us, of which the
+// products at 4.5 and 5.0 TB/s; 11 tokens, 8 experts of 4096 x 14336 in NVFP4 (793 MB)
+// 189 to 197 us, at 4.4 and 4.0 TB/s with the vector unit, which widens the weights, busy
+// in half of the cycles (E4M3: a seventh);
+// one token on 8 of 64 experts of 4096 x 1024 in MXFP4 (53 MB) 30 us, of which the
 // products 12.5 and 7.3, router 7.7 and combine 4.4: four launches of work too short to
 // fill memory.  (The combine inside the down kernel, by the last workgroup of each 128
 // rows, saved the launch but took 37 us: each workgroup's release writes back its L2.)
