@@ -500,6 +500,63 @@ fp4q_status fp8_linear_backward(const void* dy, int32_t xt, int32_t wt, int64_t 
 size_t fp8_linear_saved_bytes(int64_t tokens, int64_t in, int64_t out, int32_t want_dx, int32_t want_dw);
 size_t fp8_linear_workspace_bytes(int64_t tokens, int64_t in, int64_t out, int32_t xt, int32_t wt);
 
+/*
+ * 8-bit integers with one binary32 scale per row: activations by token, weights by
+ * output channel.
+ *   s = max(RN32(max |x| / 127), 2^-126) of the row
+ *   code = RN32(x / s) to the nearest whole number (-127..127), ties to even
+ *   x           device, rows x cols contiguous, dtype xt; aligned to its element
+ *   codes       device out: rows x ld, ld = cols rounded up to 16 (the padding is
+ *               written, as zeros); 16-byte aligned
+ *   scales      device out: rows floats
+ * Any rows below 2^31 and cols (rows * cols <= (2^31 - 1) * 512); no workspace.  A row that
+ * holds a NaN or an infinity gets that as its scale and codes of 0: on use all of
+ * it is NaN.  Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN, FP4Q_ERR_HIP.
+ */
+fp4q_status int8_quantize_rows(const void* x, int32_t xt, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                               void* stream);
+
+/*
+ * Product of two such operands: C[m][n] = acc sa[m] sb[n] + bias[n], acc = sum over k
+ * of A[m][k] B[n][k].
+ *   a_codes, b_codes    device, M x K and N x K, any values -128..127; 16-byte aligned
+ *   a_scales, b_scales  device, M and N floats
+ *   bias, bt            device, N elements of dtype bt, or NULL
+ *   M, N, K             K % 16 == 0 (the padded row length), K < 2^17 (so that acc is
+ *                       below 2^31), N < 2^21, M < 2^31; M or N == 0 is a no-op; K == 0
+ *                       gives the bias (times NaN or infinite scales: NaN)
+ *   c, ct               device out, M x N, FP4Q_F32 or FP4Q_BF16; aligned to its element
+ *   ws, ws_bytes        int8_gemm_workspace_bytes(M, N, K) bytes (0 for most shapes;
+ *                       then ws may be NULL), 16-byte aligned: sums of K ranges
+ * acc is exact.  It and sa sb are rounded to binary32 and meet in one fused
+ * multiply-add; where sa sb is no normal number, all in binary64, rounded once.  So C
+ * differs from the exact value by at most 3 * 2^-24 of |acc sa sb| and its own
+ * rounding, and an element's bits depend on its own row, column, scales and bias
+ * alone: not on M, N or the rows beside it.  At most 16 rows of A take a kernel that
+ * streams B once; others 64 x 64, 128 x 128 or 256 x 256 tiles, by the shape.
+ * Errors as for fp8_gemm_b128.
+ */
+fp4q_status int8_gemm(const int8_t* a_codes, const float* a_scales, const int8_t* b_codes, const float* b_scales,
+                      const void* bias, int32_t bt, int64_t M, int64_t N, int64_t K, void* c, int32_t ct, void* ws,
+                      size_t ws_bytes, void* stream);
+size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * A linear layer of a served model: y = x W^T + bias for tokens x `in` activations x
+ * and W (out x in) as int8_quantize_rows writes it.  x is quantized by token as that
+ * call does; equal, bit for bit, to it and int8_gemm.
+ *   x, xt; y, yt  tokens x in and tokens x out, contiguous, aligned to their elements
+ *   w_codes       out x (in rounded up to 16); 16-byte aligned
+ *   ws            int8_linear_workspace_bytes() bytes, 256-byte aligned
+ *   in            at most 131056; the other sizes as for int8_gemm
+ * Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN, FP4Q_ERR_WORKSPACE,
+ * FP4Q_ERR_HIP; nothing is launched on one other than FP4Q_ERR_HIP.
+ */
+fp4q_status int8_linear(const void* x, int32_t xt, const int8_t* w_codes, const float* w_scales, const void* bias,
+                        int32_t bt, int64_t tokens, int64_t in, int64_t out, void* y, int32_t yt, void* ws,
+                        size_t ws_bytes, void* stream);
+size_t int8_linear_workspace_bytes(int64_t tokens, int64_t in, int64_t out);
+
 /* One stacked matrix of a layer's expert weights, (experts * rows) x K, exactly as
  * the quantize calls write it. */
 typedef struct {

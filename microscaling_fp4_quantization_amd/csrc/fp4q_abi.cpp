@@ -595,6 +595,108 @@ fp4q_status fp8_linear_backward(const void* dy, int32_t xt, int32_t wt, int64_t 
     return ok();
 }
 
+fp4q_status int8_quantize_rows(const void* x, int32_t xt, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                               void* stream) {
+    const char* fn = "int8_quantize_rows";
+    TRY(check_dtype(fn, xt));
+    if (rows < 0 || cols < 0) return fail(FP4Q_ERR_SHAPE, "%s: negative size %lld x %lld", fn, (long long)rows, (long long)cols);
+    if (rows > 0 && cols > (int64_t)INT32_MAX * 512 / rows)
+        return fail(FP4Q_ERR_SHAPE, "%s: %lld x %lld elements exceed the limit of (2^31 - 1) * 512", fn, (long long)rows, (long long)cols);
+    if (rows > INT32_MAX) return fail(FP4Q_ERR_SHAPE, "%s: %lld rows exceed 2^31 - 1", fn, (long long)rows);
+    if (rows > 0) {
+        if (!scales || (cols > 0 && (!x || !codes))) return fail(FP4Q_ERR_ARG, "%s: x, codes and scales must not be NULL", fn);
+        if (!aligned(x, xt == FP4Q_F32 ? 4 : 2)) return fail(FP4Q_ERR_ALIGN, "%s: x is not aligned to its element", fn);
+        if (!aligned(codes, 16)) return fail(FP4Q_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
+        if (!aligned(scales, 4)) return fail(FP4Q_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+    }
+    char msg[256] = {0};
+    return launched(fp4q::launch_int8_quantize({x, xt, rows, cols, codes, scales, stream}, msg, sizeof msg), msg);
+}
+
+static fp4q_status int8_shape(const char* fn, int64_t M, int64_t N, int64_t K, int32_t ct) {
+    TRY(check_dtype(fn, ct));
+    if (M < 0 || N < 0 || K < 0) return fail(FP4Q_ERR_SHAPE, "%s: negative size", fn);
+    if (K % 16 != 0) return fail(FP4Q_ERR_SHAPE, "%s: K = %lld is not a multiple of 16", fn, (long long)K);
+    if (K >= (int64_t)1 << 17) return fail(FP4Q_ERR_SHAPE, "%s: K = %lld: the sums of 2^17 products may pass 2^31", fn, (long long)K);
+    if (N >= (int64_t)1 << 21) return fail(FP4Q_ERR_SHAPE, "%s: N = %lld exceeds 2^21 - 1", fn, (long long)N);
+    if (M >= (int64_t)1 << 31) return fail(FP4Q_ERR_SHAPE, "%s: M = %lld exceeds 2^31 - 1", fn, (long long)M);
+    return FP4Q_OK;
+}
+
+fp4q_status int8_gemm(const int8_t* a_codes, const float* a_scales, const int8_t* b_codes, const float* b_scales,
+                      const void* bias, int32_t bt, int64_t M, int64_t N, int64_t K, void* c, int32_t ct, void* ws,
+                      size_t ws_bytes, void* stream) {
+    const char* fn = "int8_gemm";
+    TRY(int8_shape(fn, M, N, K, ct));
+    if (bias) TRY(check_dtype(fn, bt));
+    if (M > 0 && N > 0) {
+        if (!c || !a_scales || !b_scales || (K > 0 && (!a_codes || !b_codes)))
+            return fail(FP4Q_ERR_ARG, "%s: codes, scales and c must not be NULL", fn);
+        if (!aligned(a_codes, 16) || !aligned(b_codes, 16)) return fail(FP4Q_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
+        if (!aligned(a_scales, 4) || !aligned(b_scales, 4)) return fail(FP4Q_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+        if (!aligned(c, ct == FP4Q_F32 ? 4 : 2) || !aligned(bias, bt == FP4Q_F32 ? 4 : 2))
+            return fail(FP4Q_ERR_ALIGN, "%s: c and bias must be aligned to their elements", fn);
+        const size_t need = fp4q::int8_gemm_workspace_bytes(M, N, K);
+        if (need > 0 && (!ws || ws_bytes < need))
+            return fail(FP4Q_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
+        if (need > 0 && !aligned(ws, 16)) return fail(FP4Q_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+    }
+    char msg[256] = {0};
+    return launched(fp4q::launch_int8_gemm({a_codes, a_scales, b_codes, b_scales, bias, bt, M, N, K, c, ct, ws, stream}, msg, sizeof msg), msg);
+}
+
+size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || int8_shape("int8_gemm_workspace_bytes", M, N, K, FP4Q_BF16) != FP4Q_OK) return 0;
+    return fp4q::int8_gemm_workspace_bytes(M, N, K);
+}
+
+// A linear layer: the codes and scales of x in the workspace, then the product's own part.
+namespace {
+struct Int8Linear {
+    int8_t* codes;
+    float* scales;
+    void* product;
+    size_t product_bytes, bytes;
+    Int8Linear(void* p, int64_t M, int64_t K, int64_t N) {
+        Carve c{static_cast<char*>(p)};
+        codes = static_cast<int8_t*>(c.take((size_t)(M * up16(K))));
+        scales = static_cast<float*>(c.take((size_t)(4 * M)));
+        product_bytes = M > 0 && N > 0 ? fp4q::int8_gemm_workspace_bytes(M, N, up16(K)) : 0;
+        product = c.take(product_bytes);
+        bytes = c.used;
+    }
+};
+}  // namespace
+
+fp4q_status int8_linear(const void* x, int32_t xt, const int8_t* w_codes, const float* w_scales, const void* bias,
+                        int32_t bt, int64_t tokens, int64_t in, int64_t out, void* y, int32_t yt, void* ws,
+                        size_t ws_bytes, void* stream) {
+    const char* fn = "int8_linear";
+    TRY(check_dtype(fn, xt));
+    if (in < 0 || in > (int64_t)1 << 17) return fail(FP4Q_ERR_SHAPE, "%s: %lld inputs: 0 to 131056 are taken", fn, (long long)in);
+    TRY(int8_shape(fn, tokens, out, up16(in), yt));
+    if (bias) TRY(check_dtype(fn, bt));
+    if (tokens == 0 || out == 0) return ok();
+    if ((in > 0 && (!x || !w_codes)) || !w_scales || !y)
+        return fail(FP4Q_ERR_ARG, "%s: x, codes, scales and y must not be NULL", fn);
+    if (!aligned(x, xt == FP4Q_F32 ? 4 : 2) || !aligned(y, yt == FP4Q_F32 ? 4 : 2) || !aligned(bias, bt == FP4Q_F32 ? 4 : 2))
+        return fail(FP4Q_ERR_ALIGN, "%s: x, bias and y must be aligned to their elements", fn);
+    if (!aligned(w_codes, 16) || !aligned(w_scales, 4))
+        return fail(FP4Q_ERR_ALIGN, "%s: codes must be 16-byte and scales 4-byte aligned", fn);
+    const Int8Linear l(ws, tokens, in, out);
+    TRY(linear_buffer(fn, "a workspace", ws, ws_bytes, l.bytes));
+    char msg[256] = {0};
+    TRY(launched(fp4q::launch_int8_quantize({x, xt, tokens, in, l.codes, l.scales, stream}, msg, sizeof msg), msg));
+    return launched(fp4q::launch_int8_gemm({l.codes, l.scales, w_codes, w_scales, bias, bt, tokens, out, up16(in), y, yt, l.product, stream}, msg, sizeof msg), msg);
+}
+
+size_t int8_linear_workspace_bytes(int64_t tokens, int64_t in, int64_t out) {
+    if (in < 0 || in > (int64_t)1 << 17 || int8_shape("int8_linear_workspace_bytes", tokens, out, up16(in), FP4Q_BF16) != FP4Q_OK ||
+        tokens == 0 || out == 0)
+        return 0;
+    return Int8Linear(nullptr, tokens, in, out).bytes;
+}
+
 static fp4q_status moe_weights(const char* fn, const char* what, const fp4q_expert_weights* w, int32_t fmt,
                                int64_t experts, fp4q::MoeWeights& out) {
     if (!w) return fail(FP4Q_ERR_ARG, "%s: %s must not be NULL", fn, what);

@@ -145,6 +145,33 @@ struct Fp8GemmJob {
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int ct);
 
+// 8-bit integers with a binary32 scale per row.
+struct Int8QuantJob {
+    const void* x;
+    int xt;            // 0 bf16, 1 f32
+    int64_t rows, cols;
+    int8_t* codes;
+    float* scales;
+    void* stream;
+};
+
+// Product of two such operands, with a bias per column.
+struct Int8GemmJob {
+    const int8_t* a_codes;
+    const float* a_scales;
+    const int8_t* b_codes;
+    const float* b_scales;
+    const void* bias;  // nullable
+    int bt;            // 0 bf16, 1 f32
+    int64_t M, N, K;
+    void* c;
+    int ct;            // 0 bf16, 1 f32
+    void* ws;          // int8_gemm_workspace_bytes(M, N, K) bytes: sums of K ranges
+    void* stream;
+};
+
+size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 // Mixture-of-experts layer for a few tokens.
 struct MoeWeights {
     const uint8_t* codes;  // (E * rows) x K
@@ -218,6 +245,8 @@ int launch_fp8_quantize(const Fp8QuantJob& j, char* msg, size_t msg_len);
 // x under row scales and w under tile scales: one launch where both outputs of both are wanted.
 int launch_fp8_quantize_two(const Fp8QuantJob& x, const Fp8QuantJob& w, char* msg, size_t msg_len);
 int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len);
+int launch_int8_quantize(const Int8QuantJob& j, char* msg, size_t msg_len);
+int launch_int8_gemm(const Int8GemmJob& j, char* msg, size_t msg_len);
 int launch_moe(const MoeJob& j, char* msg, size_t msg_len);
 
 // Adds the binary32 partial products of `splits` K ranges (splits x count, range
