@@ -547,7 +547,9 @@ size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * call does; equal, bit for bit, to it and int8_gemm.
  *   x, xt; y, yt  tokens x in and tokens x out, contiguous, aligned to their elements
  *   w_codes       out x (in rounded up to 16); 16-byte aligned
- *   ws            int8_linear_workspace_bytes() bytes, 256-byte aligned
+ *   ws            int8_linear_workspace_bytes() bytes (0 for one token of up to 32768
+ *                 values and up to 4096 outputs, which takes one launch; then ws may be
+ *                 NULL), 256-byte aligned
  *   in            at most 131056; the other sizes as for int8_gemm
  * Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN, FP4Q_ERR_WORKSPACE,
  * FP4Q_ERR_HIP; nothing is launched on one other than FP4Q_ERR_HIP.

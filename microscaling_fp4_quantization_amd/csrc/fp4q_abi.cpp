@@ -657,10 +657,12 @@ struct Int8Linear {
     float* scales;
     void* product;
     size_t product_bytes, bytes;
+    bool one;  // in one launch, without codes in memory
     Int8Linear(void* p, int64_t M, int64_t K, int64_t N) {
         Carve c{static_cast<char*>(p)};
-        codes = static_cast<int8_t*>(c.take((size_t)(M * up16(K))));
-        scales = static_cast<float*>(c.take((size_t)(4 * M)));
+        one = fp4q::int8_linear_in_one(M, N, up16(K));
+        codes = one ? nullptr : static_cast<int8_t*>(c.take((size_t)(M * up16(K))));
+        scales = one ? nullptr : static_cast<float*>(c.take((size_t)(4 * M)));
         product_bytes = M > 0 && N > 0 ? fp4q::int8_gemm_workspace_bytes(M, N, up16(K)) : 0;
         product = c.take(product_bytes);
         bytes = c.used;
@@ -686,6 +688,8 @@ fp4q_status int8_linear(const void* x, int32_t xt, const int8_t* w_codes, const 
     const Int8Linear l(ws, tokens, in, out);
     TRY(linear_buffer(fn, "a workspace", ws, ws_bytes, l.bytes));
     char msg[256] = {0};
+    if (l.one)
+        return launched(fp4q::launch_int8_gemm({nullptr, nullptr, w_codes, w_scales, bias, bt, tokens, out, up16(in), y, yt, nullptr, stream, xt, x, in}, msg, sizeof msg), msg);
     TRY(launched(fp4q::launch_int8_quantize({x, xt, tokens, in, l.codes, l.scales, stream}, msg, sizeof msg), msg));
     return launched(fp4q::launch_int8_gemm({l.codes, l.scales, w_codes, w_scales, bias, bt, tokens, out, up16(in), y, yt, l.product, stream}, msg, sizeof msg), msg);
 }

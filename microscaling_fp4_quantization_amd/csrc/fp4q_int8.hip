@@ -185,13 +185,16 @@ __device__ __forceinline__ float bias_at(const I8Params& p, int64_t n) {
 template <int T>
 struct Ends {
     float sa[T], sb[T], bias[T];
-    __device__ __forceinline__ void load(const I8Params& p, int64_t m0, int64_t n0) {
-        for (int t = threadIdx.x; t < T; t += 256) {
-            const int64_t n = min(n0 + t, p.N - 1);
-            sa[t] = p.sa[min(m0 + t, p.M - 1)];
-            sb[t] = p.sb[n];
-            bias[t] = bias_at(p, n);
-        }
+    // Of 256 threads, each brings (T < 256: the first T do) one row's and one column's.
+    __device__ __forceinline__ void fetch(float (&v)[3], const I8Params& p, int64_t m0, int64_t n0) const {
+        const int t = threadIdx.x % T;
+        const int64_t n = min(n0 + t, p.N - 1);
+        v[0] = p.sa[min(m0 + t, p.M - 1)];
+        v[1] = p.sb[n];
+        v[2] = bias_at(p, n);
+    }
+    __device__ __forceinline__ void put(const float (&v)[3]) {
+        if (threadIdx.x < T) sa[threadIdx.x] = v[0], sb[threadIdx.x] = v[1], bias[threadIdx.x] = v[2];
     }
 };
 
@@ -255,146 +258,340 @@ __device__ __forceinline__ void tile_at(unsigned g, int64_t rows, int64_t cols, 
     n0 = (int64_t)__builtin_amdgcn_readfirstlane(n) * side;
 }
 
-// A 256 x 256 tile of C by four waves of 128 x 128, one per SIMD, whose sums fill half of its
-// registers: such a wave reads 32 KB of LDS for its 2048 cycles of products per K block, where
-// eight waves of 128 x 64 read 192 KB together, as long as the products take.  A K block (128
-// bytes per row, a cache line) per stage, two stages.  The operands of the next half block are
-// read while this half's products run, so that a stage is free half a block before its products
-// end: one barrier per block, and loads go out a block and a half before they are read.
+// Tiles of 256 x 256 (F = 8) by four waves of 128 x 128, one per SIMD, whose sums fill half of
+// its registers: such a wave reads 32 KB of LDS for its 2048 cycles of products per K block,
+// where eight waves of 128 x 64 read 192 KB together, as long as the products take.  A K block
+// (128 bytes per row, a cache line) per stage, two stages.  The operands of the next half block
+// are read while this half's products run, so that a stage is free half a block before its
+// products end: one barrier per block, and loads go out a block and a half before they are read.
+// Workgroups are persistent: a tile's first two stages are loaded while the tile before is
+// scaled and stored, straight from registers, so that LDS is free.
+//
+// For that a lane's columns are neighbours: fragment i of a wave's B holds at position r its row
+// 4 F (r / 4) + 4 i + r % 4, so that lane l ends up with columns 4 F (l / 16) .. + 4 F - 1 of row
+// l % 16 of each fragment of A.  B's slots in LDS go by ((row / 2) % 2 + 2 (row / 4 F)) % 8 in the
+// place of (row / 2) % 8, which keeps the rows that are read together in distinct banks.
 constexpr int kBigThreads = 256;
-constexpr int kBigF = 8;                            // fragments of 16 rows per wave and side
-constexpr int kBigLoads = (BM + BN) / 8 / 4;        // direct loads per wave and stage
+constexpr int kSpread = 4096;                       // LDS bytes that a wave spreads its rows through
 
-template <int EB>
-__device__ __forceinline__ void store_big(const v4i (&acc)[kBigF][kBigF], const Ends<256>& ends, bool partial, uint8_t* lds, void* c,
-                                          Rsrc rc, int wave, int lane, int64_t rows_a, int64_t n0, int64_t N, bool whole) {
-    typedef EpiPlan<EB> P;
-    const int wm = wave / 2, wn = wave % 2;
-#pragma unroll
-    for (int h = 0; h < P::kPasses; ++h) {
-        if (wm * WM / P::kRowsPass == h)
-            finish(acc, ends, partial, wm * WM, wn * 128, lane, [&](int i, int j, v4f v) {
-                put_quad<EB>(lds, wm * WM + j * kF16 + lane % kF16 - h * P::kRowsPass, (wn * 128 + i * kF16) / 4 + lane / kF16, v[0],
-                             v[1], v[2], v[3]);
-            });
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {  // four waves in place of eight
-            if (whole) store_pass<EB>(lds, h, c, rc, wave * 2 + k, lane, rows_a, n0, N, true);
-            else store_pass<EB>(lds, h, c, rc, wave * 2 + k, lane, rows_a, n0, N, false);
-        }
-        if (h + 1 < P::kPasses) __syncthreads();
-    }
-}
-
-__global__ __launch_bounds__(kBigThreads, 1) void k_gemm_i8(I8Params p) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kCodeBytes + sizeof(Ends<256>)];
-    Ends<256>& ends = *reinterpret_cast<Ends<256>*>(lds + 2 * kCodeBytes);
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wm = wave / 2, wn = wave % 2;
-    const int splits = p.splits;
-    const unsigned group = p.first + blockIdx.x;
-    const int split = __builtin_amdgcn_readfirstlane(group % (unsigned)splits);
+// One tile (of one K range) of a product.
+template <int F>
+struct BigTile {
+    static constexpr int T = 32 * F;               // rows and columns
+    static constexpr int kStage = 2 * T * kRowStage;
+    static constexpr int kLoads = 2 * T / 8 / 4;   // direct loads per wave and stage
     int64_t m0, n0;
-    tile_at(group / (unsigned)splits, p.M, p.N, BM, m0, n0);
-    const int64_t rows_a = p.M - m0 < BM ? p.M - m0 : BM;
-    const int64_t rows_b = p.N - n0 < BN ? p.N - n0 : BN;
-    const int K = (int)p.K, S = p.S;
-    const int per = __builtin_amdgcn_readfirstlane((S + splits - 1) / splits);
-    const int s_lo = split * per, s_hi = s_lo + per < S ? s_lo + per : S;
-    const Rsrc ra = make_rsrc(p.a + m0 * K, rows_a * K);
-    const Rsrc rb = make_rsrc(p.b + n0 * K, rows_b * K);
-    // Load q of a wave moves rows 8 d .. 8 d + 7, d = wave + 4 (q % 8), of A (q < 8) or B, into
-    // the slots of op_offset: lane l row 8 d + l / 8, slot l % 8.
-    const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
-    const int lane_off = (lane / 8) * K + piece * 16;
-    auto issue = [&](int s, int q) {
-        const int k0 = s * kBlock;
-        const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
-        const int d = wave + 4 * (q % (kBigLoads / 2));
-        uint8_t* dst = lds + (s & 1) * kCodeBytes + (q < kBigLoads / 2 ? 0 : BM * kRowStage) + d * 8 * kRowStage;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < kBigLoads / 2 ? ra : rb, (LdsPtr)dst, 16, base + 8 * d * K, 0, 0, 0);
-    };
-    v4i acc[kBigF][kBigF];
-#pragma unroll
-    for (int i = 0; i < kBigF; ++i)
-#pragma unroll
-        for (int j = 0; j < kBigF; ++j) acc[i][j] = v4i{};
-    const int a_row = wm * WM + lane % kF16, b_row = wn * 128 + lane % kF16;
-    int a_at[2], b_at[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        a_at[h] = op_offset(a_row, lane, h);
-        b_at[h] = BM * kRowStage + op_offset(b_row, lane, h);
+    int rows_a, rows_b, s_lo, s_hi, split;
+    Rsrc ra, rb;
+
+    __device__ __forceinline__ BigTile(const I8Params& p, int64_t m, int64_t n, int range) : m0(m), n0(n), split(range) {
+        rows_a = (int)(p.M - m0 < T ? p.M - m0 : T);
+        rows_b = (int)(p.N - n0 < T ? p.N - n0 : T);
+        const int per = __builtin_amdgcn_readfirstlane((p.S + p.splits - 1) / p.splits);
+        s_lo = split * per;
+        s_hi = s_lo + per < p.S ? s_lo + per : p.S;
+        ra = make_rsrc(p.a + m0 * p.K, (int64_t)rows_a * p.K);
+        rb = make_rsrc(p.b + n0 * p.K, (int64_t)rows_b * p.K);
     }
-    auto read = [&](const uint8_t* at, int frag) { return *reinterpret_cast<const v4i*>(at + frag * kF16 * kRowStage); };
-    v4i a[2][kBigF], b[2][kBigF];
-    ends.load(p, m0, n0);
-    if (s_lo < s_hi) {  // K = 0 has no operands to read
+    // Load q of a stage moves rows 8 d .. 8 d + 7, d = wave + 4 (q % half), of A (the first half
+    // of the loads) or B: lane l row 8 d + l / 8, slot l % 8.  `at` holds the lane's offset of each
+    // load, so that the loop over K moves nothing but the stage's scalar offset.
+    int at[kLoads];
+    __device__ __forceinline__ void offsets(int K, int wave, int lane) {
 #pragma unroll
-        for (int q = 0; q < kBigLoads; ++q) issue(s_lo, q);
-#pragma unroll
-        for (int q = 0; q < kBigLoads; ++q) issue(s_lo + 1, q);
-        // Both stages have landed.  The zeros of the sums are written before the pause: the
-        // compiler does not know the products below for matrix instructions.
-#pragma unroll
-        for (int i = 0; i < kBigF; ++i)
-#pragma unroll
-            for (int j = 0; j < kBigF; ++j) asm volatile("" : "+a"(acc[i][j]));
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_nop 15\n\ts_barrier" ::: "memory");
-        const uint8_t* here = lds + (s_lo & 1) * kCodeBytes;
-#pragma unroll
-        for (int i = 0; i < kBigF; ++i) b[0][i] = read(here + b_at[0], i);
-#pragma unroll
-        for (int j = 0; j < kBigF; ++j) a[0][j] = read(here + a_at[0], j);
+        for (int q = 0; q < kLoads; ++q) at[q] = (8 * load_row(q, wave) + lane / 8) * K + 16 * load_piece(q, wave, lane);
     }
-    for (int s = s_lo; s < s_hi; ++s) {
-        const uint8_t* here = lds + (s & 1) * kCodeBytes;
-        const uint8_t* next = lds + (~s & 1) * kCodeBytes;
+    static __device__ __forceinline__ int load_row(int q, int wave) { return wave + 4 * (q % (kLoads / 2)); }
+    static __device__ __forceinline__ int load_piece(int q, int wave, int lane) {
+        return (lane % 8) ^ (q < kLoads / 2 ? 4 * (wave & 1) + lane / 16 : lane / 16 % 2 + 2 * (2 * load_row(q, wave) / F % 4));
+    }
+    // The last stage of K: pieces past it are not read (zeros take their place).
+    __device__ __forceinline__ void cut(int K, int s, int wave, int lane) {
+        if (__builtin_expect((s + 1) * kBlock <= K || s >= s_hi, 1)) return;
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) at[q] = s * kBlock + 16 * load_piece(q, wave, lane) < K ? at[q] : kPastWindow;
+    }
+    // (s >= s_hi: nothing is read.)
+    __device__ __forceinline__ void issue(uint8_t* lds, int wave, int s, int q) const {
+        const bool is_a = q < kLoads / 2;
+        uint8_t* dst = lds + (s & 1) * kStage + (is_a ? 0 : T * kRowStage) + load_row(q, wave) * 8 * kRowStage;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (LdsPtr)dst, 16, at[q], s < s_hi ? s * kBlock : kPastWindow, 0, 0);
+    }
+    __device__ __forceinline__ void first_stages(uint8_t* lds, int K, int wave, int lane) {
+        if (s_lo >= s_hi) return;  // K = 0 has no operands to read
+        offsets(K, wave, lane);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            cut(K, s_lo + n, wave, lane);
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) issue(lds, wave, s_lo + n, q);
+        }
+    }
+    // The sums, from two stages that have landed.
+    __device__ __forceinline__ void sums(v4i (&acc)[F][F], uint8_t* lds, int K, int wave, int lane) {
+        const int r = lane % kF16, wm = wave / 2, wn = wave % 2;
+        const int a_row = wm * 16 * F + r, b_row = wn * 16 * F + 4 * F * (r / 4) + r % 4;
+        int a_at[2], b_at[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (h == 1) {
-                // The next stage has landed, and no wave reads this one any more.
-                __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-                asm volatile("s_barrier" ::: "memory");
-            }
-            const uint8_t* from = h == 0 ? here : next;
+            a_at[h] = op_offset(a_row, lane, h);
+            const int slot = (lane / kF16 + 4 * h) ^ (r / 2 % 2 + 2 * (r / 4));
+            b_at[h] = T * kRowStage + b_row * kRowStage + slot * 16;
+        }
+        auto read_a = [&](const uint8_t* stage, int h, int j) { return *reinterpret_cast<const v4i*>(stage + a_at[h] + j * kF16 * kRowStage); };
+        auto read_b = [&](const uint8_t* stage, int h, int i) { return *reinterpret_cast<const v4i*>(stage + b_at[h] + i * 4 * kRowStage); };
 #pragma unroll
-            for (int j = 0; j < kBigF; ++j) {
-                __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < F; ++i)
 #pragma unroll
-                for (int i = 0; i < kBigF; ++i) {
-                    mma_in_place(acc[i][j], b[h][i], a[h][j]);
-                    if (i == 1) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        b[1 - h][j] = read(from + b_at[1 - h], j);
-                        a[1 - h][j] = read(from + a_at[1 - h], j);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                    if (h == 1 && i == 4) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        issue(s + 2, 2 * j);
-                        issue(s + 2, 2 * j + 1);
-                        __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < F; ++j) acc[i][j] = v4i{};
+        // The zeros are written before the pause: the compiler does not know the products below
+        // for matrix instructions.
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j) asm volatile("" : "+a"(acc[i][j]));
+        asm volatile("s_nop 15" ::: "memory");
+        if (s_lo >= s_hi) return;
+        v4i a[2][F], b[2][F];
+        {
+            const uint8_t* here = lds + (s_lo & 1) * kStage;
+#pragma unroll
+            for (int i = 0; i < F; ++i) b[0][i] = read_b(here, 0, i);
+#pragma unroll
+            for (int j = 0; j < F; ++j) a[0][j] = read_a(here, 0, j);
+        }
+        for (int s = s_lo; s < s_hi; ++s) {
+            const uint8_t* here = lds + (s & 1) * kStage;
+            const uint8_t* next = lds + (~s & 1) * kStage;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1) {
+                    // The next stage has landed, and no wave reads this one any more.
+                    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+                    asm volatile("s_barrier" ::: "memory");
+                    cut(K, s + 2, wave, lane);
+                }
+                const uint8_t* from = h == 0 ? here : next;
+#pragma unroll
+                for (int j = 0; j < F; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < F; ++i) {
+                        mma_in_place(acc[i][j], b[h][i], a[h][j]);
+                        if (i == 1) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            b[1 - h][j] = read_b(from, 1 - h, j);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                        if (i == F / 2 + 1) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            a[1 - h][j] = read_a(from, 1 - h, j);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                        if (h == 1 && i % 4 == 3) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            constexpr int kEach = kLoads * 4 / (F * F);
+#pragma unroll
+                            for (int e = 0; e < kEach; ++e) issue(lds, wave, s + 2, (j * (F / 4) + i / 4) * kEach + e);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
                     }
                 }
             }
         }
+        // The last products are done before their sums are read.
+        asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j) asm volatile("" : "+a"(acc[i][j]));
     }
-    // LDS is reused below, and the last products are done before their sums are read.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_nop 15\n\ts_nop 15\n\ts_barrier" ::: "memory");
+    // A sum out of its accumulation register.  (Left to the compiler, all of them moved at once.)
+    static __device__ __forceinline__ int sum_of(const v4i& c, int e) {
+        int v;
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(c[e]));
+        return v;
+    }
+    // The values of the sums (PARTIAL: the sums) to memory, EB bytes each, 16 bytes a store.
+    // HOW: 0 C's rows start on 16 bytes, 1 they do not, 2 element by element and by value()'s
+    // full form, for a tile whose rows end inside 16 bytes or whose scales need it.
+    template <int EB, bool PARTIAL, int HOW>
+    __device__ __forceinline__ void store(const v4i (&acc)[F][F], const I8Params& p, const Ends<T>& ends, uint8_t* spread, int wave, int lane) const {
+        typedef uint32_t Unit __attribute__((ext_vector_type(4), aligned(2)));
+        const int wm = wave / 2, wn = wave % 2, r = lane % kF16, q = lane / kF16, col = wn * 16 * F + 4 * F * q;
+        char* c = PARTIAL ? reinterpret_cast<char*>(p.partial + (int64_t)split * p.M * p.N) : static_cast<char*>(p.c);
+        c += m0 * p.N * EB;
+        const Rsrc rc = make_rsrc(c, rows_a * p.N * EB);
+        v4f sb[F], bias[F];
 #pragma unroll
-    for (int i = 0; i < kBigF; ++i)
+        for (int i = 0; i < F; ++i) {
+            sb[i] = *reinterpret_cast<const v4f*>(ends.sb + col + 4 * i);
+            bias[i] = *reinterpret_cast<const v4f*>(ends.bias + col + 4 * i);
+        }
+        float sa;
+        auto at = [&](int i, int j, int e) {
+            const int sum = sum_of(acc[i][j], e);
+            if (PARTIAL) return __int_as_float(sum);
+            return HOW == 2 ? value(sum, sa, sb[i][e], bias[i][e]) : fmaf((float)sum, sa * sb[i][e], bias[i][e]);
+        };
+        if (HOW == 2) {
 #pragma unroll
-        for (int j = 0; j < kBigF; ++j) asm volatile("" : "+a"(acc[i][j]));
-    void* c = splits > 1 ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.c;
-    const int ct = splits > 1 ? 1 : p.ct;
-    void* tile = static_cast<char*>(c) + m0 * p.N * (ct == 1 ? 4 : 2);
-    const Rsrc rc = make_rsrc(tile, rows_a * p.N * (ct == 1 ? 4 : 2));
-    const bool whole = splits > 1 ? (p.N & 3) == 0 : p.whole;
-    if (ct == 1) store_big<4>(acc, ends, splits > 1, lds, tile, rc, wave, lane, rows_a, n0, p.N, whole);
-    else store_big<2>(acc, ends, false, lds, tile, rc, wave, lane, rows_a, n0, p.N, whole);
+            for (int j = 0; j < F; ++j) {
+                const int row = wm * 16 * F + j * kF16 + r;
+                sa = ends.sa[row];
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int n = col + 4 * i + e, off = row < rows_a && n < rows_b ? (int)((row * p.N + n0 + n) * EB) : kDropped;
+                        const float v = at(i, j, e);
+                        if (EB == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rc, off, 0, 0);
+                        else __builtin_amdgcn_raw_buffer_store_b16((unsigned short)pack_bf16x2(v, v), rc, off, 0, 0);
+                    }
+                __builtin_amdgcn_sched_barrier(0);  // few values in flight
+            }
+            return;
+        }
+        // The rows of a fragment of A go through the wave's own 4 KB of LDS, kRows in a step, so
+        // that a store covers whole lines.  (A lane's 64 bytes stored by itself, 16 at a time, took
+        // 170 us for 8192 x 16384 bf16, half as long as its products.)  Unit u of row r sits at
+        // u ^ r: a write's rows and a read's units fall in distinct banks.
+        constexpr int kUnits = F * EB;                       // of 16 bytes, in a row of the wave
+        constexpr int kMine = F * EB / 4;                    // those of a lane
+        constexpr int kPerRead = kWave / kUnits;             // rows
+        constexpr int kReads = kPerRead < 8 ? 4 : 2;
+        constexpr int kRows = kReads * kPerRead;             // in a step
+        constexpr int kSteps = F * 16 / kRows;
+        static_assert(kRows <= 16 && kRows * kUnits * 16 <= kSpread, "a step is part of a fragment");
+        u32x4_t w[kReads], v[kMine];
+        auto store_step = [&](int step) {
+#pragma unroll
+            for (int t = 0; t < kReads; ++t) {
+                const int m = wm * 16 * F + step * kRows + t * kPerRead + lane / kUnits, n = wn * 16 * F + lane % kUnits * (16 / EB);
+                const bool in = m < rows_a && n < rows_b;
+                const int64_t off = ((int64_t)m * p.N + n0 + n) * EB;
+                if (HOW == 0) __builtin_amdgcn_raw_buffer_store_b128(w[t], rc, in ? (int)off : kDropped, 0, kStoreNT);
+                else if (in) *reinterpret_cast<Unit*>(c + off) = w[t];
+            }
+        };
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) {
+            __builtin_amdgcn_sched_barrier(0);  // few values in flight
+            const int j = step * kRows / 16, h = step % (16 / kRows);
+            if (h == 0) {
+                sa = PARTIAL ? 0.0f : ends.sa[wm * 16 * F + j * kF16 + r];
+#pragma unroll
+                for (int k = 0; k < kMine; ++k)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        v[k][u] = EB == 4 ? __float_as_uint(at(k, j, u))
+                                          : pack_bf16x2(at(2 * k + u / 2, j, u % 2 * 2), at(2 * k + u / 2, j, u % 2 * 2 + 1));
+            }
+            if (r / kRows == h) {
+#pragma unroll
+                for (int k = 0; k < kMine; ++k)
+                    *reinterpret_cast<u32x4_t*>(spread + (r % kRows * kUnits + ((q * kMine + k) ^ r) % kUnits) * 16) = v[k];
+            }
+            asm volatile("" ::: "memory");  // (a wave's LDS accesses run in order)
+#pragma unroll
+            for (int t = 0; t < kReads; ++t) {
+                const int rr = t * kPerRead + lane / kUnits, u = lane % kUnits;
+                w[t] = *reinterpret_cast<const u32x4_t*>(spread + (rr * kUnits + (u ^ (h * kRows + rr)) % kUnits) * 16);
+            }
+            asm volatile("" ::: "memory");
+            store_step(step);
+        }
+    }
+    template <int EB, bool PARTIAL>
+    __device__ __forceinline__ void store(const v4i (&acc)[F][F], const I8Params& p, const Ends<T>& ends, uint8_t* spread, int wave, int lane) const {
+        const bool whole = PARTIAL ? (p.N & 3) == 0 : p.whole;
+        // Whether every product of two scales is a normal number: then the first form of value() alone.
+        bool normal = true;
+        if (!PARTIAL) {
+            float lo_a = __builtin_inff(), hi_a = 0.0f, lo_b = lo_a, hi_b = 0.0f;
+            for (int t = lane; t < T; t += kWave) {
+                lo_a = __builtin_elementwise_minimum(lo_a, fabsf(ends.sa[t])), hi_a = __builtin_elementwise_maximum(hi_a, fabsf(ends.sa[t]));
+                lo_b = __builtin_elementwise_minimum(lo_b, fabsf(ends.sb[t])), hi_b = __builtin_elementwise_maximum(hi_b, fabsf(ends.sb[t]));
+            }
+#pragma unroll
+            for (int d = 1; d < kWave; d *= 2) {
+                lo_a = __builtin_elementwise_minimum(lo_a, __shfl_xor(lo_a, d)), hi_a = __builtin_elementwise_maximum(hi_a, __shfl_xor(hi_a, d));
+                lo_b = __builtin_elementwise_minimum(lo_b, __shfl_xor(lo_b, d)), hi_b = __builtin_elementwise_maximum(hi_b, __shfl_xor(hi_b, d));
+            }
+            normal = __builtin_amdgcn_ballot_w64(!(lo_a * lo_b >= 0x1p-126f && hi_a * hi_b < __builtin_inff())) == 0;
+        }
+        asm volatile("" : "+v"(lane));  // addresses are formed here, not kept through the sums
+        if (normal && whole) store<EB, PARTIAL, 0>(acc, p, ends, spread, wave, lane);
+        else if (normal && rows_b % (16 / EB) == 0) store<EB, PARTIAL, 1>(acc, p, ends, spread, wave, lane);
+        else store<EB, PARTIAL, 2>(acc, p, ends, spread, wave, lane);
+    }
+};
+
+template <int F>
+__device__ __forceinline__ void store_any(const BigTile<F>& tile, const v4i (&acc)[F][F], const I8Params& p, const Ends<32 * F>& ends,
+                                          uint8_t* spread, int wave, int lane) {
+    if (p.splits > 1) tile.template store<4, true>(acc, p, ends, spread, wave, lane);
+    else if (p.ct == 1) tile.template store<4, false>(acc, p, ends, spread, wave, lane);
+    else tile.template store<2, false>(acc, p, ends, spread, wave, lane);
+}
+
+// Items: a tile and a K range each, dealt to the workgroups in turn.  `quarters`: the last so many
+// tiles (without K ranges), too few to give each workgroup one, go out as four tiles of 128 x 128
+// each, one to a workgroup.
+__global__ __launch_bounds__(kBigThreads, 1) void k_gemm_i8(I8Params p, unsigned items, unsigned quarters) {
+    typedef BigTile<8> Tile;
+    typedef BigTile<4> Quarter;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * Tile::kStage + sizeof(Ends<Tile::T>) + 4 * kSpread];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int K = (int)p.K;
+    uint8_t* spread = lds + 2 * Tile::kStage + sizeof(Ends<Tile::T>) + wave * kSpread;
+    float end[3];
+    if (blockIdx.x < items) {
+        Ends<Tile::T>& ends = *reinterpret_cast<Ends<Tile::T>*>(lds + 2 * Tile::kStage);
+        auto item = [&](unsigned g) {
+            int64_t m0, n0;
+            tile_at(g / (unsigned)p.splits, p.M, p.N, Tile::T, m0, n0);
+            return Tile(p, m0, n0, __builtin_amdgcn_readfirstlane(g % (unsigned)p.splits));
+        };
+        Tile tile = item(blockIdx.x);
+        tile.first_stages(lds, K, wave, lane);
+        ends.fetch(end, p, tile.m0, tile.n0);
+        for (unsigned g = blockIdx.x; g < items; g += gridDim.x) {
+            ends.put(end);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // both stages have landed
+            v4i acc[8][8];
+            tile.sums(acc, lds, K, wave, lane);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // no wave reads or fills a stage any more
+            const Tile done = tile;
+            if (g + gridDim.x < items) {
+                tile = item(g + gridDim.x);
+                tile.first_stages(lds, K, wave, lane);
+                ends.fetch(end, p, tile.m0, tile.n0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            store_any<8>(done, acc, p, ends, spread, wave, lane);
+            __syncthreads();  // `ends` is read before the next tile's take its place
+        }
+    }
+    // Quarters of one tile go to workgroups 8 apart: to one XCD.
+    const unsigned left = blockIdx.x / 32 * 8 + blockIdx.x % 8, quarter = blockIdx.x / 8 % 4;
+    if (left >= quarters) return;
+    int64_t m0, n0;
+    tile_at(items + left, p.M, p.N, Tile::T, m0, n0);
+    m0 += quarter / 2 * Quarter::T;
+    n0 += quarter % 2 * Quarter::T;
+    if (m0 >= p.M || n0 >= p.N) return;
+    Ends<Quarter::T>& ends = *reinterpret_cast<Ends<Quarter::T>*>(lds + 2 * Tile::kStage);
+    Quarter tile(p, m0, n0, 0);
+    tile.first_stages(lds, K, wave, lane);
+    ends.fetch(end, p, m0, n0);
+    ends.put(end);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    v4i acc[4][4];
+    tile.sums(acc, lds, K, wave, lane);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    store_any<4>(tile, acc, p, ends, spread, wave, lane);
 }
 
 // Tiles of T x T (128 or 64), four waves of T / 2 x T / 2 through two LDS stages; several
@@ -452,7 +649,9 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_i8_mid(I8Params 
     const int b_lo = T * kRowStage + op_offset(b_row, lane, 0), b_hi = T * kRowStage + op_offset(b_row, lane, 1);
     Ends<T>& ends = *reinterpret_cast<Ends<T>*>(lds + P::kTile);
     if (s_lo < s_hi) issue(s_lo);
-    ends.load(p, m0, n0);
+    float end[3];
+    ends.fetch(end, p, m0, n0);
+    ends.put(end);
     for (int s = s_lo; s < s_hi; ++s) {
         const uint8_t* here = lds + (s & 1) * P::kStage;
         // Stage s has landed, and no wave still reads stage s - 1.
@@ -518,14 +717,22 @@ __global__ __launch_bounds__(256) void k_i8_ranges(I8Params p) {
 }
 
 // At most 16 rows of A: C is a pass over B.  A workgroup takes 16 rows of B, its waves K blocks
-// in turn, operands straight into registers; their sums meet in LDS.
+// in turn, operands straight into registers, the next blocks' on their way while these are
+// multiplied; their sums meet in LDS.
+// XT >= 0: one row of A, not codes but x itself (0 bf16, 1 f32), which each workgroup quantizes
+// into LDS with the first of B's blocks on their way: about 2 us where each CU has one workgroup,
+// less than a launch of its own.  Where a CU has several, one after the other, it is not (1 x 4096
+// x 14336: 23.1 us against 18.3 and the launch), nor for more rows (8 x 4096: 13 us).
 constexpr int kFewMaxM = 16;
 constexpr int kFewRows = 16;
 constexpr int kFewMaxWaves = 16;
+constexpr int kFewMaxCodes = 1 << 15;  // of x, in LDS
 
-__global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_i8_few(I8Params p) {
-    constexpr int U = 2;
+template <int XT>
+__global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_i8_few(I8Params p, const void* x, int cols) {
+    constexpr bool OWN = XT >= 0;
     __shared__ __attribute__((aligned(16))) int red[kFewMaxWaves * 256];
+    __shared__ __attribute__((aligned(16))) int8_t codes[OWN ? kFewMaxCodes : 16];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int waves = blockDim.x / kWave;
@@ -534,36 +741,77 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_i8_few(I8Params p
     const int K = (int)p.K, M = (int)p.M, S = p.S;
     const int r = lane % 16, q = lane / 16;
     const Rsrc rb = make_rsrc(p.b + n0 * K, (int64_t)rows_b * K);
-    const Rsrc ra = make_rsrc(p.a, (int64_t)M * K);
+    const Rsrc ra = make_rsrc(p.a, OWN ? 0 : (int64_t)M * K);
+    struct Block { u32x4_t a[2], b[2]; };
+    auto place = [&](int s, int h) {
+        const int pos = s * kBlock + h * 64 + q * 16;
+        return s < S && pos < K ? r * K + pos : kDropped;
+    };
+    auto load = [&](Block& t, int s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            t.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, place(s, h), 0, 0);
+            if (!OWN) t.a[h] = __builtin_amdgcn_raw_buffer_load_b128(ra, place(s, h), 0, 0);
+        }
+    };
+    // One block read ahead (1 x 18944 x 3584: 17.6 us by events; two at once 18.4, four 19.5, two
+    // and none ahead 20.8).
+    Block now, next;
+    load(now, wave);
+    float scale = 0.0f;
+    if (OWN) {
+        constexpr int kHeld = 3;  // pieces of 8 that a thread keeps
+        float* part = reinterpret_cast<float*>(red);  // each wave's maximum
+        float v[kHeld][8], u[8], top = 0.0f;
+        const int at0 = threadIdx.x * 8, step = blockDim.x * 8;
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) load8<XT>(v[c], x, min(at0 + c * step, cols), cols);
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) top = max8(v[c], top);
+        for (int at = at0 + kHeld * step; at < cols; at += step) {
+            load8<XT>(u, x, at, cols);
+            top = max8(u, top);
+        }
+        top = wave_max(top);
+        if (lane == 0) part[wave] = top;
+        __syncthreads();
+        for (int w = 0; w < waves; ++w) top = __builtin_elementwise_maximum(top, part[w]);
+        const RowScale sc(top);
+        scale = sc.s;
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c)
+            if (at0 + c * step < K) *reinterpret_cast<uint2*>(codes + at0 + c * step) = sc.codes(v[c]);
+        for (int at = at0 + kHeld * step; at < K; at += step) {
+            load8<XT>(u, x, min(at, cols), cols);
+            *reinterpret_cast<uint2*>(codes + at) = sc.codes(u);
+        }
+        __syncthreads();
+    }
     v4i acc = {};
-    for (int s0 = wave; s0 < S; s0 += waves * U) {
-        u32x4_t b[U][2], a[U][2];
+    for (int s = wave; s < S; s += waves) {
+        load(next, s + waves);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int s = s0 + u * waves, pos = s * kBlock + h * 64 + q * 16;
-                const int off = s < S && pos < K ? r * K + pos : kDropped;
-                b[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, off, 0, 0);
-                a[u][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, off, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+            if (OWN) {
+                const int off = place(s, h);
+                now.a[h] = u32x4_t{0, 0, 0, 0};
+                if (r == 0 && off != kDropped) now.a[h] = *reinterpret_cast<const u32x4_t*>(codes + off);
             }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) acc = mma(__builtin_bit_cast(v4i, b[u][h]), __builtin_bit_cast(v4i, a[u][h]), acc);
+            acc = mma(__builtin_bit_cast(v4i, now.b[h]), __builtin_bit_cast(v4i, now.a[h]), acc);
+        }
+        now = next;
     }
     *reinterpret_cast<v4i*>(red + (wave * 16 + r) * 16 + 4 * q) = acc;
     __syncthreads();
     for (int e = threadIdx.x; e < 256; e += blockDim.x) {
+        const int m = e / 16, n = e % 16;
+        if (m >= M || n >= rows_b) continue;
         int sum = 0;
         for (int w = 0; w < waves; ++w) sum += red[w * 256 + e];
-        const int m = e / 16, n = e % 16;
-        if (m < M && n < rows_b) {
-            const int64_t at = m * p.N + n0 + n;
-            const float v = value(sum, p.sa[m], p.sb[n0 + n], bias_at(p, n0 + n));
-            if (p.ct == 1) static_cast<float*>(p.c)[at] = v;
-            else static_cast<uint16_t*>(p.c)[at] = (uint16_t)pack_bf16x2(v, v);
-        }
+        const int64_t at = m * p.N + n0 + n;
+        const float v = value(sum, OWN ? scale : p.sa[m], p.sb[n0 + n], bias_at(p, n0 + n));
+        if (p.ct == 1) static_cast<float*>(p.c)[at] = v;
+        else static_cast<uint16_t*>(p.c)[at] = (uint16_t)pack_bf16x2(v, v);
     }
 }
 
@@ -578,9 +826,16 @@ struct TileCost {
     int tile, per_cu;
     double alone, each, fixed;
 };
-constexpr TileCost kTileCosts[] = {{256, 1, 1.2, 1.2, 6.0}, {128, 2, 0.6, 0.42, 4.0}, {64, 4, 0.4, 0.2, 3.0}};
+constexpr TileCost kTileCosts[] = {{256, 1, 1.35, 1.35, 7.0}, {128, 2, 0.58, 0.48, 2.5}, {64, 4, 0.3, 0.195, 1.5}};
 constexpr int kCus = 256;
 constexpr int kRanges[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+
+// How many of the tiles of 256 x 256, dealt to all CUs in turn, are left for a last round in which
+// four workgroups can share each.
+int64_t quartered(int64_t tiles, int splits) {
+    const int64_t rest = tiles % kCus;
+    return splits == 1 && tiles > kCus && rest <= kCus / 4 ? rest : 0;
+}
 
 Choice choose(int64_t M, int64_t N, int64_t K) {
     const int64_t S = (K + kBlock - 1) / kBlock;
@@ -592,10 +847,12 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
             const int64_t per = (S + sp - 1) / sp;
             if (sp > 1 && (sp > S || tiles * sp > 4 * kCus || 4 * sp * M * N > kMaxPartialBytes)) break;
             if (sp > 1 && per * (sp - 1) >= S) continue;  // a range would be empty
-            const int64_t groups = (tiles * sp + kCus - 1) / kCus, full = groups / c.per_cu, rest = groups % c.per_cu;
+            const int64_t quarters = c.tile == 256 ? quartered(tiles, sp) : 0;
+            const int64_t groups = (tiles * sp - quarters + kCus - 1) / kCus, full = groups / c.per_cu, rest = groups % c.per_cu;
             double t = (double)full * ((double)per * std::max(c.alone, c.each * c.per_cu) + c.fixed);
             if (rest) t += (double)per * std::max(c.alone, c.each * (double)rest) + c.fixed;
-            if (sp > 1) t += 3.0 + 8.0 * (double)sp * (double)M * (double)N / 8e6;
+            if (quarters) t += (double)per * 0.6 + 4.0;
+            if (sp > 1) t += 4.0 + 8.0 * (double)sp * (double)M * (double)N / 8e6;
             if (t < least) least = t, best = Choice{c.tile, sp};
         }
     }
@@ -628,6 +885,8 @@ size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return sp > 1 ? (size_t)(4 * sp * M * N) : 0;
 }
 
+bool int8_linear_in_one(int64_t M, int64_t N, int64_t K) { return M == 1 && K <= kFewMaxCodes && N <= kFewRows * kCus; }
+
 int launch_int8_quantize(const Int8QuantJob& j, char* msg, size_t msg_len) {
     if (j.rows == 0) return 0;
     const I8QuantParams p{j.x, j.rows, j.cols, (j.cols + 15) / 16 * 16, j.codes, j.scales, 0};
@@ -656,7 +915,10 @@ int launch_int8_gemm(const Int8GemmJob& j, char* msg, size_t msg_len) {
         const int64_t groups = (j.N + kFewRows - 1) / kFewRows;
         int waves = groups <= 256 ? kFewMaxWaves : groups <= 1024 ? 8 : 4;
         while (waves > 1 && waves >= 2 * S) waves /= 2;
-        FP4Q_LAUNCH(k_gemm_i8_few, dim3((unsigned)groups), dim3(waves * kWave), 0, stream, p);
+        const dim3 grid((unsigned)groups), block(waves * kWave);
+        if (j.xt < 0) FP4Q_LAUNCH((k_gemm_i8_few<-1>), grid, block, 0, stream, p, nullptr, 0);
+        else if (j.xt == 0) FP4Q_LAUNCH((k_gemm_i8_few<0>), grid, block, 0, stream, p, j.x, (int)j.cols);
+        else FP4Q_LAUNCH((k_gemm_i8_few<1>), grid, block, 0, stream, p, j.x, (int)j.cols);
         return status("int8 gemm", msg, msg_len);
     }
     const Choice ch = choose(j.M, j.N, j.K);
@@ -670,8 +932,13 @@ int launch_int8_gemm(const Int8GemmJob& j, char* msg, size_t msg_len) {
     for (int64_t first = 0; first < groups; first += kMaxGrid) {
         const dim3 grid((unsigned)std::min(groups - first, kMaxGrid));
         p.first = (unsigned)first;
-        if (ch.tile == 256) FP4Q_LAUNCH(k_gemm_i8, grid, dim3(kBigThreads), 0, stream, p);
-        else if (ch.tile == 128) FP4Q_LAUNCH(k_gemm_i8_mid<128>, grid, dim3(256), I8Mid<128>::kLds, stream, p);
+        if (ch.tile == 256) {
+            const int64_t quarters = quartered(groups, p.splits);
+            FP4Q_LAUNCH(k_gemm_i8, dim3((unsigned)std::min<int64_t>(groups, kCus)), dim3(kBigThreads), 0, stream, p,
+                        (unsigned)(groups - quarters), (unsigned)quarters);
+            break;
+        }
+        if (ch.tile == 128) FP4Q_LAUNCH(k_gemm_i8_mid<128>, grid, dim3(256), I8Mid<128>::kLds, stream, p);
         else FP4Q_LAUNCH(k_gemm_i8_mid<64>, grid, dim3(256), I8Mid<64>::kLds, stream, p);
     }
     if (p.splits > 1)

@@ -168,9 +168,16 @@ struct Int8GemmJob {
     int ct;            // 0 bf16, 1 f32
     void* ws;          // int8_gemm_workspace_bytes(M, N, K) bytes: sums of K ranges
     void* stream;
+    // Where int8_linear_in_one(M, N, K): A's values (M x cols, K = cols rounded up to 16) in the place
+    // of a_codes and a_scales.
+    int xt = -1;       // 0 bf16, 1 f32; -1: A is given as codes
+    const void* x = nullptr;
+    int64_t cols = 0;
 };
 
 size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+// Whether a product of unquantized A takes one launch: one row, and few rows of B.
+bool int8_linear_in_one(int64_t M, int64_t N, int64_t K);
 
 // Mixture-of-experts layer for a few tokens.
 struct MoeWeights {

@@ -47,6 +47,7 @@ def test_gemm_validation(L):
 def test_linear_validation(L):
     need = L.int8_linear_workspace_bytes(40, 100, 70)
     assert need >= 40 * 112 + 160
+    assert L.int8_linear_workspace_bytes(1, 18944, 70) == 0 and L.int8_linear_workspace_bytes(2, 18944, 70) >= 2 * 18944
 
     def lin(x=A, xt=0, w=B, sw=C, bias=None, bt=0, t=40, k=100, n=70, y=D, yt=0, ws=A, wsb=need):
         return L.int8_linear(x, xt, w, sw, bias, bt, t, k, n, y, yt, ws, wsb, None)

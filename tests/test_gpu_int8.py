@@ -116,7 +116,7 @@ def expect(acc, sa, sb, bias=None):
 SHAPES = [(1, 1, 16), (1, 5, 16), (2, 16, 112), (15, 33, 128), (16, 40, 144), (1, 3584, 3584), (3, 1000, 18944), (16, 511, 4096),
           (17, 1, 16), (17, 70, 48), (33, 64, 128), (64, 65, 1008), (65, 127, 144), (100, 256, 8192), (128, 128, 256), (129, 130, 272),
           (200, 1031, 1008), (333, 1031, 1008), (256, 256, 16), (257, 300, 400), (60, 3584, 18944), (1000, 1000, 1000 // 16 * 16),
-          (2048, 3001, 512), (4096, 4096, 256), (4100, 4099, 384), (5000, 6000, 128), (4096, 4096, 4096), (300, 200, 131056)]
+          (2048, 3001, 512), (4096, 4096, 256), (4100, 4099, 384), (5000, 6000, 128), (4096, 4096, 4096), (4100, 4099, 4000), (4400, 4104, 4096), (300, 200, 131056)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -209,7 +209,8 @@ def test_gemm_writes_its_outputs_alone(m, n, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("shape,n", [((1, 896), 100), ((2, 7, 130), 33), ((333, 1003), 1031), ((5,), 3), ((0, 40), 8), ((4, 0), 6),
-                                     ((2, 0, 3), 5), ((17, 18944), 64), ((600, 2048), 5000)])
+                                     ((2, 0, 3), 5), ((17, 18944), 64), ((600, 2048), 5000),
+                                     ((1, 18944), 3584), ((16, 2048), 33), ((16, 2049), 33), ((3, 1001), 5000), ((1, 32768), 16), ((1, 32769), 16), ((1, 500), 4097), ((1, 28000), 4096), ((2, 131056), 7)])
 def test_linear(shape, n, dtype):
     g = gen(n)
     x = (torch.randn(*shape, generator=g, device=DEV) * 2).to(dtype)
@@ -232,6 +233,20 @@ def test_linear_of_strided_input_and_other_types():
     assert torch.equal(fq.int8_linear(x, w, out_dtype=torch.bfloat16), y.bfloat16())
     out = torch.empty(64, 50, dtype=torch.bfloat16, device=DEV)
     assert fq.int8_linear(x, w, out=out) is out and torch.equal(out, y.bfloat16())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("k", [40, 2000])
+def test_linear_of_few_tokens_that_are_not_finite(k, dtype):
+    x = torch.randn(5, k, generator=gen(2), device=DEV).to(dtype)
+    w = fq.int8_quantize_rows(torch.randn(70, k, generator=gen(3), device=DEV))
+    want = fq.int8_linear(x, w)
+    x[1, k - 1], x[3, 0], x[4] = float("nan"), float("inf"), 0.0
+    y = fq.int8_linear(x, w)
+    assert bool(y[1].isnan().all()) and bool(y[3].isnan().all()) and bool((y[4] == 0).all())
+    assert torch.equal(y[::2][:2], want[::2][:2])
+    for t in range(5):  # one token: quantized inside the product
+        assert torch.equal(fq.int8_linear(x[t:t + 1], w).nan_to_num(7.0), y[t:t + 1].nan_to_num(7.0))
 
 
 def test_linear_is_near_the_unquantized_one():
