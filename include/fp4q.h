@@ -559,6 +559,79 @@ fp4q_status int8_linear(const void* x, int32_t xt, const int8_t* w_codes, const 
                         size_t ws_bytes, void* stream);
 size_t int8_linear_workspace_bytes(int64_t tokens, int64_t in, int64_t out);
 
+/*
+ * The slots of a routing by expert, which is what the grouped products below take:
+ * slot t * top_k + j is token t's j-th expert.
+ *   ids         device, tokens x top_k, int64 (wide != 0) or int32.  An id outside
+ *               0..experts-1 names no expert (a slot dropped for capacity, say)
+ *   offsets     device out, experts + 1: expert e owns sorted rows offsets[e] ..
+ *               offsets[e + 1] - 1
+ *   order       device out, slots: the slot of each sorted row, by expert and within
+ *               one by slot; slots of no expert last
+ *   token       device out, slots: order / top_k
+ *   position    device out, tokens x top_k: the sorted row of each slot
+ *   experts     1..512; tokens * top_k below 2^31 (0 tokens: offsets of 0)
+ *   ws          expert_order_workspace_bytes() bytes (0 up to 4096 slots; then ws may
+ *               be NULL), 4-byte aligned, any contents
+ * The same on every run.  Errors: FP4Q_ERR_ARG, FP4Q_ERR_SHAPE, FP4Q_ERR_ALIGN,
+ * FP4Q_ERR_WORKSPACE, FP4Q_ERR_HIP.
+ */
+fp4q_status expert_order(const void* ids, int32_t wide, int64_t tokens, int32_t top_k, int32_t experts, int32_t* offsets,
+                         int32_t* order, int32_t* token, int32_t* position, void* ws, size_t ws_bytes, void* stream);
+size_t expert_order_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);
+
+/*
+ * Products grouped by expert, of any number of rows each: C[i] = A_hat[tokens[i]]
+ * W_hat_e^T for offsets[e] <= i < offsets[e + 1].
+ *   a_codes, a_scales  A (a_rows x K) under row scales, as fp8_quantize_b128 writes it
+ *   b_codes     device, the experts' matrices of N x K one after the other
+ *   b_scales    their tile scales: of each matrix by itself (stacked == 0: experts x
+ *               ceil(N / 128) x ceil(K / 128)) or of the whole (experts * N) x K matrix,
+ *               as moe_layer takes it (stacked != 0).  (The same where N % 128 == 0.)
+ *   offsets     device, experts + 1, as expert_order writes them: read by the kernels,
+ *               so no size of a group needs to be known to the host.  One outside
+ *               0..rows is taken as the nearest inside, a group that ends before it
+ *               starts as empty; groups that overlap leave the rows of either, or
+ *               neither, in C.  Rows that no group owns are left as they are
+ *   tokens      device, rows: the row of A that goes into each row of C (one that A does
+ *               not have gives zeros); or NULL: row i of A (then a_rows == rows)
+ *   N, K        as for fp8_gemm_b128; experts 1..512; with tokens, A is at most 2^31 - 1
+ *               bytes
+ *   c, ct       device out, rows x N
+ * No workspace.  Groups of up to 8 rows on average take a kernel that streams the
+ * weights of the experts in use once; others tiles of 64, 128 or 256.  Arithmetic and
+ * errors as for fp8_gemm_b128; the same on every run for given sizes.
+ */
+fp4q_status fp8_grouped_gemm_b128(const uint8_t* a_codes, const float* a_scales, int64_t a_rows, const uint8_t* b_codes,
+                                  const float* b_scales, int32_t stacked, const int32_t* offsets, int32_t experts,
+                                  const int32_t* tokens, int64_t rows, int64_t N, int64_t K, void* c, int32_t ct,
+                                  void* stream);
+
+/*
+ * A training step's expert layer on them, its rows already by expert: for the rows of
+ * expert e, y = Qr(x) Qt(w_e)^T, dx = Qr(dy) Qt(w_e), dw_e = Qr(dy_e^T) Qr(x_e^T)^T,
+ * Qr and Qt as for fp8_linear_forward, the blocks of the transposes starting at the
+ * group's first row.  (The quantizer counts as the identity in the backward pass.)
+ *   x, y, dy, dx  rows x in and rows x out, dtype xt; w, dw experts x out x in, dtype
+ *                 wt; contiguous, aligned to their elements
+ *   offsets       device, experts + 1, as for fp8_grouped_gemm_b128 and the same for
+ *                 both calls.  Rows behind the last group get zeros in y and dx; an
+ *                 expert without rows gets a dw of zeros
+ *   want_dx, want_dw, saved, ws  as for fp8_linear_forward
+ *   rows, in, out  each below 2^21; experts 1..512
+ * Errors as for fp8_linear_forward.
+ */
+fp4q_status fp8_grouped_linear_forward(const void* x, int32_t xt, const void* w, int32_t wt, const int32_t* offsets,
+                                       int32_t experts, int64_t rows, int64_t in, int64_t out, void* y, int32_t want_dx,
+                                       int32_t want_dw, void* saved, size_t saved_bytes, void* ws, size_t ws_bytes,
+                                       void* stream);
+fp4q_status fp8_grouped_linear_backward(const void* dy, int32_t xt, int32_t wt, const int32_t* offsets, int32_t experts,
+                                        int64_t rows, int64_t in, int64_t out, void* dx, void* dw, const void* saved,
+                                        size_t saved_bytes, void* ws, size_t ws_bytes, void* stream);
+size_t fp8_grouped_linear_saved_bytes(int64_t rows, int64_t in, int64_t out, int32_t experts, int32_t want_dx,
+                                      int32_t want_dw);
+size_t fp8_grouped_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t experts);
+
 /* One stacked matrix of a layer's expert weights, (experts * rows) x K, exactly as
  * the quantize calls write it. */
 typedef struct {

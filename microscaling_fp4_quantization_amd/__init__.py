@@ -43,6 +43,9 @@ EXPORTS = ("mxfp4_quantize", "nvfp4_quantize", "nvfp4_quantize_noalloc", "fp4_qu
            "fp8_quantize_b128", "fp8_gemm_b128", "fp8_gemm_b128_workspace_bytes",
            "fp8_linear_forward", "fp8_linear_backward", "fp8_linear_saved_bytes", "fp8_linear_workspace_bytes",
            "int8_quantize_rows", "int8_gemm", "int8_gemm_workspace_bytes", "int8_linear", "int8_linear_workspace_bytes",
+           "expert_order", "expert_order_workspace_bytes", "fp8_grouped_gemm_b128",
+           "fp8_grouped_linear_forward", "fp8_grouped_linear_backward", "fp8_grouped_linear_saved_bytes",
+           "fp8_grouped_linear_workspace_bytes",
            "moe_layer", "moe_layer_workspace_bytes",
            "fp4q_workspace_bytes",
            "fp4q_last_error", "fp4q_abi_version", "fp4q_profile_events", "fp4q_profile_count")
@@ -106,6 +109,17 @@ def _bind(l):
     l.int8_quantize_rows.restype = l.int8_gemm.restype = l.int8_linear.restype = c.c_int
     l.int8_gemm_workspace_bytes.argtypes = l.int8_linear_workspace_bytes.argtypes = [i64, i64, i64]
     l.int8_gemm_workspace_bytes.restype = l.int8_linear_workspace_bytes.restype = sz
+    l.expert_order.argtypes = [P, i32, i64, i32, i32, P, P, P, P, P, sz, P]
+    l.expert_order_workspace_bytes.argtypes = [i64, i32, i32]
+    l.fp8_grouped_gemm_b128.argtypes = [P, P, i64, P, P, i32, P, i32, P, i64, i64, i64, P, i32, P]
+    l.fp8_grouped_linear_forward.argtypes = [P, i32, P, i32, P, i32, i64, i64, i64, P, i32, i32, P, sz, P, sz, P]
+    l.fp8_grouped_linear_backward.argtypes = [P, i32, i32, P, i32, i64, i64, i64, P, P, P, sz, P, sz, P]
+    l.expert_order.restype = l.fp8_grouped_gemm_b128.restype = c.c_int
+    l.fp8_grouped_linear_forward.restype = l.fp8_grouped_linear_backward.restype = c.c_int
+    l.fp8_grouped_linear_saved_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
+    l.fp8_grouped_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    l.expert_order_workspace_bytes.restype = sz
+    l.fp8_grouped_linear_saved_bytes.restype = l.fp8_grouped_linear_workspace_bytes.restype = sz
     l.moe_layer.argtypes = [P, i32, i64, i64, i64, i32, i32, i32, P, P, P, i32, i32, P, P, P, i32, P, sz, P]
     l.moe_layer.restype = c.c_int
     l.moe_layer_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
@@ -858,4 +872,5 @@ class LaunchTimer:
 
 
 from .fp8_linear import fp8_linear  # noqa: E402  (needs the functions above)
+from .grouped import ExpertOrder, expert_order, fp8_grouped_gemm_b128, fp8_grouped_linear  # noqa: E402
 from .int8 import Int8Quantized, int8_gemm, int8_linear, int8_quantize_rows  # noqa: E402

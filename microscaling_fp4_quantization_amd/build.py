@@ -34,7 +34,7 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contra
              "-Wall", "-Wno-unused-function"]
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 FILE_FLAGS = {"fp4q_gemm.hip": VGPR_FORM, "fp4q_fp8_gemm.hip": VGPR_FORM,
-              "fp4q_moe.hip": VGPR_FORM}
+              "fp4q_grouped.hip": VGPR_FORM, "fp4q_moe.hip": VGPR_FORM}
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 
 

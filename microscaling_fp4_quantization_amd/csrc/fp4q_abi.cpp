@@ -701,6 +701,189 @@ size_t int8_linear_workspace_bytes(int64_t tokens, int64_t in, int64_t out) {
     return Int8Linear(nullptr, tokens, in, out).bytes;
 }
 
+static fp4q_status check_experts(const char* fn, int64_t experts) {
+    if (experts < 1 || experts > fp4q::kMoeMaxExperts)
+        return fail(FP4Q_ERR_SHAPE, "%s: %lld experts: 1 to %lld are taken", fn, (long long)experts, (long long)fp4q::kMoeMaxExperts);
+    return FP4Q_OK;
+}
+
+static fp4q_status order_shape(const char* fn, int64_t tokens, int64_t top_k, int64_t experts) {
+    TRY(check_experts(fn, experts));
+    if (tokens < 0 || top_k < 1 || top_k > INT32_MAX || tokens > INT32_MAX / top_k)
+        return fail(FP4Q_ERR_SHAPE, "%s: %lld tokens of %lld slots: at most 2^31 - 1 slots are taken", fn, (long long)tokens, (long long)top_k);
+    return FP4Q_OK;
+}
+
+fp4q_status expert_order(const void* ids, int32_t wide, int64_t tokens, int32_t top_k, int32_t experts, int32_t* offsets,
+                         int32_t* order, int32_t* token, int32_t* position, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "expert_order";
+    TRY(order_shape(fn, tokens, top_k, experts));
+    if (!offsets || (tokens > 0 && (!ids || !order || !token || !position)))
+        return fail(FP4Q_ERR_ARG, "%s: ids, offsets, order, token and position must not be NULL", fn);
+    if (!aligned(ids, wide ? 8 : 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(token, 4) || !aligned(position, 4))
+        return fail(FP4Q_ERR_ALIGN, "%s: arrays must be aligned to their elements", fn);
+    const size_t need = fp4q::expert_order_workspace_bytes(tokens * top_k, experts);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(FP4Q_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
+    if (need > 0 && !aligned(ws, 4)) return fail(FP4Q_ERR_ALIGN, "%s: workspace must be 4-byte aligned", fn);
+    char msg[256] = {0};
+    return launched(fp4q::launch_expert_order({ids, wide != 0, tokens, top_k, experts, offsets, order, token, position, ws, stream}, msg, sizeof msg), msg);
+}
+
+size_t expert_order_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts) {
+    if (order_shape("expert_order_workspace_bytes", tokens, top_k, experts) != FP4Q_OK) return 0;
+    return fp4q::expert_order_workspace_bytes(tokens * top_k, experts);
+}
+
+fp4q_status fp8_grouped_gemm_b128(const uint8_t* a_codes, const float* a_scales, int64_t a_rows, const uint8_t* b_codes,
+                                  const float* b_scales, int32_t stacked, const int32_t* offsets, int32_t experts,
+                                  const int32_t* tokens, int64_t rows, int64_t N, int64_t K, void* c, int32_t ct,
+                                  void* stream) {
+    const char* fn = "fp8_grouped_gemm_b128";
+    TRY(check_dtype(fn, ct));
+    TRY(check_experts(fn, experts));
+    if (a_rows < 0 || rows < 0 || N < 0 || K < 0) return fail(FP4Q_ERR_SHAPE, "%s: negative size", fn);
+    if (K % 16 != 0) return fail(FP4Q_ERR_SHAPE, "%s: K = %lld is not a multiple of 16", fn, (long long)K);
+    if (K > (int64_t)1 << 22) return fail(FP4Q_ERR_SHAPE, "%s: K = %lld exceeds 2^22", fn, (long long)K);
+    if (N * (ct == FP4Q_F32 ? 4 : 2) >= (int64_t)1 << 23)
+        return fail(FP4Q_ERR_SHAPE, "%s: N = %lld is too large for this output type", fn, (long long)N);
+    if (rows > INT32_MAX) return fail(FP4Q_ERR_SHAPE, "%s: %lld rows exceed 2^31 - 1", fn, (long long)rows);
+    if (!tokens && a_rows != rows)
+        return fail(FP4Q_ERR_SHAPE, "%s: A has %lld rows, C %lld; without tokens they must agree", fn, (long long)a_rows, (long long)rows);
+    if (tokens && (a_rows >= (int64_t)1 << 29 || a_rows * K > INT32_MAX))
+        return fail(FP4Q_ERR_SHAPE, "%s: A is %lld x %lld: with tokens, at most 2^31 - 1 bytes and 2^29 - 1 rows are taken", fn,
+                    (long long)a_rows, (long long)K);
+    if (rows > 0 && N > 0) {
+        if (!offsets || !c) return fail(FP4Q_ERR_ARG, "%s: offsets and c must not be NULL", fn);
+        if (K > 0 && ((a_rows > 0 && (!a_codes || !a_scales)) || !b_codes || !b_scales))
+            return fail(FP4Q_ERR_ARG, "%s: codes and scales must not be NULL", fn);
+        if (!aligned(a_codes, 16) || !aligned(b_codes, 16)) return fail(FP4Q_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
+        if (!aligned(a_scales, 4) || !aligned(b_scales, 4)) return fail(FP4Q_ERR_ALIGN, "%s: scales must be 4-byte aligned", fn);
+        if (!aligned(c, ct == FP4Q_F32 ? 4 : 2)) return fail(FP4Q_ERR_ALIGN, "%s: c is not aligned to its element", fn);
+        if (!aligned(offsets, 4) || !aligned(tokens, 4)) return fail(FP4Q_ERR_ALIGN, "%s: offsets and tokens must be 4-byte aligned", fn);
+    }
+    char msg[256] = {0};
+    return launched(fp4q::launch_grouped_gemm({a_codes, a_scales, a_rows, b_codes, b_scales, stacked != 0, offsets, experts, tokens, rows, N, K,
+                                               c, ct, false, stream}, msg, sizeof msg), msg);
+}
+
+// An expert layer's operands in memory, as LinearSaved and the others lay out a linear layer's.
+namespace {
+
+// The transpose of rows in groups.
+B128Part group_part(Carve& c, int64_t rows, int64_t cols, int64_t experts) {
+    const int64_t blocks = fp4q::fp8_group_blocks(rows, experts);
+    B128Part b;
+    b.codes = static_cast<uint8_t*>(c.take((size_t)(cols * blocks * 128)));
+    b.scales = static_cast<float*>(c.take((size_t)(4 * cols * blocks)));
+    return b;
+}
+
+// One matrix per expert.
+B128Part expert_part(Carve& c, int64_t experts, int64_t rows, int64_t cols) {
+    B128Part b;
+    b.codes = static_cast<uint8_t*>(c.take((size_t)(experts * rows * up16(cols))));
+    b.scales = static_cast<float*>(c.take((size_t)(4 * experts * ((rows + 127) / 128) * ((cols + 127) / 128))));
+    return b;
+}
+
+struct GroupedSaved {
+    B128Part wt{}, xt{};
+    size_t bytes;
+    GroupedSaved(void* p, int64_t T, int64_t K, int64_t N, int64_t E, bool dx, bool dw) {
+        Carve c{static_cast<char*>(p)};
+        if (dx) wt = expert_part(c, E, K, N);
+        if (dw) xt = group_part(c, T, K, E);
+        bytes = c.used;
+    }
+};
+
+struct GroupedForward {
+    B128Part x, w;
+    size_t bytes;
+    GroupedForward(void* p, int64_t T, int64_t K, int64_t N, int64_t E) {
+        Carve c{static_cast<char*>(p)};
+        x = c.part(T, K, false);
+        w = expert_part(c, E, N, K);
+        bytes = c.used;
+    }
+};
+
+struct GroupedBackward {
+    B128Part dy{}, dyt{};
+    size_t bytes;
+    GroupedBackward(void* p, int64_t T, int64_t N, int64_t E, bool dx, bool dw) {
+        Carve c{static_cast<char*>(p)};
+        if (dx) dy = c.part(T, N, false);
+        if (dw) dyt = group_part(c, T, N, E);
+        bytes = c.used;
+    }
+};
+
+fp4q_status grouped_shape(const char* fn, int64_t T, int64_t K, int64_t N, int64_t E, int32_t xt, int32_t wt) {
+    TRY(check_experts(fn, E));
+    TRY(linear_shape(fn, T, K, N, xt, wt));
+    if (N * K > (int64_t)INT32_MAX * 512 / E)
+        return fail(FP4Q_ERR_SHAPE, "%s: the weights exceed (2^31 - 1) * 512 elements", fn);
+    return FP4Q_OK;
+}
+
+}  // namespace
+
+size_t fp8_grouped_linear_saved_bytes(int64_t rows, int64_t in, int64_t out, int32_t experts, int32_t want_dx, int32_t want_dw) {
+    if (grouped_shape("fp8_grouped_linear_saved_bytes", rows, in, out, experts, FP4Q_BF16, FP4Q_BF16) != FP4Q_OK) return 0;
+    return GroupedSaved(nullptr, rows, in, out, experts, want_dx != 0, want_dw != 0).bytes;
+}
+
+size_t fp8_grouped_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t experts) {
+    if (grouped_shape("fp8_grouped_linear_workspace_bytes", rows, in, out, experts, FP4Q_BF16, FP4Q_BF16) != FP4Q_OK) return 0;
+    const size_t f = GroupedForward(nullptr, rows, in, out, experts).bytes, b = GroupedBackward(nullptr, rows, out, experts, true, true).bytes;
+    return f > b ? f : b;
+}
+
+fp4q_status fp8_grouped_linear_forward(const void* x, int32_t xt, const void* w, int32_t wt, const int32_t* offsets,
+                                       int32_t experts, int64_t rows, int64_t in, int64_t out, void* y, int32_t want_dx,
+                                       int32_t want_dw, void* saved, size_t saved_bytes, void* ws, size_t ws_bytes,
+                                       void* stream) {
+    const char* fn = "fp8_grouped_linear_forward";
+    TRY(grouped_shape(fn, rows, in, out, experts, xt, wt));
+    if ((rows > 0 && in > 0 && !x) || (out > 0 && in > 0 && !w) || (rows > 0 && out > 0 && !y) || !offsets)
+        return fail(FP4Q_ERR_ARG, "%s: x, w, offsets and y must not be NULL", fn);
+    if (!aligned(x, xt == FP4Q_F32 ? 4 : 2) || !aligned(w, wt == FP4Q_F32 ? 4 : 2) || !aligned(y, xt == FP4Q_F32 ? 4 : 2) || !aligned(offsets, 4))
+        return fail(FP4Q_ERR_ALIGN, "%s: x, w, offsets and y must be aligned to their elements", fn);
+    const GroupedSaved s(saved, rows, in, out, experts, want_dx != 0, want_dw != 0);
+    TRY(linear_buffer(fn, "saved", saved, saved_bytes, s.bytes));
+    const GroupedForward f(ws, rows, in, out, experts);
+    TRY(linear_buffer(fn, "a workspace", ws, ws_bytes, f.bytes));
+    char msg[256] = {0};
+    TRY(launched(fp4q::launch_fp8_quantize_grouped({x, xt, rows, in, offsets, experts, f.x.codes, f.x.scales, s.xt.codes, s.xt.scales, stream},
+                                                   {w, wt, experts, out, in, f.w.codes, f.w.scales, s.wt.codes, s.wt.scales, stream},
+                                                   msg, sizeof msg), msg));
+    return launched(fp4q::launch_grouped_gemm({f.x.codes, f.x.scales, rows, f.w.codes, f.w.scales, false, offsets, experts, nullptr, rows, out,
+                                               up16(in), y, xt, true, stream}, msg, sizeof msg), msg);
+}
+
+fp4q_status fp8_grouped_linear_backward(const void* dy, int32_t xt, int32_t wt, const int32_t* offsets, int32_t experts,
+                                        int64_t rows, int64_t in, int64_t out, void* dx, void* dw, const void* saved,
+                                        size_t saved_bytes, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "fp8_grouped_linear_backward";
+    TRY(grouped_shape(fn, rows, in, out, experts, xt, wt));
+    if (!dx && !dw) return fail(FP4Q_ERR_ARG, "%s: dx and dw must not both be NULL", fn);
+    if ((rows > 0 && out > 0 && !dy) || !offsets) return fail(FP4Q_ERR_ARG, "%s: dy and offsets must not be NULL", fn);
+    if (!aligned(dy, xt == FP4Q_F32 ? 4 : 2) || !aligned(dx, xt == FP4Q_F32 ? 4 : 2) || !aligned(dw, wt == FP4Q_F32 ? 4 : 2) || !aligned(offsets, 4))
+        return fail(FP4Q_ERR_ALIGN, "%s: dy, dx, dw and offsets must be aligned to their elements", fn);
+    const GroupedSaved s(const_cast<void*>(saved), rows, in, out, experts, dx != nullptr, dw != nullptr);
+    TRY(linear_buffer(fn, "saved", saved, saved_bytes, s.bytes));
+    const GroupedBackward b(ws, rows, out, experts, dx != nullptr, dw != nullptr);
+    TRY(linear_buffer(fn, "a workspace", ws, ws_bytes, b.bytes));
+    char msg[256] = {0};
+    TRY(launched(fp4q::launch_fp8_quantize_groups({dy, xt, rows, out, offsets, experts, b.dy.codes, b.dy.scales, b.dyt.codes, b.dyt.scales, stream}, msg, sizeof msg), msg));
+    if (dx) TRY(launched(fp4q::launch_grouped_gemm({b.dy.codes, b.dy.scales, rows, s.wt.codes, s.wt.scales, false, offsets, experts, nullptr, rows, in,
+                                                    up16(out), dx, xt, true, stream}, msg, sizeof msg), msg));
+    if (dw) TRY(launched(fp4q::launch_grouped_outer({b.dyt.codes, b.dyt.scales, s.xt.codes, s.xt.scales, offsets, experts, rows, out, in, dw, wt, stream}, msg, sizeof msg), msg));
+    return ok();
+}
+
 static fp4q_status moe_weights(const char* fn, const char* what, const fp4q_expert_weights* w, int32_t fmt,
                                int64_t experts, fp4q::MoeWeights& out) {
     if (!w) return fail(FP4Q_ERR_ARG, "%s: %s must not be NULL", fn, what);

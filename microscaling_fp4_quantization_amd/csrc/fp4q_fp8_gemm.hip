@@ -74,54 +74,22 @@ struct F8Params {
     unsigned first;    // this launch's first workgroup (of tiles times K ranges)
 };
 
-// A wave's sums formed again, for scales whose product passes binary32's range: operands and
-// scales straight from memory, no LDS and no barrier.  FA and FB fragments of 16 rows from
-// row a0 and b0 of the tile (whose first rows are m0 and n0), K blocks s_lo .. s_hi - 1.
-template <bool BROW, bool WIDE, int NA, int NB>
-__device__ __forceinline__ void sums_again(v4f (&acc)[NB][NA], const F8Params& p, Rsrc ra, Rsrc rb, int64_t m0, int64_t n0, int rows_a,
-                           int rows_b, int a0, int b0, int s_lo, int s_hi, int lane) {
-    const int K = (int)p.K, r = lane % kF16, q = lane / kF16;
-    const Rsrc rst = make_rsrc(p.sb + n0 / kBlock * p.S, (int64_t)((rows_b + kBlock - 1) / kBlock) * p.S * 4);
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < NA; ++j) acc[i][j] = v4f{};
-    auto codes = [&](Rsrc w, int row, int s) {
-        u32x4_t half[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int pos = s * kBlock + h * 64 + q * 16;
-            half[h] = __builtin_amdgcn_raw_buffer_load_b128(w, pos < K ? row * K + pos : kDropped, 0, 0);
-        }
-        return Operand<WIDE>::of(join(__builtin_bit_cast(v4i, half[0]), __builtin_bit_cast(v4i, half[1])));
-    };
-    auto scale = [](Rsrc w, int at) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w, at * 4, 0, 0)); };
-    for (int s = s_lo; s < s_hi; ++s) {
-        const Rsrc rsa = make_rsrc(p.sa + s * p.M + m0, rows_a * 4);
-        const Rsrc rsb = make_rsrc(BROW ? p.sb + s * p.N + n0 : p.sb, rows_b * 4);
-        for (int i = 0; i < NB; ++i) {
-            const typename Operand<WIDE>::T b = codes(rb, b0 + i * kF16 + r, s);
-            float sb[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = b0 + i * kF16 + 4 * q + e;
-                sb[e] = BROW ? scale(rsb, row) : scale(rst, row / kBlock * p.S + s);
-            }
-#pragma unroll
-            for (int j = 0; j < NA; ++j) {
-                const int row = a0 + j * kF16 + r;
-                const v4f d = mma16(b, codes(ra, row, s));
-                const float sa = scale(rsa, row);
-#pragma unroll
-                for (int k = 0; k < NB; ++k)  // (registers have no run-time index)
-                    if (k == i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[k][j][e] = scaled_sum(d[e], sa, sb[e], acc[k][j][e]);
-            }
-        }
-    }
+template <bool BROW>
+__device__ __forceinline__ F8Tile dense_tile(const F8Params& p, int64_t m0, int64_t n0, int rows_a, int rows_b, int s_lo, int s_hi) {
+    F8Tile t;
+    t.K = (int)p.K;
+    t.ra = make_rsrc(p.a + m0 * t.K, (int64_t)rows_a * t.K);
+    t.rb = make_rsrc(p.b + n0 * t.K, (int64_t)rows_b * t.K);
+    t.rows_a = rows_a, t.rows_b = rows_b, t.s_lo = s_lo, t.s_hi = s_hi;
+    t.sa = p.sa + m0, t.sa_step = p.M, t.sa_size = rows_a * 4;
+    t.sb = BROW ? p.sb + n0 : p.sb + n0 / kBlock * p.S;
+    t.sb_step = BROW ? p.N : 1;
+    t.sb_size = (BROW ? rows_b : (rows_b + kBlock - 1) / kBlock * p.S) * 4;
+    t.sb_shrink = BROW ? 0 : 4;
+    t.sb_tile = BROW ? 0 : p.S;
+    t.sb_phase = 0;
+    return t;
 }
-
 
 template <bool BROW>
 __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
@@ -139,133 +107,12 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const int64_t rows_a = p.M - m0 < BM ? p.M - m0 : BM;
     const int64_t rows_b = p.N - n0 < BN ? p.N - n0 : BN;
     // Every offset below fits 32 bits: K <= 2^22, so a window is at most 2^30 bytes.
-    const int K = (int)p.K, S = p.S;
+    const int S = p.S;
     const int per = (S + splits - 1) / splits;
     const int s_lo = split * per, s_hi = s_lo + per < S ? s_lo + per : S;
-    const Rsrc ra = make_rsrc(p.a + m0 * K, rows_a * K);
-    const Rsrc rb = make_rsrc(p.b + n0 * K, rows_b * K);
-
-    // Code load q of a wave moves rows 8 d .. 8 d + 7, d = wave + 8 (q % 4), of A
-    // (q < 4) or B: lane l fetches row 8 d + l / 8 into slot l % 8 of that row (row /
-    // 2 = 4 d + l / 16 and d = wave mod 2, so that the piece is the same for every q).
-    const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
-    const int lane_off = (lane / 8) * K + piece * 16;
-    // Scales of a stage: waves 0-3 bring 64 rows of A each, waves 4-7 of B; B's tile
-    // scales are spread to one per row.  Chosen once per wave, so that the K loop
-    // has no branch: a stage's window starts sc_step floats after the one before.
-    const bool sc_a = wave < 4;
-    const int sc_row = (wave % 4) * kWave + lane;
-    const float* sc_base = sc_a ? p.sa + m0 : BROW ? p.sb + n0 : p.sb + n0 / kBlock * S;
-    const int64_t sc_step = sc_a ? p.M : BROW ? p.N : 1;
-    const int sc_size = (int)(sc_a ? rows_a : BROW ? rows_b : (rows_b + kBlock - 1) / kBlock * S) * 4;
-    const int sc_shrink = sc_a || BROW ? 0 : 4;  // the tile scales' window ends where it did
-    const int sc_off = (sc_a || BROW ? sc_row : sc_row / kBlock * S) * 4;
-    // Load L of stage s: the code loads, then the scales.  A stage past the range
-    // reads zero codes (and some other stage's scales).
-    auto issue = [&](int s, int L) {
-        uint8_t* stage = lds + (s & 1) * kStageBytes;
-        if (L < kLoads) {
-            const int k0 = s * kBlock;
-            const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
-            const int d = wave + kWaves * (L % (kLoads / 2));
-            uint8_t* dst = stage + (L < kLoads / 2 ? 0 : BM * kRowStage) + d * 8 * kRowStage;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? ra : rb, (LdsPtr)dst, 16, base + 8 * d * K, 0, 0, 0);
-        } else {
-            const int at = s < s_hi ? s : s_lo;
-            const Rsrc rs = make_rsrc(sc_base + at * sc_step, sc_size - at * sc_shrink);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(stage + kCodeBytes + wave * kWave * 4), 4, sc_off, 0, 0, 0);
-        }
-    };
-
+    const F8Tile t = dense_tile<BROW>(p, m0, n0, (int)rows_a, (int)rows_b, s_lo, s_hi);
     v4f acc[TB][TA];
-#pragma unroll
-    for (int i = 0; i < TB; ++i)
-#pragma unroll
-        for (int j = 0; j < TA; ++j) acc[i][j] = v4f{};
-
-    // Groups of products: the fragments of B against fragment j of A.  While a group's
-    // products run, the previous group's are scaled into the sums, the next
-    // fragment of A is read and loads of the next stage go out, kEarly per group: early
-    // enough to land within the stage, without a burst that fills the load queue.
-    // With one scale of B for all (kCarry), the last group's products of a stage are
-    // scaled in the next one, while its first operands are on their way from LDS.
-    constexpr bool kCarry = !BROW;
-    constexpr int kEarly = 2;
-    v4f t[2][TB];
-    float f_old = 0.0f, sb_old = 0.0f;
-#pragma unroll
-    for (int i = 0; i < TB; ++i) t[1][i] = v4f{};
-    const int a_row = wm * WM + lane % kF16;  // within the tile
-    const int b_row = wn * WN + lane % kF16;
-    const int a_lo = op_offset(a_row, lane, 0), a_hi = op_offset(a_row, lane, 1);
-    const int b_lo = BM * kRowStage + op_offset(b_row, lane, 0), b_hi = BM * kRowStage + op_offset(b_row, lane, 1);
-    auto scale_in = [&](int i, int j, const v4f& d, float f, const v4f& sb) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], BROW ? sb[e] * f : f, acc[i][j][e]);
-    };
-    if (s_lo < s_hi) {  // K = 0 has no operands to read
-#pragma unroll
-        for (int L = 0; L <= kLoads; ++L) issue(s_lo, L);
-    }
-    for (int s = s_lo; s < s_hi; ++s) {
-        const uint8_t* here = lds + (s & 1) * kStageBytes;
-        const float* fa = reinterpret_cast<const float*>(here + kCodeBytes) + a_row;
-        const float* fb = reinterpret_cast<const float*>(here + kCodeBytes) + BM + wn * WN;
-        // Stage s has landed, and no wave still reads stage s - 1.  (The compiler's own
-        // wait, so that it adds none before the first operands arrive.)
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-        asm volatile("s_barrier" ::: "memory");
-        v8i a_next = read_op(here + a_lo, here + a_hi, 0);
-        v8i b[TB];
-        v4f sb[BROW ? TB : 1];
-#pragma unroll
-        for (int i = 0; i < TB; ++i) {
-            __builtin_amdgcn_sched_barrier(0);  // the first products wait for as few reads as can be
-            b[i] = read_op(here + b_lo, here + b_hi, i);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        float f_next = fa[0];
-        const float sb_tile = BROW ? 1.0f : fb[0];
-        if (BROW) {
-#pragma unroll
-            for (int i = 0; i < TB; ++i) sb[BROW ? i : 0] = *reinterpret_cast<const v4f*>(fb + i * kF16 + 4 * (lane / kF16));
-        }
-#pragma unroll
-        for (int j = 0; j < TA; ++j) {
-            const v8i a = a_next;
-            const float f = f_next;
-            if (j + 1 < TA) {
-                a_next = read_op(here + a_lo, here + a_hi, j + 1);
-                f_next = fa[(j + 1) * kF16];
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            const float scale = BROW ? f_old : f_old * sb_old;
-#pragma unroll
-            for (int i = 0; i < TB; ++i) {
-                t[j % 2][i] = mma16(b[i], a);
-                if (kCarry || j > 0) scale_in(i, (j + TA - 1) % TA, t[(j + 1) % 2][i], scale, sb[BROW ? i : 0]);
-                __builtin_amdgcn_sched_barrier(0);
-                if (i == 0) {
-#pragma unroll
-                    for (int e = 0; e < kEarly; ++e)
-                        if (j * kEarly + e <= kLoads) issue(s + 1, j * kEarly + e);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
-            f_old = f;
-            if (j == 0) sb_old = sb_tile;
-        }
-        if (!kCarry) {
-#pragma unroll
-            for (int i = 0; i < TB; ++i) scale_in(i, TA - 1, t[1][i], f_old, sb[BROW ? i : 0]);
-        }
-    }
-    if (kCarry) {
-#pragma unroll
-        for (int i = 0; i < TB; ++i) scale_in(i, TA - 1, t[1][i], f_old * sb_old, v4f{});
-    }
-    if (__builtin_expect(not_finite(acc), 0))
-        sums_again<BROW, false>(acc, p, ra, rb, m0, n0, (int)rows_a, (int)rows_b, wm * WM, wn * WN, s_lo, s_hi, lane);
+    tile_sums<BROW, false>(acc, t, lds, wave, lane);
     wait_all_barrier();  // LDS is reused below
 
     void* c = splits > 1 ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.c;
@@ -289,12 +136,9 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
 template <int T, bool BROW, bool WIDE>
 __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_fp8_mid(F8Params p) {
     typedef MidPlan<T> P;
-    typedef Operand<WIDE> Op;
-    constexpr int F = P::kF;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wm = wave / 2, wn = wave % 2;
     const int64_t tiles_m = (p.M + T - 1) / T, tiles_n = (p.N + T - 1) / T;
     const int splits = p.splits;
     const unsigned group = p.first + blockIdx.x;
@@ -303,114 +147,18 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_fp8_mid(F8Params
     tile_of(group / splits, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = tm * T, n0 = tn * T;
     const int rows_a = (int)(p.M - m0 < T ? p.M - m0 : T), rows_b = (int)(p.N - n0 < T ? p.N - n0 : T);
-    const int K = (int)p.K, S = p.S;
+    const int S = p.S;
     const int per = (S + splits - 1) / splits;
     const int s_lo = split * per, s_hi = s_lo + per < S ? s_lo + per : S;
-    const Rsrc ra = make_rsrc(p.a + m0 * K, (int64_t)rows_a * K);
-    const Rsrc rb = make_rsrc(p.b + n0 * K, (int64_t)rows_b * K);
-
-    // Code load q of a wave moves rows 8 d .. 8 d + 7 of the 2 T (A's, then B's), d =
-    // 4 q + wave; slots as in the tile kernel (T is a multiple of 16).
-    const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
-    const int lane_off = (lane / 8) * K + piece * 16;
-    // Scales: waves 0 and 1 bring A's, 2 and 3 B's, 64 each (T = 64: the same twice).
-    const bool sc_a = wave < 2;
-    const int sc_row = (wave % 2 * kWave + lane) % T;
-    const float* sc_base = sc_a ? p.sa + m0 : BROW ? p.sb + n0 : p.sb + n0 / kBlock * S;
-    const int64_t sc_step = sc_a ? p.M : BROW ? p.N : 1;
-    const int sc_size = (sc_a ? rows_a : BROW ? rows_b : S) * 4;
-    const int sc_shrink = sc_a || BROW ? 0 : 4;
-    const int sc_off = sc_a || BROW ? sc_row * 4 : 0;  // a tile's 64 or 128 rows are in one block of B
-    auto issue = [&](int s) {
-        uint8_t* stage = lds + (s & 1) * P::kStage;
-        const int k0 = s * kBlock;
-        const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
-#pragma unroll
-        for (int q = 0; q < P::kCodeLoads; ++q) {
-            const int d = 4 * q + wave;
-            const bool is_a = q < P::kCodeLoads / 2;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (LdsPtr)(stage + d * 8 * kRowStage), 16,
-                                                     base + (is_a ? 8 * d : 8 * d - T) * K, 0, 0, 0);
-        }
-        const int at = s < s_hi ? s : s_lo;
-        const Rsrc rs = make_rsrc(sc_base + at * sc_step, sc_size - at * sc_shrink);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (LdsPtr)(stage + P::kCode + ((sc_a ? 0 : T) + wave % 2 * kWave % T) * 4), 4, sc_off, 0, 0, 0);
-    };
-
-    v4f acc[F][F];
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = v4f{};
-    const int a_row = wm * (T / 2) + lane % kF16, b_row = wn * (T / 2) + lane % kF16;
-    const int a_lo = op_offset(a_row, lane, 0), a_hi = op_offset(a_row, lane, 1);
-    const int b_lo = T * kRowStage + op_offset(b_row, lane, 0), b_hi = T * kRowStage + op_offset(b_row, lane, 1);
-    if (s_lo < s_hi) issue(s_lo);  // K = 0 has no operands to read
-    for (int s = s_lo; s < s_hi; ++s) {
-        const uint8_t* here = lds + (s & 1) * P::kStage;
-        // Stage s has landed, and no wave still reads stage s - 1.
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-        asm volatile("s_barrier" ::: "memory");
-        issue(s + 1);
-        const float* fa = reinterpret_cast<const float*>(here + P::kCode) + a_row;
-        const float* fb = reinterpret_cast<const float*>(here + P::kCode) + T + wn * (T / 2);
-        typename Op::T b[F];
-        v4f sb[BROW ? F : 1];
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-            b[i] = Op::of(read_op(here + b_lo, here + b_hi, i));
-            if (BROW) sb[i] = *reinterpret_cast<const v4f*>(fb + i * kF16 + 4 * (lane / kF16));
-        }
-        const float sb_tile = BROW ? 1.0f : fb[0];
-#pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const typename Op::T a = Op::of(read_op(here + a_lo, here + a_hi, j));
-            const float f = fa[j * kF16] * sb_tile;
-            v4f t[F];
-#pragma unroll
-            for (int i = 0; i < F; ++i) t[i] = mma16(b[i], a);
-#pragma unroll
-            for (int i = 0; i < F; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(t[i][e], BROW ? sb[i][e] * f : f, acc[i][j][e]);
-        }
-    }
-    if (__builtin_expect(not_finite(acc), 0))
-        sums_again<BROW, WIDE>(acc, p, ra, rb, m0, n0, rows_a, rows_b, wm * (T / 2), wn * (T / 2), s_lo, s_hi, lane);
+    v4f acc[P::kF][P::kF];
+    mid_sums<T, BROW, WIDE, false>(acc, dense_tile<BROW>(p, m0, n0, rows_a, rows_b, s_lo, s_hi), lds, wave, lane);
     wait_all_barrier();  // LDS is reused below
-
-    // The tile as binary32 in LDS, then whole row segments to memory.
-    float* st = reinterpret_cast<float*>(lds);
-#pragma unroll
-    for (int j = 0; j < F; ++j)
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-            *reinterpret_cast<v4f*>(st + (a_row + j * kF16) * P::kPitch + wn * (T / 2) + i * kF16 + 4 * (lane / kF16)) =
-                acc[i][j];
-    __syncthreads();
     void* c = splits > 1 ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.c;
     const int ct = splits > 1 ? 1 : p.ct;
     const int eb = ct == 1 ? 4 : 2;
     void* tile = static_cast<char*>(c) + m0 * p.N * eb;
-    const Rsrc rc = make_rsrc(tile, (int64_t)rows_a * p.N * eb);
     const bool whole = splits > 1 ? (p.N & 3) == 0 : p.whole;
-    const int units = T * eb / 16;  // 16-byte units per row
-    for (int u = threadIdx.x; u < rows_a * units; u += 256) {
-        const int r = u / units, col = u % units * (16 / eb);
-        const float* src = st + r * P::kPitch + col;
-        u32x4_t v;
-        if (ct == 1) {
-            v = *reinterpret_cast<const u32x4_t*>(src);
-        } else {
-            const v4f x = *reinterpret_cast<const v4f*>(src), y = *reinterpret_cast<const v4f*>(src + 4);
-            v = u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-        }
-        if (whole) __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < rows_b ? (int)((r * p.N + n0 + col) * eb) : kDropped, 0, kStoreNT);
-        else if (col >= rows_b) continue;
-        else if (ct == 1) store_unit<4>(tile, r, n0 + col, p.N, v);
-        else store_unit<2>(tile, r, n0 + col, p.N, v);
-    }
+    store_mid<T>(acc, lds, tile, ct, rows_a, rows_b, n0, p.N, whole, wave, lane);
 }
 
 // ---------------------------------------------------------------------------

@@ -25,6 +25,9 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <algorithm>
+
+#include "fp4q_groups.h"
 #include "fp4q_launch.h"
 
 namespace fp4q {
@@ -122,20 +125,35 @@ struct Fp8Lds {
     float col_s[kTile], col_r[kTile];
 };
 
+// Where a tile is and where what it gives goes.
+struct Fp8At {
+    int64_t r0, r_end;       // its first row, and the end of its matrix or group
+    int64_t tile_c;          // tile along the columns
+    int64_t scale, scale_t;  // TILE: places of its scales; else scale_t of its first transposed block's
+    uint8_t* codes_t;        // the transpose
+    int64_t t0;              // its first column there
+    int64_t t_bytes;         // columns there from t0 on
+};
+
+__device__ __forceinline__ Fp8At dense_at(const Fp8Params& p, unsigned tile, bool tiles) {
+    const int64_t tile_r = tile / p.tiles_c, tile_c = tile % p.tiles_c, r0 = tile_r * kTile;
+    return {r0, p.rows, tile_c, tile_r * p.tiles_c + tile_c,
+            tiles ? tile_c * ((p.rows + kTile - 1) / kTile) + tile_r : tile_r * p.cols, p.codes_t, r0, p.ld_t - r0};
+}
+
 // One workgroup's tile.  TILE: one scale per 128 x 128, else one per 128 of a row (and,
 // for the transposed output, of a column).  OUT, TOUT: which outputs are wanted; flip: 128
 // transposed rows, with TOUT.
 template <int XT, bool TILE, bool OUT, bool TOUT>
-__device__ __forceinline__ void quantize_tile(const Fp8Params& p, unsigned tile, Fp8Lds& lds, uint8_t* flip) {
+__device__ __forceinline__ void quantize_tile(const Fp8Params& p, const Fp8At& at, Fp8Lds& lds, uint8_t* flip) {
     typedef typename Elem<XT>::Bits Bits;
     auto& part = lds.part;
     auto& col_s = lds.col_s;
     auto& col_r = lds.col_r;
     const int t = threadIdx.x, i = t / 16, j = t % 16;
-    const int64_t tile_r = tile / p.tiles_c, tile_c = tile % p.tiles_c;
-    const int64_t r0 = tile_r * kTile, c0 = tile_c * kTile;
+    const int64_t tile_c = at.tile_c, r0 = at.r0, c0 = tile_c * kTile;
     const int64_t row0 = r0 + kSide * i, col0 = c0 + kSide * j;
-    const int n_rows = (int)min((int64_t)kSide, max((int64_t)0, p.rows - row0));
+    const int n_rows = (int)min((int64_t)kSide, max((int64_t)0, at.r_end - row0));
     const int n_cols = (int)min((int64_t)kSide, max((int64_t)0, p.cols - col0));
 
     // Rows need not start on any boundary past their element's: 8 elements are one
@@ -195,7 +213,7 @@ __device__ __forceinline__ void quantize_tile(const Fp8Params& p, unsigned tile,
             const float s = scale_of(m);
             col_s[t] = s;
             col_r[t] = 1.0f / s;
-            if (c0 + t < p.cols) p.scales_t[tile_r * p.cols + c0 + t] = s;
+            if (c0 + t < p.cols) p.scales_t[at.scale_t + c0 + t] = s;
         }
         __syncthreads();
     }
@@ -214,8 +232,8 @@ __device__ __forceinline__ void quantize_tile(const Fp8Params& p, unsigned tile,
 #pragma unroll
         for (int a = 0; a < 8; ++a) s[a] = sc, r[a] = rc;
         if (t == 0) {
-            if (OUT) p.scales[tile_r * p.tiles_c + tile_c] = sc;
-            if (TOUT) p.scales_t[tile_c * ((p.rows + kTile - 1) / kTile) + tile_r] = sc;
+            if (OUT) p.scales[at.scale] = sc;
+            if (TOUT) p.scales_t[at.scale_t] = sc;
         }
     } else if (OUT) {
         // Lane j of a row group forms the scale of its row j (mod 8), and hands it out.
@@ -269,11 +287,11 @@ __device__ __forceinline__ void quantize_tile(const Fp8Params& p, unsigned tile,
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int c = k * 32 + t / 8;
-            const int64_t at = r0 + 16 * (t % 8);
+            const int64_t col = 16 * (t % 8);
             const uint2 lo = *reinterpret_cast<const uint2*>(flip + c * kPitch + 16 * (t % 8));
             const uint2 hi = *reinterpret_cast<const uint2*>(flip + c * kPitch + 16 * (t % 8) + 8);
-            if (c0 + c < p.cols && at < p.ld_t)
-                *reinterpret_cast<uint4*>(p.codes_t + (c0 + c) * p.ld_t + at) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            if (c0 + c < p.cols && col < at.t_bytes)
+                *reinterpret_cast<uint4*>(at.codes_t + (c0 + c) * p.ld_t + at.t0 + col) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
     }
 }
@@ -282,7 +300,7 @@ template <int XT, bool TILE, bool OUT, bool TOUT>
 __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Fp8Params p) {
     __shared__ Fp8Lds lds;
     __shared__ __attribute__((aligned(16))) uint8_t flip[TOUT ? kTile * kPitch : 16];
-    quantize_tile<XT, TILE, OUT, TOUT>(p, p.first + blockIdx.x, lds, flip);
+    quantize_tile<XT, TILE, OUT, TOUT>(p, dense_at(p, p.first + blockIdx.x, TILE), lds, flip);
 }
 
 // A linear layer's input (row scales) and weight (tile scales), both outputs of each, in
@@ -292,8 +310,56 @@ template <int XT, int WT>
 __global__ __launch_bounds__(kThreads) void k_fp8_quantize_two(Fp8Params x, Fp8Params w, unsigned x_tiles) {
     __shared__ Fp8Lds lds;
     __shared__ __attribute__((aligned(16))) uint8_t flip[kTile * kPitch];
-    if (blockIdx.x < x_tiles) quantize_tile<XT, false, true, true>(x, blockIdx.x, lds, flip);
-    else quantize_tile<WT, true, true, true>(w, blockIdx.x - x_tiles, lds, flip);
+    if (blockIdx.x < x_tiles) quantize_tile<XT, false, true, true>(x, dense_at(x, blockIdx.x, false), lds, flip);
+    else quantize_tile<WT, true, true, true>(w, dense_at(w, blockIdx.x - x_tiles, true), lds, flip);
+}
+
+// Rows in groups, row scales.  The transpose's blocks start at each group's first row: a group's
+// rows are columns of their own there, rounded up to whole blocks (the rest zeros).
+__device__ __forceinline__ bool group_at(const Fp8Params& p, const Groups& g, unsigned tile, Fp8At& at) {
+    const int tiles_c = (int)p.tiles_c;
+    const int tile_r = (int)(tile / (unsigned)tiles_c);
+    const GroupTile t = group_tile(g, kTile, tile_r);
+    const int64_t t0 = (int64_t)tile_r * kTile;
+    if (t.group < 0 || (p.codes_t && t0 + kTile > p.ld_t)) return false;
+    at = {t.row, t.end, (int64_t)(tile - (unsigned)tile_r * tiles_c), 0, tile_r * p.cols, p.codes_t, t0, kTile};
+    return true;
+}
+
+// A matrix per expert, tile scales: p.rows and p.ld_t are one expert's.
+__device__ __forceinline__ Fp8At expert_at(const Fp8Params& p, int64_t rows, unsigned tile) {
+    const int64_t tile_r = tile / p.tiles_c, tile_c = tile % p.tiles_c;
+    const int64_t per = (rows + kTile - 1) / kTile, e = tile_r / per, i = tile_r % per;
+    return {e * rows + i * kTile, (e + 1) * rows, tile_c, tile_r * p.tiles_c + tile_c, (e * p.tiles_c + tile_c) * per + i,
+            p.codes_t + e * p.cols * p.ld_t, i * kTile, p.ld_t - i * kTile};
+}
+
+template <int XT, bool OUT, bool TOUT>
+__global__ __launch_bounds__(kThreads) void k_fp8_quantize_groups(Fp8Params p, Groups g) {
+    __shared__ Fp8Lds lds;
+    __shared__ __attribute__((aligned(16))) uint8_t flip[TOUT ? kTile * kPitch : 16];
+    Fp8At at;
+    if (group_at(p, g, p.first + blockIdx.x, at)) quantize_tile<XT, false, OUT, TOUT>(p, at, lds, flip);
+}
+
+template <int WT, bool TOUT>
+__global__ __launch_bounds__(kThreads) void k_fp8_quantize_experts(Fp8Params p, int64_t rows) {
+    __shared__ Fp8Lds lds;
+    __shared__ __attribute__((aligned(16))) uint8_t flip[TOUT ? kTile * kPitch : 16];
+    quantize_tile<WT, true, true, TOUT>(p, expert_at(p, rows, p.first + blockIdx.x), lds, flip);
+}
+
+// An expert layer's rows and weights, all outputs, in one launch.
+template <int XT, int WT>
+__global__ __launch_bounds__(kThreads) void k_fp8_quantize_grouped(Fp8Params x, Groups g, unsigned x_tiles, Fp8Params w, int64_t rows) {
+    __shared__ Fp8Lds lds;
+    __shared__ __attribute__((aligned(16))) uint8_t flip[kTile * kPitch];
+    if (blockIdx.x < x_tiles) {
+        Fp8At at;
+        if (group_at(x, g, blockIdx.x, at)) quantize_tile<XT, false, true, true>(x, at, lds, flip);
+    } else {
+        quantize_tile<WT, true, true, true>(w, expert_at(w, rows, blockIdx.x - x_tiles), lds, flip);
+    }
 }
 
 template <int XT, bool TILE>
@@ -346,6 +412,83 @@ int launch_fp8_quantize_two(const Fp8QuantJob& x, const Fp8QuantJob& w, char* ms
     else if (x.xt == 0) FP4Q_LAUNCH((k_fp8_quantize_two<0, 1>), grid, block, 0, stream, px, pw, n);
     else if (w.xt == 0) FP4Q_LAUNCH((k_fp8_quantize_two<1, 0>), grid, block, 0, stream, px, pw, n);
     else FP4Q_LAUNCH((k_fp8_quantize_two<1, 1>), grid, block, 0, stream, px, pw, n);
+    return launch_status(msg, msg_len);
+}
+
+int64_t fp8_group_blocks(int64_t rows, int64_t groups) {
+    // A group that holds a row ends inside at most one block.
+    return (rows + (kTile - 1) * std::min(rows, groups)) / kTile;
+}
+
+namespace {
+// Groups of x's rows; what the transpose's rows hold (all groups' blocks).
+Fp8Params group_params(const Fp8GroupQuantJob& j) {
+    Fp8Params p = params_of({j.x, j.xt, j.rows, j.cols, false, j.codes, j.scales, j.codes_t, j.scales_t, j.stream});
+    p.ld_t = fp8_group_blocks(j.rows, j.groups) * kTile;
+    return p;
+}
+Fp8Params expert_params(const Fp8ExpertQuantJob& j) {
+    Fp8Params p = params_of({j.w, j.wt, j.rows, j.cols, true, j.codes, j.scales, j.codes_t, j.scales_t, j.stream});
+    p.rows = j.rows * j.experts;
+    return p;
+}
+int64_t group_quant_tiles(const Fp8GroupQuantJob& j, const Fp8Params& p) { return fp8_group_blocks(j.rows, j.groups) * p.tiles_c; }
+int64_t expert_quant_tiles(const Fp8ExpertQuantJob& j, const Fp8Params& p) { return j.experts * ((j.rows + kTile - 1) / kTile) * p.tiles_c; }
+
+template <int XT>
+void launch_groups(const Fp8Params& p, const Groups& g, unsigned grid, hipStream_t stream) {
+    if (p.codes && p.codes_t) FP4Q_LAUNCH((k_fp8_quantize_groups<XT, true, true>), dim3(grid), dim3(kThreads), 0, stream, p, g);
+    else if (p.codes) FP4Q_LAUNCH((k_fp8_quantize_groups<XT, true, false>), dim3(grid), dim3(kThreads), 0, stream, p, g);
+    else FP4Q_LAUNCH((k_fp8_quantize_groups<XT, false, true>), dim3(grid), dim3(kThreads), 0, stream, p, g);
+}
+}  // namespace
+
+int launch_fp8_quantize_groups(const Fp8GroupQuantJob& j, char* msg, size_t msg_len) {
+    if (j.rows == 0 || j.cols == 0 || (!j.codes && !j.codes_t)) return 0;
+    Fp8Params p = group_params(j);
+    const Groups g{j.offsets, (int)j.groups, (int)j.rows, false};
+    const int64_t tiles = group_quant_tiles(j, p);
+    for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+        const unsigned grid = (unsigned)std::min(tiles - first, kMaxGrid);
+        p.first = (unsigned)first;
+        if (j.xt == 0) launch_groups<0>(p, g, grid, static_cast<hipStream_t>(j.stream));
+        else launch_groups<1>(p, g, grid, static_cast<hipStream_t>(j.stream));
+    }
+    return launch_status(msg, msg_len);
+}
+
+int launch_fp8_quantize_experts(const Fp8ExpertQuantJob& j, char* msg, size_t msg_len) {
+    if (j.rows == 0 || j.cols == 0) return 0;
+    Fp8Params p = expert_params(j);
+    hipStream_t stream = static_cast<hipStream_t>(j.stream);
+    const int64_t tiles = expert_quant_tiles(j, p);
+    for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+        const dim3 grid((unsigned)std::min(tiles - first, kMaxGrid));
+        p.first = (unsigned)first;
+        if (j.wt == 0 && p.codes_t) FP4Q_LAUNCH((k_fp8_quantize_experts<0, true>), grid, dim3(kThreads), 0, stream, p, j.rows);
+        else if (j.wt == 0) FP4Q_LAUNCH((k_fp8_quantize_experts<0, false>), grid, dim3(kThreads), 0, stream, p, j.rows);
+        else if (p.codes_t) FP4Q_LAUNCH((k_fp8_quantize_experts<1, true>), grid, dim3(kThreads), 0, stream, p, j.rows);
+        else FP4Q_LAUNCH((k_fp8_quantize_experts<1, false>), grid, dim3(kThreads), 0, stream, p, j.rows);
+    }
+    return launch_status(msg, msg_len);
+}
+
+int launch_fp8_quantize_grouped(const Fp8GroupQuantJob& x, const Fp8ExpertQuantJob& w, char* msg, size_t msg_len) {
+    const bool all = x.rows > 0 && x.cols > 0 && w.rows > 0 && x.codes && x.codes_t && w.codes_t;
+    const Fp8Params px = group_params(x), pw = expert_params(w);
+    const int64_t tx = group_quant_tiles(x, px), tiles = tx + expert_quant_tiles(w, pw);
+    if (!all || tiles > kMaxGrid) {
+        const int rc = launch_fp8_quantize_groups(x, msg, msg_len);
+        return rc ? rc : launch_fp8_quantize_experts(w, msg, msg_len);
+    }
+    const Groups g{x.offsets, (int)x.groups, (int)x.rows, false};
+    hipStream_t stream = static_cast<hipStream_t>(x.stream);
+    const dim3 grid((unsigned)tiles), block(kThreads);
+    const unsigned n = (unsigned)tx;
+    if (x.xt == 0 && w.wt == 0) FP4Q_LAUNCH((k_fp8_quantize_grouped<0, 0>), grid, block, 0, stream, px, g, n, pw, w.rows);
+    else if (x.xt == 0) FP4Q_LAUNCH((k_fp8_quantize_grouped<0, 1>), grid, block, 0, stream, px, g, n, pw, w.rows);
+    else if (w.wt == 0) FP4Q_LAUNCH((k_fp8_quantize_grouped<1, 0>), grid, block, 0, stream, px, g, n, pw, w.rows);
+    else FP4Q_LAUNCH((k_fp8_quantize_grouped<1, 1>), grid, block, 0, stream, px, g, n, pw, w.rows);
     return launch_status(msg, msg_len);
 }
 

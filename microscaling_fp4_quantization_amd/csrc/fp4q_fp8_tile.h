@@ -201,5 +201,341 @@ struct MidPlan {
     static constexpr int kLds = 2 * kStage > T * kPitch * 4 ? 2 * kStage : T * kPitch * 4;
 };
 
+// One tile of a product of E4M3 operands: where its rows, K blocks and scales are.
+struct F8Tile {
+    Rsrc ra, rb;            // rows of K bytes
+    int rows_a, rows_b;
+    int K, s_lo, s_hi;      // K blocks s_lo .. s_hi - 1 of the rows' K bytes
+    const float* sa;        // the scales of A's rows in block s start at sa + s * sa_step, sa_size bytes
+    int64_t sa_step;
+    int sa_size;
+    const float* sb;        // B's at sb + s * sb_step, sb_size bytes less sb_shrink for each s:
+    int64_t sb_step;
+    int sb_size, sb_shrink;
+    int sb_tile;            // 0: one a row; else tile scales, sb_tile of them along K, and the
+    int sb_phase;           // tile's first row is this one of its block (BROW; else 0)
+    const int* rows;        // GATHER: row r of the tile is row rows[r] of A (none: zeros)
+    int rows_all;           // of A
+
+    // Row r of the tile in A, or -1.
+    template <bool GATHER>
+    __device__ __forceinline__ int a_row(int r) const {
+        if (!GATHER) return r;
+        const int at = r < rows_a ? rows[r] : -1;
+        return at >= 0 && at < rows_all ? at : -1;
+    }
+    template <bool BROW>
+    __device__ __forceinline__ int sb_at(int r) const {
+        if (!BROW) return r / kBlock * sb_tile;
+        return sb_tile ? (r + sb_phase) / kBlock * sb_tile : r;
+    }
+};
+
+// A wave's sums formed again, for scales whose product passes binary32's range: operands and
+// scales straight from memory, no LDS and no barrier.  NA and NB fragments of 16 rows from
+// row a0 and b0 of the tile.
+template <bool BROW, bool WIDE, bool GATHER, int NA, int NB>
+__device__ __forceinline__ void sums_again(v4f (&acc)[NB][NA], const F8Tile& t, int a0, int b0, int lane) {
+    const int r = lane % kF16, q = lane / kF16;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < NA; ++j) acc[i][j] = v4f{};
+    auto codes = [&](Rsrc w, int row, int s) {
+        u32x4_t half[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pos = s * kBlock + h * 64 + q * 16;
+            half[h] = __builtin_amdgcn_raw_buffer_load_b128(w, row >= 0 && pos < t.K ? row * t.K + pos : kDropped, 0, 0);
+        }
+        return Operand<WIDE>::of(join(__builtin_bit_cast(v4i, half[0]), __builtin_bit_cast(v4i, half[1])));
+    };
+    auto scale = [](Rsrc w, int at) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w, at < 0 ? kDropped : at * 4, 0, 0)); };
+    for (int s = t.s_lo; s < t.s_hi; ++s) {
+        const Rsrc rsa = make_rsrc(t.sa + s * t.sa_step, t.sa_size);
+        const Rsrc rsb = make_rsrc(t.sb + s * t.sb_step, t.sb_size - s * t.sb_shrink);
+        for (int i = 0; i < NB; ++i) {
+            const typename Operand<WIDE>::T b = codes(t.rb, b0 + i * kF16 + r, s);
+            float sb[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sb[e] = scale(rsb, t.sb_at<BROW>(b0 + i * kF16 + 4 * q + e));
+#pragma unroll
+            for (int j = 0; j < NA; ++j) {
+                const int row = t.a_row<GATHER>(a0 + j * kF16 + r);
+                const v4f d = mma16(b, codes(t.ra, row, s));
+                const float sa = scale(rsa, row);
+#pragma unroll
+                for (int k = 0; k < NB; ++k)  // (registers have no run-time index)
+                    if (k == i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[k][j][e] = scaled_sum(d[e], sa, sb[e], acc[k][j][e]);
+            }
+        }
+    }
+}
+
+// The sums of a 256 x 256 tile by 8 waves (2 x 4 of 128 x 64), through two LDS stages of
+// kStageBytes.  BROW: B's scales differ within 64 rows; else one goes for all of a wave's.
+template <bool BROW, bool GATHER>
+__device__ __forceinline__ void tile_sums(v4f (&acc)[TB][TA], const F8Tile& t, uint8_t* lds, int wave, int lane) {
+    const int wm = wave >> 2, wn = wave & 3;
+    // Code load q of a wave moves rows 8 d .. 8 d + 7, d = wave + 8 (q % 4), of A
+    // (q < 4) or B: lane l fetches row 8 d + l / 8 into slot l % 8 of that row (row /
+    // 2 = 4 d + l / 16 and d = wave mod 2, so that the piece is the same for every q).
+    const int K = t.K, s_lo = t.s_lo, s_hi = t.s_hi;
+    const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
+    const int lane_off = (lane / 8) * K + piece * 16;
+    int a_off[GATHER ? kLoads / 2 : 1];
+    if (GATHER) {
+#pragma unroll
+        for (int q = 0; q < kLoads / 2; ++q) {
+            const int row = t.a_row<GATHER>(8 * (wave + kWaves * q) + lane / 8);
+            a_off[GATHER ? q : 0] = row >= 0 ? row * K + piece * 16 : -1;
+        }
+    }
+    // Scales of a stage: waves 0-3 bring 64 rows of A each, waves 4-7 of B; B's tile
+    // scales are spread to one per row.  Chosen once per wave, so that the K loop
+    // has no branch: a stage's window starts sc_step floats after the one before.
+    const bool sc_a = wave < 4;
+    const int sc_row = (wave % 4) * kWave + lane;
+    const float* sc_base = sc_a ? t.sa : t.sb;
+    const int64_t sc_step = sc_a ? t.sa_step : t.sb_step;
+    const int sc_size = sc_a ? t.sa_size : t.sb_size;
+    const int sc_shrink = sc_a ? 0 : t.sb_shrink;  // tile scales' window ends where it did
+    const int sc_at = sc_a ? t.a_row<GATHER>(sc_row) : t.sb_at<BROW>(sc_row);
+    const int sc_off = GATHER && sc_at < 0 ? kDropped : sc_at * 4;
+    // Load L of stage s: the code loads, then the scales.  A stage past the range
+    // reads zero codes (and some other stage's scales).
+    auto issue = [&](int s, int L) {
+        uint8_t* stage = lds + (s & 1) * kStageBytes;
+        if (L < kLoads) {
+            const int k0 = s * kBlock;
+            const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
+            const int d = wave + kWaves * (L % (kLoads / 2));
+            uint8_t* dst = stage + (L < kLoads / 2 ? 0 : BM * kRowStage) + d * 8 * kRowStage;
+            int off = base + 8 * d * K;
+            if (GATHER && L < kLoads / 2) off = base == kPastWindow || a_off[GATHER ? L : 0] < 0 ? kDropped : a_off[GATHER ? L : 0] + k0;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? t.ra : t.rb, (LdsPtr)dst, 16, off, 0, 0, 0);
+        } else {
+            const int at = s < s_hi ? s : s_lo;
+            const Rsrc rs = make_rsrc(sc_base + at * sc_step, sc_size - at * sc_shrink);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(stage + kCodeBytes + wave * kWave * 4), 4, sc_off, 0, 0, 0);
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+        for (int j = 0; j < TA; ++j) acc[i][j] = v4f{};
+
+    // Groups of products: the fragments of B against fragment j of A.  While a group's
+    // products run, the previous group's are scaled into the sums, the next
+    // fragment of A is read and loads of the next stage go out, kEarly per group: early
+    // enough to land within the stage, without a burst that fills the load queue.
+    // With one scale of B for all (kCarry), the last group's products of a stage are
+    // scaled in the next one, while its first operands are on their way from LDS.
+    constexpr bool kCarry = !BROW;
+    constexpr int kEarly = 2;
+    v4f d[2][TB];
+    float f_old = 0.0f, sb_old = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TB; ++i) d[1][i] = v4f{};
+    const int a_row = wm * WM + lane % kF16;  // within the tile
+    const int b_row = wn * WN + lane % kF16;
+    const int a_lo = op_offset(a_row, lane, 0), a_hi = op_offset(a_row, lane, 1);
+    const int b_lo = BM * kRowStage + op_offset(b_row, lane, 0), b_hi = BM * kRowStage + op_offset(b_row, lane, 1);
+    auto scale_in = [&](int i, int j, const v4f& p, float f, const v4f& sb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], BROW ? sb[e] * f : f, acc[i][j][e]);
+    };
+    if (s_lo < s_hi) {  // K = 0 has no operands to read
+#pragma unroll
+        for (int L = 0; L <= kLoads; ++L) issue(s_lo, L);
+    }
+    for (int s = s_lo; s < s_hi; ++s) {
+        const uint8_t* here = lds + (s & 1) * kStageBytes;
+        const float* fa = reinterpret_cast<const float*>(here + kCodeBytes) + a_row;
+        const float* fb = reinterpret_cast<const float*>(here + kCodeBytes) + BM + wn * WN;
+        // Stage s has landed, and no wave still reads stage s - 1.  (The compiler's own
+        // wait, so that it adds none before the first operands arrive.)
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+        v8i a_next = read_op(here + a_lo, here + a_hi, 0);
+        v8i b[TB];
+        v4f sb[BROW ? TB : 1];
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // the first products wait for as few reads as can be
+            b[i] = read_op(here + b_lo, here + b_hi, i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float f_next = fa[0];
+        const float sb_tile = BROW ? 1.0f : fb[0];
+        if (BROW) {
+#pragma unroll
+            for (int i = 0; i < TB; ++i) sb[BROW ? i : 0] = *reinterpret_cast<const v4f*>(fb + i * kF16 + 4 * (lane / kF16));
+        }
+#pragma unroll
+        for (int j = 0; j < TA; ++j) {
+            const v8i a = a_next;
+            const float f = f_next;
+            if (j + 1 < TA) {
+                a_next = read_op(here + a_lo, here + a_hi, j + 1);
+                f_next = fa[(j + 1) * kF16];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const float scale = BROW ? f_old : f_old * sb_old;
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+                d[j % 2][i] = mma16(b[i], a);
+                if (kCarry || j > 0) scale_in(i, (j + TA - 1) % TA, d[(j + 1) % 2][i], scale, sb[BROW ? i : 0]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (i == 0) {
+#pragma unroll
+                    for (int e = 0; e < kEarly; ++e)
+                        if (j * kEarly + e <= kLoads) issue(s + 1, j * kEarly + e);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            f_old = f;
+            if (j == 0) sb_old = sb_tile;
+        }
+        if (!kCarry) {
+#pragma unroll
+            for (int i = 0; i < TB; ++i) scale_in(i, TA - 1, d[1][i], f_old, sb[BROW ? i : 0]);
+        }
+    }
+    if (kCarry) {
+#pragma unroll
+        for (int i = 0; i < TB; ++i) scale_in(i, TA - 1, d[1][i], f_old * sb_old, v4f{});
+    }
+    if (__builtin_expect(not_finite(acc), 0))
+        sums_again<BROW, false, GATHER>(acc, t, wm * WM, wn * WN, lane);
+}
+
+// The sums of a T x T tile by 4 waves, through two LDS stages.
+template <int T, bool BROW, bool WIDE, bool GATHER>
+__device__ __forceinline__ void mid_sums(v4f (&acc)[MidPlan<T>::kF][MidPlan<T>::kF], const F8Tile& t, uint8_t* lds, int wave, int lane) {
+    typedef MidPlan<T> P;
+    typedef Operand<WIDE> Op;
+    constexpr int F = P::kF;
+    const int wm = wave / 2, wn = wave % 2;
+    // Code load q of a wave moves rows 8 d .. 8 d + 7 of the 2 T (A's, then B's), d =
+    // 4 q + wave; slots as in the tile kernel (T is a multiple of 16).
+    const int K = t.K, s_lo = t.s_lo, s_hi = t.s_hi;
+    const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
+    const int lane_off = (lane / 8) * K + piece * 16;
+    int a_off[GATHER ? P::kCodeLoads / 2 : 1];
+    if (GATHER) {
+#pragma unroll
+        for (int q = 0; q < P::kCodeLoads / 2; ++q) {
+            const int row = t.a_row<GATHER>(8 * (4 * q + wave) + lane / 8);
+            a_off[GATHER ? q : 0] = row >= 0 ? row * K + piece * 16 : -1;
+        }
+    }
+    // Scales: waves 0 and 1 bring A's, 2 and 3 B's, 64 each (T = 64: the same twice).
+    const bool sc_a = wave < 2;
+    const int sc_row = (wave % 2 * kWave + lane) % T;
+    const float* sc_base = sc_a ? t.sa : t.sb;
+    const int64_t sc_step = sc_a ? t.sa_step : t.sb_step;
+    const int sc_size = sc_a ? t.sa_size : t.sb_size;
+    const int sc_shrink = sc_a ? 0 : t.sb_shrink;
+    const int sc_at = sc_a ? t.a_row<GATHER>(sc_row) : BROW ? t.sb_at<BROW>(sc_row) : 0;  // else one block holds the tile's rows of B
+    const int sc_off = GATHER && sc_at < 0 ? kDropped : sc_at * 4;
+    auto issue = [&](int s) {
+        uint8_t* stage = lds + (s & 1) * P::kStage;
+        const int k0 = s * kBlock;
+        const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
+#pragma unroll
+        for (int q = 0; q < P::kCodeLoads; ++q) {
+            const int d = 4 * q + wave;
+            const bool is_a = q < P::kCodeLoads / 2;
+            int off = base + (is_a ? 8 * d : 8 * d - T) * K;
+            if (GATHER && is_a) off = base == kPastWindow || a_off[GATHER ? q : 0] < 0 ? kDropped : a_off[GATHER ? q : 0] + k0;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? t.ra : t.rb, (LdsPtr)(stage + d * 8 * kRowStage), 16, off, 0, 0, 0);
+        }
+        const int at = s < s_hi ? s : s_lo;
+        const Rsrc rs = make_rsrc(sc_base + at * sc_step, sc_size - at * sc_shrink);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, (LdsPtr)(stage + P::kCode + ((sc_a ? 0 : T) + wave % 2 * kWave % T) * 4), 4, sc_off, 0, 0, 0);
+    };
+
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = v4f{};
+    const int a_row = wm * (T / 2) + lane % kF16, b_row = wn * (T / 2) + lane % kF16;
+    const int a_lo = op_offset(a_row, lane, 0), a_hi = op_offset(a_row, lane, 1);
+    const int b_lo = T * kRowStage + op_offset(b_row, lane, 0), b_hi = T * kRowStage + op_offset(b_row, lane, 1);
+    if (s_lo < s_hi) issue(s_lo);  // K = 0 has no operands to read
+    for (int s = s_lo; s < s_hi; ++s) {
+        const uint8_t* here = lds + (s & 1) * P::kStage;
+        // Stage s has landed, and no wave still reads stage s - 1.
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+        issue(s + 1);
+        const float* fa = reinterpret_cast<const float*>(here + P::kCode) + a_row;
+        const float* fb = reinterpret_cast<const float*>(here + P::kCode) + T + wn * (T / 2);
+        typename Op::T b[F];
+        v4f sb[BROW ? F : 1];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            b[i] = Op::of(read_op(here + b_lo, here + b_hi, i));
+            if (BROW) sb[i] = *reinterpret_cast<const v4f*>(fb + i * kF16 + 4 * (lane / kF16));
+        }
+        const float sb_tile = BROW ? 1.0f : fb[0];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const typename Op::T a = Op::of(read_op(here + a_lo, here + a_hi, j));
+            const float f = fa[j * kF16] * sb_tile;
+            v4f d[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) d[i] = mma16(b[i], a);
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[i][e], BROW ? sb[i][e] * f : f, acc[i][j][e]);
+        }
+    }
+    if (__builtin_expect(not_finite(acc), 0))
+        sums_again<BROW, WIDE, GATHER>(acc, t, wm * (T / 2), wn * (T / 2), lane);
+}
+
+// The tile through LDS (after a barrier) as binary32, then whole row segments to memory.  tile: C's
+// row 0 of the tile, N elements a row (ct: 0 bf16, 1 f32), columns from n0 on.
+template <int T>
+__device__ __forceinline__ void store_mid(const v4f (&acc)[MidPlan<T>::kF][MidPlan<T>::kF], uint8_t* lds, void* tile, int ct, int rows_a,
+                                          int rows_b, int64_t n0, int64_t N, bool whole, int wave, int lane) {
+    typedef MidPlan<T> P;
+    constexpr int F = P::kF;
+    const int wn = wave % 2, a_row = wave / 2 * (T / 2) + lane % kF16;
+    const int eb = ct == 1 ? 4 : 2;
+    const Rsrc rc = make_rsrc(tile, (int64_t)rows_a * N * eb);
+    float* st = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+            *reinterpret_cast<v4f*>(st + (a_row + j * kF16) * P::kPitch + wn * (T / 2) + i * kF16 + 4 * (lane / kF16)) =
+                acc[i][j];
+    __syncthreads();
+    const int units = T * eb / 16;  // 16-byte units per row
+    for (int u = threadIdx.x; u < rows_a * units; u += 256) {
+        const int r = u / units, col = u % units * (16 / eb);
+        const float* src = st + r * P::kPitch + col;
+        u32x4_t v;
+        if (ct == 1) {
+            v = *reinterpret_cast<const u32x4_t*>(src);
+        } else {
+            const v4f x = *reinterpret_cast<const v4f*>(src), y = *reinterpret_cast<const v4f*>(src + 4);
+            v = u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+        }
+        if (whole) __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < rows_b ? (int)((r * N + n0 + col) * eb) : kDropped, 0, kStoreNT);
+        else if (col >= rows_b) continue;
+        else if (ct == 1) store_unit<4>(tile, r, n0 + col, N, v);
+        else store_unit<2>(tile, r, n0 + col, N, v);
+    }
+}
+
 }  // namespace
 }  // namespace fp4q

@@ -145,6 +145,83 @@ struct Fp8GemmJob {
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int ct);
 
+// Rows in groups: group e owns rows offsets[e] .. offsets[e + 1] - 1 (device, groups + 1 of them).
+// Row scales; the transpose holds fp8_group_blocks() blocks of 128 columns, each group's own from a
+// whole block on: codes_t cols x (128 blocks), scales_t blocks x cols.
+struct Fp8GroupQuantJob {
+    const void* x;
+    int xt;            // 0 bf16, 1 f32
+    int64_t rows, cols;
+    const int* offsets;
+    int64_t groups;
+    uint8_t* codes;    // nullable, as codes_t
+    float* scales;     // ceil(cols / 128) x rows
+    uint8_t* codes_t;
+    float* scales_t;
+    void* stream;
+};
+// Blocks that the groups take at most.
+int64_t fp8_group_blocks(int64_t rows, int64_t groups);
+
+// One matrix per expert, tile scales of each: codes (experts x rows) x ld, codes_t experts x cols x
+// ld_t (nullable), scales and scales_t alike.
+struct Fp8ExpertQuantJob {
+    const void* w;
+    int wt;            // 0 bf16, 1 f32
+    int64_t experts, rows, cols;
+    uint8_t* codes;
+    float* scales;
+    uint8_t* codes_t;
+    float* scales_t;
+    void* stream;
+};
+
+// A product per group of A's rows with its expert's matrix: C[i] = A[tokens[i]] W_e^T.
+struct GroupedGemmJob {
+    const uint8_t* a_codes;
+    const float* a_scales;   // ceil(K / 128) x a_rows
+    int64_t a_rows;
+    const uint8_t* b_codes;  // (experts x N) x K
+    const float* b_scales;
+    bool stacked;            // tile scales of the stacked matrix; else of each expert's
+    const int* offsets;
+    int64_t experts;
+    const int* tokens;       // nullable: row i of C is row i of A
+    int64_t rows, N, K;
+    void* c;
+    int ct;                  // 0 bf16, 1 f32
+    bool clear_rest;         // rows behind the last group: zeros, else left as they are
+    void* stream;
+};
+
+// A weight gradient per group: dW_e = At_e Bt_e^T over the group's blocks of transposed operands
+// as Fp8GroupQuantJob writes them.
+struct GroupedOuterJob {
+    const uint8_t* a_codes;  // M x (128 blocks)
+    const float* a_scales;   // blocks x M
+    const uint8_t* b_codes;  // N x (128 blocks)
+    const float* b_scales;
+    const int* offsets;
+    int64_t experts, rows, M, N;
+    void* c;                 // experts x M x N
+    int ct;
+    void* stream;
+};
+
+// The slots of a routing by expert.
+struct ExpertOrderJob {
+    const void* ids;   // tokens x top_k
+    bool wide;         // int64 (else int32)
+    int64_t tokens, top_k, experts;
+    int* offsets;      // experts + 1
+    int* order;        // slot of each sorted row
+    int* token;        // its token
+    int* position;     // sorted row of each slot
+    void* ws;          // expert_order_workspace_bytes() bytes
+    void* stream;
+};
+size_t expert_order_workspace_bytes(int64_t slots, int64_t experts);
+
 // 8-bit integers with a binary32 scale per row.
 struct Int8QuantJob {
     const void* x;
@@ -252,6 +329,13 @@ int launch_fp8_quantize(const Fp8QuantJob& j, char* msg, size_t msg_len);
 // x under row scales and w under tile scales: one launch where both outputs of both are wanted.
 int launch_fp8_quantize_two(const Fp8QuantJob& x, const Fp8QuantJob& w, char* msg, size_t msg_len);
 int launch_fp8_gemm(const Fp8GemmJob& j, char* msg, size_t msg_len);
+int launch_fp8_quantize_groups(const Fp8GroupQuantJob& j, char* msg, size_t msg_len);
+int launch_fp8_quantize_experts(const Fp8ExpertQuantJob& j, char* msg, size_t msg_len);
+// Both: one launch where all outputs of both are wanted.
+int launch_fp8_quantize_grouped(const Fp8GroupQuantJob& x, const Fp8ExpertQuantJob& w, char* msg, size_t msg_len);
+int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len);
+int launch_grouped_outer(const GroupedOuterJob& j, char* msg, size_t msg_len);
+int launch_expert_order(const ExpertOrderJob& j, char* msg, size_t msg_len);
 int launch_int8_quantize(const Int8QuantJob& j, char* msg, size_t msg_len);
 int launch_int8_gemm(const Int8GemmJob& j, char* msg, size_t msg_len);
 int launch_moe(const MoeJob& j, char* msg, size_t msg_len);

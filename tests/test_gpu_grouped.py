@@ -1,0 +1,483 @@
+"""expert_order, fp8_grouped_gemm_b128 and fp8_grouped_linear against plain forms in 64 bits.
+
+Bounds are fp8_gemm_b128's: binary32 results are off by at most (K / 128 + 8) 2^-23 of size =
+|A_hat| |B_hat|^T; bf16 ones by 2^-14 of size (the 8-bit matrix cores' sums hold about 16 bits)
+and half a step of bf16, 2^-8 of the value (its own bound of half a step, 2^-9, doubled where
+the value crosses a power of two)."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref
+import microscaling_fp4_quantization_amd as fq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+ROW, TILE = fq.B128_ROW, fq.B128_TILE
+TYPES = [torch.bfloat16, torch.float32]
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+# ---------------------------------------------------------------------------
+# expert_order
+
+
+def check_order(ids, experts):
+    o = fq.expert_order(ids, experts)
+    flat = ids.cpu().numpy().astype(np.int64).ravel()
+    key = np.where((flat >= 0) & (flat < experts), flat, experts)
+    order = np.argsort(key, kind="stable")
+    assert o.offsets.dtype == o.order.dtype == o.tokens.dtype == o.position.dtype == torch.int32
+    assert np.array_equal(o.offsets.cpu().numpy(), np.searchsorted(key[order], np.arange(experts + 1)))
+    assert np.array_equal(o.order.cpu().numpy(), order)
+    assert np.array_equal(o.tokens.cpu().numpy(), order // ids.shape[1])
+    back = np.empty_like(order)
+    back[order] = np.arange(order.size)
+    assert np.array_equal(o.position.cpu().numpy(), back.reshape(ids.shape))
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("tokens,top_k,experts", [(1, 1, 1), (1, 8, 64), (5, 8, 64), (63, 1, 2), (64, 3, 512), (100, 7, 511), (1024, 4, 63),
+                                                  (1025, 4, 65), (4097, 1, 128), (4096, 8, 8), (16384, 8, 128), (70000, 5, 3),
+                                                  (140000, 2, 512), (0, 2, 5)])
+def test_order(tokens, top_k, experts, dtype):
+    ids = torch.randint(-1, experts + 1, (tokens, top_k), generator=gen(tokens + experts), device=DEV, dtype=dtype)
+    check_order(ids, experts)
+
+
+@pytest.mark.parametrize("tokens", [9, 5000, 30000])
+def test_order_of_one_expert_and_of_none(tokens):
+    check_order(torch.full((tokens, 2), 3, dtype=torch.int32, device=DEV), 7)
+    check_order(torch.full((tokens, 2), -5, dtype=torch.int32, device=DEV), 7)
+    check_order(torch.full((tokens, 2), 2 ** 40 + 1, dtype=torch.int64, device=DEV), 7)  # its low half names expert 1
+    check_order((torch.arange(2 * tokens, device=DEV) % 7).view(tokens, 2), 7)
+    check_order((torch.arange(2 * tokens, device=DEV) * 7 // (2 * tokens)).flip(0).view(tokens, 2), 7)
+
+
+# ---------------------------------------------------------------------------
+# fp8_grouped_gemm_b128
+
+
+def value(codes, scales, kind):
+    """Dequantized operand in 64 bits."""
+    s = scales.double() if kind == TILE else scales.double().t()
+    rows = torch.arange(codes.shape[0], device=DEV) // (128 if kind == TILE else 1)
+    return codes.double() * s[rows][:, torch.arange(codes.shape[1], device=DEV) // 128]
+
+
+def experts_of(w):
+    """Codes and scales of each expert's matrix by itself."""
+    q = [fq.fp8_quantize_b128(m.contiguous(), TILE) for m in w]
+    return torch.stack([x.codes for x in q]), torch.stack([x.scales for x in q])
+
+
+def bar(want, size, k, dtype):
+    if dtype == torch.float32:
+        return (-(-k // 128) + 8) * 2.0 ** -23 * size
+    return 2.0 ** -14 * size + 2.0 ** -8 * want.abs()
+
+
+def expect(a, w, ends, tokens, rows):
+    """(C, size) in 64 bits; rows of no group are NaN."""
+    n = w[0].shape[0]
+    c = torch.full((rows, n), float("nan"), dtype=torch.float64, device=DEV)
+    size = c.clone()
+    for e, (lo, hi) in enumerate(zip(ends, ends[1:])):
+        if lo < hi:
+            x = a[lo:hi] if tokens is None else a[tokens[lo:hi].long()]
+            c[lo:hi] = x @ w[e].t().contiguous()
+            size[lo:hi] = x.abs() @ w[e].abs().t().contiguous()
+    return c, size
+
+
+def sizes_to_ends(sizes):
+    return [0] + list(np.cumsum(sizes))
+
+
+# Sizes of the groups, N, K.  Few rows, 64, 128 and 256 tiles; empty groups; groups that end inside
+# a tile, on its edge and one past it.
+CASES = [([1], 16, 16), ([0, 1, 0, 0, 2], 100, 128), ([3, 0, 16, 1], 48, 400), ([17, 0, 0, 8], 40, 144), ([8] * 16, 256, 1024),
+         ([1] * 70, 130, 256), ([70, 0, 65, 64, 1], 200, 272), ([128, 129, 0, 127], 128, 512), ([300, 5, 0, 700], 1031, 904),
+         ([255, 256, 257, 0, 1], 640, 256), ([1500, 10, 900], 2048, 384), ([2000, 0, 3000, 1], 4096, 256), ([0] * 300 + [40] + [0] * 100 + [9, 500], 96, 128),
+         ([0, 0], 64, 64), ([5000], 1000, 1008)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("form", ["experts", "stacked", "gathered"])
+@pytest.mark.parametrize("sizes,n,k", CASES)
+def test_grouped_gemm(sizes, n, k, form, dtype):
+    g = gen(n + k + len(sizes))
+    e, ends = len(sizes), sizes_to_ends(sizes)
+    rows = ends[-1] + 3  # three rows of no group
+    w = torch.randn(e, n, k, generator=g, device=DEV) * torch.exp(torch.randn(e, 1, 1, generator=g, device=DEV))
+    if form == "stacked":
+        q = fq.fp8_quantize_b128(w.view(e * n, k), TILE)
+        codes, scales = q.codes, q.scales
+        wv = value(codes, scales, TILE).view(e, n, -1)
+    else:
+        codes, scales = experts_of(w)
+        wv = torch.stack([value(c, s, TILE) for c, s in zip(codes, scales)])
+    a_rows = rows // 2 + 1 if form == "gathered" else rows
+    qa = fq.fp8_quantize_b128(torch.randn(a_rows, k, generator=g, device=DEV) * 3)
+    tokens = torch.randint(0, a_rows, (rows,), generator=g, device=DEV, dtype=torch.int32) if form == "gathered" else None
+    out = torch.full((rows, n), 77.0, dtype=dtype, device=DEV)
+    got = fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32(ends), tokens=tokens, out=out)
+    assert got is out
+    want, size = expect(value(qa.codes, qa.scales, ROW), wv, ends, tokens, rows)
+    assert bool((out[ends[-1]:] == 77.0).all())  # left as they were
+    err, lim = (out.double() - want).abs()[:ends[-1]], bar(want, size, k, dtype)[:ends[-1]]
+    assert bool((err <= lim).all()), float((err / lim).max())
+    again = fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32(ends), tokens=tokens, out_dtype=dtype)
+    assert torch.equal(again[:ends[-1]], out[:ends[-1]])
+
+
+@pytest.mark.parametrize("tokens_given", [False, True])
+@pytest.mark.parametrize("rows,n,k", [(4, 33, 64), (200, 70, 128), (2000, 300, 256), (3000, 4099, 128)])
+def test_rows_of_a_start_anywhere(rows, n, k, tokens_given):
+    """C starts on any element; a row of A that does not exist gives zeros; first group not at row 0."""
+    g = gen(rows)
+    e, ends = 3, [rows // 4, rows // 2, rows // 2, rows - 1]
+    codes, scales = experts_of(torch.randn(e, n, k, generator=g, device=DEV))
+    qa = fq.fp8_quantize_b128(torch.randn(rows, k, generator=g, device=DEV))
+    tokens = None
+    if tokens_given:
+        tokens = torch.randperm(rows, generator=g, device=DEV).int()
+        tokens[rows // 4] = -1
+        tokens[rows - 2] = rows
+    for dtype in TYPES:
+        buf = torch.full((rows * n + 2,), 5.0, dtype=dtype, device=DEV)
+        out = buf[1:1 + rows * n].view(rows, n)
+        fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32(ends), tokens=tokens, out=out)
+        av = torch.cat([value(qa.codes, qa.scales, ROW), torch.zeros(1, qa.codes.shape[1], dtype=torch.float64, device=DEV)])
+        t = None if tokens is None else torch.where((tokens >= 0) & (tokens < rows), tokens, rows)
+        want, size = expect(av, [value(c, s, TILE) for c, s in zip(codes, scales)], ends, t, rows)
+        inside = slice(ends[0], ends[-1])
+        assert bool(((out.double() - want).abs() <= bar(want, size, k, dtype))[inside].all())
+        assert bool((out[:ends[0]] == 5.0).all()) and bool((out[ends[-1]:] == 5.0).all()) and buf[0] == 5.0 and buf[-1] == 5.0
+
+
+@pytest.mark.parametrize("n", [96, 1000])
+def test_offsets_that_are_wrong_stay_inside(n):
+    """Offsets outside the rows or out of order touch nothing outside C (and give some of the products)."""
+    rows, k = 300, 128
+    codes, scales = experts_of(torch.randn(4, n, k, generator=gen(1), device=DEV))
+    qa = fq.fp8_quantize_b128(torch.randn(rows, k, generator=gen(2), device=DEV))
+    for ends in ([-5, 100, 50, 200, 900], [0, 2 ** 31 - 1, 7, -2 ** 31, 300], [300, 200, 100, 0, 0]):
+        buf = torch.full((rows + 200, n), 5.0, device=DEV)
+        fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32(ends), out=buf[100:100 + rows])
+        x = torch.randn(rows, 64, device=DEV, requires_grad=True)
+        w = torch.randn(4, 40, 64, device=DEV, requires_grad=True)
+        fq.fp8_grouped_linear(x, w, i32(ends)).sum().backward()
+        torch.cuda.synchronize()
+        assert bool((buf[:100] == 5.0).all()) and bool((buf[100 + rows:] == 5.0).all())
+    assert fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32([0, 0, 0, 0, 0])).shape == (rows, n)
+
+
+@pytest.mark.parametrize("rows", [3, 90, 700, 3000])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scale_products_past_the_range(rows, dtype):
+    """Scales of 2^62 and more under codes whose products are exact and small enough."""
+    n, k, g = 600, 400, gen(rows)
+    ends = [0, rows // 3, rows]
+    pick = lambda *s: torch.randint(0, 6, s, generator=g, device=DEV)
+
+    def sparse(*s):
+        v = torch.rand(*s, generator=g, device=DEV)
+        return torch.where(v < 0.05, 2.0 ** -9, torch.where(v > 0.95, -(2.0 ** -9), 0.0))
+
+    a, b = sparse(rows, k), sparse(2, n, k)
+    sa, sb = torch.exp2(62.0 + pick(4, rows)), torch.exp2(62.0 + pick(2, 5, 4))
+    f8 = lambda x: x.to(torch.float8_e4m3fn)
+    for tokens in (None, torch.randperm(rows, generator=g, device=DEV).int()):
+        got = fq.fp8_grouped_gemm_b128(f8(a), sa, f8(b), sb, i32(ends), tokens=tokens, out_dtype=dtype).double()
+        want, size = expect(value(f8(a), sa, ROW), [value(f8(c), s, TILE) for c, s in zip(b, sb)], ends, tokens, rows)
+        assert bool((size < 2.0 ** 127).all())
+        assert bool(((got - want).abs() <= 12 * 2.0 ** -23 * size + (2.0 ** -8 * want.abs() if dtype == torch.bfloat16 else 0)).all())
+
+
+@pytest.mark.parametrize("rows", [5, 200, 3000])
+def test_nan_stays_in_its_rows_and_columns(rows):
+    n, k = 300, 256
+    codes, scales = experts_of(torch.randn(2, n, k, generator=gen(1), device=DEV))
+    qa = fq.fp8_quantize_b128(torch.randn(rows, k, generator=gen(2), device=DEV))
+    ends = [0, rows - 2, rows]
+    want = fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32(ends))
+    qa.codes.view(torch.uint8)[1, 200] = 0x7F
+    scales[1, 1, 0] = float("nan")
+    got = fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32(ends))
+    assert bool(got[1].isnan().all()) and bool(got[rows - 2:, 128:256].isnan().all())
+    keep = torch.ones(rows, n, dtype=torch.bool, device=DEV)
+    keep[1] = False
+    keep[rows - 2:, 128:256] = False
+    assert torch.equal(got[keep], want[keep])
+
+
+# ---------------------------------------------------------------------------
+# fp8_grouped_linear
+
+
+def quantized(x, kind=ROW):
+    """Values of x (2-D) as the quantizer gives them, in 64 bits, without padding."""
+    if x.numel() == 0:
+        return torch.zeros(x.shape, dtype=torch.float64, device=DEV)
+    q = fq.fp8_quantize_b128(x.contiguous(), kind)
+    return value(q.codes, q.scales, kind)[:, :x.shape[1]]
+
+
+def linear_expect(x, w, dy, ends):
+    z = lambda *s: torch.zeros(s, dtype=torch.float64, device=DEV)
+    out = {n: (z(*s), z(*s)) for n, s in (("y", dy.shape), ("dx", x.shape), ("dw", w.shape))}
+    for e, (lo, hi) in enumerate(zip(ends, ends[1:])):
+        if lo == hi:
+            continue
+        wq = quantized(w[e], TILE)
+        for name, at, a, b in (("y", slice(lo, hi), quantized(x[lo:hi]), wq), ("dx", slice(lo, hi), quantized(dy[lo:hi]), wq.t()),
+                               ("dw", e, quantized(dy[lo:hi].t()), quantized(x[lo:hi].t()))):
+            out[name][0][at] = a @ b.t().contiguous()
+            out[name][1][at] = a.abs() @ b.abs().t().contiguous()
+    return out
+
+
+LINEAR = [([5], 3, 7), ([1, 0, 2], 16, 40), ([100, 0, 28, 129], 200, 136), ([7] * 20, 90, 300), ([128, 256, 1], 128, 256), ([300, 0, 209], 1000, 488),
+          ([0, 900, 700], 515, 640), ([2000, 1000, 3000], 1024, 512), ([0] * 130 + [50, 3], 65, 129)]
+
+
+@pytest.mark.parametrize("xt", TYPES)
+@pytest.mark.parametrize("wt", TYPES)
+@pytest.mark.parametrize("sizes,n,k", LINEAR)
+def test_linear(sizes, n, k, xt, wt):
+    g = gen(n + k)
+    ends = sizes_to_ends(sizes)
+    rows = ends[-1] + 2
+    x = torch.randn(rows, k, generator=g, device=DEV).to(xt).requires_grad_()
+    w = (torch.randn(len(sizes), n, k, generator=g, device=DEV) * 0.1).to(wt).requires_grad_()
+    dy = (torch.randn(rows, n, generator=g, device=DEV) * 1e-2).to(xt)
+    y = fq.fp8_grouped_linear(x, w, i32(ends))
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    assert y.dtype == dx.dtype == xt and dw.dtype == wt
+    want = linear_expect(x.detach(), w.detach(), dy, ends)
+    for name, got, terms in (("y", y.detach(), k), ("dx", dx, n), ("dw", dw, max(sizes))):
+        v, size = want[name]
+        err, lim = (got.double() - v).abs(), bar(v, size, terms, got.dtype)
+        assert bool((err <= lim).all()), name
+    assert bool((y[ends[-1]:] == 0).all()) and bool((dx[ends[-1]:] == 0).all())
+    for e, m in enumerate(sizes):
+        assert m or bool((dw[e] == 0).all())
+    # One gradient at a time gives the same bits.
+    assert torch.equal(torch.autograd.grad(fq.fp8_grouped_linear(x, w.detach(), i32(ends)), x, dy)[0], dx)
+    assert torch.equal(torch.autograd.grad(fq.fp8_grouped_linear(x.detach(), w, i32(ends)), w, dy)[0], dw)
+    with torch.no_grad():
+        assert torch.equal(fq.fp8_grouped_linear(x, w, i32(ends)), y)
+
+
+def test_linear_against_numpy():
+    """The whole of it from the formulas, codes included (tests/fp8_ref.py)."""
+    rng = np.random.default_rng(7)
+    ends, n, k = [0, 140, 140, 203], 70, 150
+    x, dy = rng.standard_normal((203, k)).astype(np.float32), rng.standard_normal((203, n)).astype(np.float32)
+    w = rng.standard_normal((3, n, k)).astype(np.float32)
+    t = lambda v: torch.from_numpy(np.ascontiguousarray(v)).to(DEV)
+    xt, wt = t(x).requires_grad_(), t(w).requires_grad_()
+    y = fq.fp8_grouped_linear(xt, wt, i32(ends))
+    dx, dw = torch.autograd.grad(y, (xt, wt), t(dy))
+
+    def q(v, tile=False):
+        v = np.ascontiguousarray(v)
+        return fp8_ref.value(*fp8_ref.quantize(v, tile), tile)[:, :v.shape[1]]
+
+    for e, (lo, hi) in enumerate(zip(ends, ends[1:])):
+        if lo == hi:
+            assert bool((dw[e] == 0).all())
+            continue
+        for got, a, b in ((y[lo:hi], q(x[lo:hi]), q(w[e], True)), (dx[lo:hi], q(dy[lo:hi]), q(w[e], True).T),
+                          (dw[e], q(dy[lo:hi].T), q(x[lo:hi].T))):
+            err = np.abs(got.detach().cpu().numpy() - a @ b.T)
+            assert np.all(err <= 10 * 2.0 ** -23 * (np.abs(a) @ np.abs(b).T))
+
+
+def test_linear_gradients_against_differences():
+    """Of a sum of y with weights, along random directions.  The inputs are codes already (whole
+    numbers up to 15, and 448 once in each block, so that every scale is 1): the layer is the exact
+    product, and a difference quotient of it the gradient's share in that direction, up to
+    binary32's sums."""
+    g = gen(9)
+    rows, n, k, ends = 200, 40, 64, [0, 90, 90, 200]
+    whole = lambda *s: torch.randint(-15, 16, s, generator=g, device=DEV).float()
+    x, w, dy = whole(rows, k), whole(3, n, k), whole(rows, n)
+    for t in (x, dy):
+        t[:, 0] = t[0] = t[90] = 448.0  # along the rows, and along the columns of each group
+    w[:, 0, 0] = 448.0
+    a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+    y = fq.fp8_grouped_linear(a, b, i32(ends))
+    dx, dw = torch.autograd.grad(y, (a, b), dy)
+    layer = lambda u, v: torch.cat([u[lo:hi].double() @ v[e].double().t() for e, (lo, hi) in enumerate(zip(ends, ends[1:]))])
+    assert torch.equal(y.double(), layer(x, w))
+    for _ in range(3):
+        u, v = whole(rows, k), whole(3, n, k)
+        for moved, got, along in ((layer(x + u, w) - layer(x - u, w), dx, u), (layer(x, w + v) - layer(x, w - v), dw, v)):
+            want = (moved / 2 * dy.double()).sum()
+            assert abs(float((got.double() * along.double()).sum() - want)) <= 2.0 ** -22 * float((got.double().abs() * along.double().abs()).sum())
+
+
+@pytest.mark.parametrize("rows,n,k,e", [(0, 8, 16, 2), (5, 0, 16, 2), (5, 8, 0, 2)])
+def test_linear_of_empty_sizes(rows, n, k, e):
+    x, w = torch.randn(rows, k, device=DEV, requires_grad=True), torch.randn(e, n, k, device=DEV, requires_grad=True)
+    y = fq.fp8_grouped_linear(x, w, i32([0, rows // 2, rows]))
+    assert y.shape == (rows, n) and bool((y == 0).all())
+    dx, dw = torch.autograd.grad(y, (x, w), torch.ones_like(y))
+    assert dx.shape == x.shape and dw.shape == w.shape and bool((dx == 0).all()) and bool((dw == 0).all())
+
+
+def test_linear_of_strided_inputs():
+    g = gen(4)
+    x = torch.randn(60, 100, generator=g, device=DEV).t().requires_grad_()
+    w = torch.randn(2, 60, 50, generator=g, device=DEV).transpose(1, 2).requires_grad_()
+    dy = torch.randn(50, 100, generator=g, device=DEV).t()
+    ends = i32([0, 33, 100])
+    got = torch.autograd.grad(fq.fp8_grouped_linear(x, w, ends), (x, w), dy)
+    x2, w2 = x.detach().contiguous().requires_grad_(), w.detach().contiguous().requires_grad_()
+    want = torch.autograd.grad(fq.fp8_grouped_linear(x2, w2, ends), (x2, w2), dy.contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y = fq.fp8_grouped_linear(x2, w2, ends)
+    grads = torch.autograd.grad(y.sum(), (x2, w2))  # an expanded gradient
+    assert torch.equal(grads[0], torch.autograd.grad(fq.fp8_grouped_linear(x2, w2, ends), x2, torch.ones_like(y))[0])
+
+
+def test_no_gradient_of_the_product():
+    codes, scales = experts_of(torch.randn(2, 20, 32, device=DEV))
+    q = fq.fp8_quantize_b128(torch.randn(4, 32, device=DEV))
+    y = fq.fp8_grouped_gemm_b128(q.codes, q.scales.requires_grad_(), codes, scales, i32([0, 1, 4]))
+    with pytest.raises(NotImplementedError, match="fp8_grouped_gemm_b128 has no gradient"):
+        y.sum().backward()
+
+
+# ---------------------------------------------------------------------------
+# Together
+
+
+def layer(h, w13, w2, o, weights):
+    """A mixture-of-experts layer over a prompt, of its parts."""
+    q = fq.fp8_quantize_b128(h)
+    gate, up = fq.fp8_grouped_gemm_b128(q.codes, q.scales, *w13, o.offsets, tokens=o.tokens).chunk(2, 1)
+    q2 = fq.fp8_quantize_b128((torch.nn.functional.silu(gate) * up).contiguous())
+    down = fq.fp8_grouped_gemm_b128(q2.codes, q2.scales, *w2, o.offsets)
+    return (down[o.position.long()] * weights[..., None]).sum(1)
+
+
+@pytest.mark.parametrize("tokens", [1, 64, 700])
+def test_a_prompt_through_the_experts(tokens):
+    """Against 64 bits with the same codes; and, up to 64 tokens, near moe_layer, whose activations are not quantized."""
+    g = gen(tokens)
+    dim, inter, experts, top_k = 256, 128, 8, 2
+    w13 = torch.randn(experts * 2 * inter, dim, generator=g, device=DEV) * dim ** -0.5
+    w2 = torch.randn(experts * dim, inter, generator=g, device=DEV) * inter ** -0.5
+    q13, q2 = fq.fp8_quantize_b128(w13, TILE), fq.fp8_quantize_b128(w2, TILE)
+    h = torch.randn(tokens, dim, generator=g, device=DEV)
+    p, ids = torch.softmax(torch.randn(tokens, experts, generator=g, device=DEV), 1).topk(top_k)
+    y = layer(h, (q13.codes, q13.scales), (q2.codes, q2.scales), fq.expert_order(ids, experts), p)
+    v13, v2 = value(q13.codes, q13.scales, TILE).view(experts, 2 * inter, dim), value(q2.codes, q2.scales, TILE).view(experts, dim, inter)
+    hq = quantized(h)
+    want = torch.zeros(tokens, dim, dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(want)
+    for t in range(tokens):
+        for j in range(top_k):
+            e = int(ids[t, j])
+            gu = v13[e] @ hq[t]
+            a = torch.nn.functional.silu(gu[:inter]) * gu[inter:]
+            want[t] += p[t, j].double() * (v2[e] @ quantized(a.float()[None])[0])
+            size[t] += p[t, j].double() * (v2[e].abs() @ torch.full_like(a, float(a.abs().max())))
+    # A difference of 2^-20 before the second quantizer can move a code by its whole step, 2^-4 of the element at most.
+    assert bool(((y.double() - want).abs() <= 2.0 ** -4 * size).all())
+    assert float((y.double() - want).norm() / want.norm()) < 2.0 ** -9
+    if tokens <= 64:
+        m = fq.moe_layer(h, fq.ExpertWeights(fq.FMT_E4M3_B128, q13.codes, q13.scales), fq.ExpertWeights(fq.FMT_E4M3_B128, q2.codes, q2.scales),
+                         experts, top_k, topk_ids=ids.int(), topk_weights=p)
+        assert float((y - m.y).norm() / m.y.norm()) < 0.06  # two quantizations of activations, 2^-4 / sqrt(3) of a step at most each
+
+
+def test_training_steps_of_two_layers():
+    """Routed rows through two grouped layers: the gradients that autograd gathers are the parts' own."""
+    g = gen(5)
+    tokens, dim, inter, experts, top_k = 90, 64, 48, 5, 2
+    h = torch.randn(tokens, dim, generator=g, device=DEV, requires_grad=True)
+    w1 = (torch.randn(experts, inter, dim, generator=g, device=DEV) * 0.1).requires_grad_()
+    w2 = (torch.randn(experts, dim, inter, generator=g, device=DEV) * 0.1).requires_grad_()
+    ids = torch.rand(tokens, experts, generator=g, device=DEV).topk(top_k).indices
+    o = fq.expert_order(ids, experts)
+    x = h[o.tokens.long()]
+    u = fq.fp8_grouped_linear(x, w1, o.offsets)
+    v = fq.fp8_grouped_linear(torch.relu(u), w2, o.offsets)
+    y = v[o.position.long()].sum(1)
+    dy = torch.randn(tokens, dim, generator=g, device=DEV)
+    y.backward(dy)
+    ends = o.offsets.tolist()
+    dv = torch.zeros_like(v).index_put((o.position.long().flatten(),), dy.repeat_interleave(top_k, 0))
+    r2 = linear_expect(torch.relu(u).detach(), w2.detach(), dv, ends)
+    du = torch.autograd.grad(fq.fp8_grouped_linear(torch.relu(u).detach().requires_grad_(), w2, o.offsets), w2, dv)[0]
+    assert torch.equal(w2.grad, du) and bool(((w2.grad.double() - r2["dw"][0]).abs() <= bar(*r2["dw"], 128, torch.float32)).all())
+    assert h.grad.shape == h.shape and w1.grad.shape == w1.shape and bool(h.grad.isfinite().all()) and bool((w1.grad != 0).any())
+
+
+def test_streams_threads_and_graphs():
+    import threading
+    g = gen(11)
+    e, n, k = 6, 200, 136
+    w = torch.randn(e, n, k, generator=g, device=DEV)
+    codes, scales = experts_of(w)
+
+    def case(tokens, seed):
+        gg = gen(seed)
+        ids = torch.rand(tokens, e, generator=gg, device=DEV).topk(2).indices
+        h, dy = torch.randn(tokens, k, generator=gg, device=DEV), torch.randn(2 * tokens, n, generator=gg, device=DEV)
+
+        def call():
+            o = fq.expert_order(ids, e)
+            q = fq.fp8_quantize_b128(h)
+            c = fq.fp8_grouped_gemm_b128(q.codes, q.scales, codes, scales, o.offsets, tokens=o.tokens)
+            x, ww = h[o.tokens.long()].requires_grad_(), w.clone().requires_grad_()
+            y = fq.fp8_grouped_linear(x, ww, o.offsets)
+            return torch.cat([t.flatten() for t in (c, y.detach(), *torch.autograd.grad(y, (x, ww), dy))])
+
+        return call
+
+    cases = [case(30, 1), case(3000, 2)]
+    want = [c() for c in cases]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert torch.equal(cases[1](), want[1])
+    got, bad = {}, []
+
+    def work(i):
+        try:
+            for _ in range(20):
+                if not torch.equal(cases[i](), want[i]):
+                    bad.append(i)
+        except Exception as ex:  # noqa: BLE001
+            bad.append(ex)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not bad
+    torch.cuda.synchronize()
+    outs, graphs = [], []
+    for c in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(c())
+        graphs.append(graph)
+    for _ in range(3):
+        for i in (1, 0):
+            outs[i].zero_()
+            graphs[i].replay()
+            cases[1 - i]()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], want[i])
