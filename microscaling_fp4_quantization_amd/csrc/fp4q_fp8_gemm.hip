@@ -112,7 +112,8 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(F8Params p) {
     const int s_lo = split * per, s_hi = s_lo + per < S ? s_lo + per : S;
     const F8Tile t = dense_tile<BROW>(p, m0, n0, (int)rows_a, (int)rows_b, s_lo, s_hi);
     v4f acc[TB][TA];
-    tile_sums<BROW, false>(acc, t, lds, wave, lane);
+    F8Loads<false> none;
+    tile_sums<BROW, false, false, false>(acc, t, lds, wave, lane, none);
     wait_all_barrier();  // LDS is reused below
 
     void* c = splits > 1 ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.c;
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_gemm_fp8_mid(F8Params
     const int per = (S + splits - 1) / splits;
     const int s_lo = split * per, s_hi = s_lo + per < S ? s_lo + per : S;
     v4f acc[P::kF][P::kF];
-    mid_sums<T, BROW, WIDE, false>(acc, dense_tile<BROW>(p, m0, n0, rows_a, rows_b, s_lo, s_hi), lds, wave, lane);
+    mid_sums<T, BROW, WIDE, false, false>(acc, dense_tile<BROW>(p, m0, n0, rows_a, rows_b, s_lo, s_hi), lds, wave, lane);
     wait_all_barrier();  // LDS is reused below
     void* c = splits > 1 ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.c;
     const int ct = splits > 1 ? 1 : p.ct;

@@ -274,25 +274,73 @@ __device__ __forceinline__ void sums_again(v4f (&acc)[NB][NA], const F8Tile& t, 
     }
 }
 
+// A wave's loads of a 256 x 256 tile, with the lane's offset of each formed once, so that the loop
+// over K moves a scalar one alone: A's rows may be anywhere (formed in the loop, their offsets took
+// more registers than there are).
+template <bool GATHER>
+struct F8Loads {
+    int at[kLoads];
+    int sc_off;
+    // Load L moves rows 8 d .. 8 d + 7, d = wave + 8 (L % 4), of A (L < 4) or B, as in tile_sums;
+    // scales alike.
+    static __device__ __forceinline__ int piece(int wave, int lane) { return (lane % 8) ^ (4 * (wave & 1) + lane / 16); }
+    template <bool BROW>
+    __device__ __forceinline__ void init(const F8Tile& t, int wave, int lane) {
+#pragma unroll
+        for (int L = 0; L < kLoads; ++L) {
+            const int r = 8 * (wave + kWaves * (L % (kLoads / 2))) + lane / 8;
+            const int row = L < kLoads / 2 ? t.a_row<GATHER>(r) : r;
+            at[L] = row >= 0 ? row * t.K + piece(wave, lane) * 16 : kDropped;
+        }
+        const int r = (wave % 4) * kWave + lane, row = wave < 4 ? t.a_row<GATHER>(r) : t.sb_at<BROW>(r);
+        sc_off = row >= 0 ? row * 4 : kDropped;
+    }
+    // The last block of K: pieces past it are not read.
+    __device__ __forceinline__ void cut(const F8Tile& t, int s, int wave, int lane) {
+        if (__builtin_expect((s + 1) * kBlock <= t.K || s >= t.s_hi || s * kBlock + piece(wave, lane) * 16 < t.K, 1)) return;
+#pragma unroll
+        for (int L = 0; L < kLoads; ++L) at[L] = kDropped;
+    }
+    // (Past s_hi: nothing, or some bytes of A that no product takes.)
+    __device__ __forceinline__ void issue(const F8Tile& t, uint8_t* lds, int wave, int s, int L) const {
+        uint8_t* stage = lds + (s & 1) * kStageBytes;
+        if (L < kLoads) {
+            const int d = wave + kWaves * (L % (kLoads / 2));
+            uint8_t* dst = stage + (L < kLoads / 2 ? 0 : BM * kRowStage) + d * 8 * kRowStage;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? t.ra : t.rb, (LdsPtr)dst, 16, at[L], s < t.s_hi ? s * kBlock : kPastWindow, 0, 0);
+        } else {
+            const bool sc_a = wave < 4;
+            const int here = s < t.s_hi ? s : t.s_lo;
+            const Rsrc rs = make_rsrc((sc_a ? t.sa : t.sb) + here * (sc_a ? t.sa_step : t.sb_step),
+                                      (sc_a ? t.sa_size : t.sb_size) - here * (sc_a ? 0 : t.sb_shrink));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(stage + kCodeBytes + wave * kWave * 4), 4, sc_off, 0, 0, 0);
+        }
+    }
+    template <bool BROW>
+    __device__ __forceinline__ void first_stage(const F8Tile& t, uint8_t* lds, int wave, int lane) {
+        if (t.s_lo >= t.s_hi) return;  // K = 0 has no operands to read
+        init<BROW>(t, wave, lane);
+        cut(t, t.s_lo, wave, lane);
+#pragma unroll
+        for (int L = 0; L <= kLoads; ++L) issue(t, lds, wave, t.s_lo, L);
+    }
+};
+
 // The sums of a 256 x 256 tile by 8 waves (2 x 4 of 128 x 64), through two LDS stages of
-// kStageBytes.  BROW: B's scales differ within 64 rows; else one goes for all of a wave's.
-template <bool BROW, bool GATHER>
-__device__ __forceinline__ void tile_sums(v4f (&acc)[TB][TA], const F8Tile& t, uint8_t* lds, int wave, int lane) {
+// kStageBytes.  BROW: B's scales differ within 64 rows; else one goes for all of a wave's.  SKIP:
+// many tiles hold fewer rows of A than they have room for, and a wave that has none multiplies none
+// (the waves of the other half share its SIMDs).  AHEAD: `loads` brings the stages, the first one
+// already.
+template <bool BROW, bool GATHER, bool SKIP, bool AHEAD>
+__device__ __forceinline__ void tile_sums(v4f (&acc)[TB][TA], const F8Tile& t, uint8_t* lds, int wave, int lane, F8Loads<GATHER>& loads) {
     const int wm = wave >> 2, wn = wave & 3;
+    const bool idle = wm * WM >= t.rows_a;
     // Code load q of a wave moves rows 8 d .. 8 d + 7, d = wave + 8 (q % 4), of A
     // (q < 4) or B: lane l fetches row 8 d + l / 8 into slot l % 8 of that row (row /
     // 2 = 4 d + l / 16 and d = wave mod 2, so that the piece is the same for every q).
     const int K = t.K, s_lo = t.s_lo, s_hi = t.s_hi;
     const int piece = (lane % 8) ^ (4 * (wave & 1) + lane / 16);
     const int lane_off = (lane / 8) * K + piece * 16;
-    int a_off[GATHER ? kLoads / 2 : 1];
-    if (GATHER) {
-#pragma unroll
-        for (int q = 0; q < kLoads / 2; ++q) {
-            const int row = t.a_row<GATHER>(8 * (wave + kWaves * q) + lane / 8);
-            a_off[GATHER ? q : 0] = row >= 0 ? row * K + piece * 16 : -1;
-        }
-    }
     // Scales of a stage: waves 0-3 bring 64 rows of A each, waves 4-7 of B; B's tile
     // scales are spread to one per row.  Chosen once per wave, so that the K loop
     // has no branch: a stage's window starts sc_step floats after the one before.
@@ -302,20 +350,18 @@ __device__ __forceinline__ void tile_sums(v4f (&acc)[TB][TA], const F8Tile& t, u
     const int64_t sc_step = sc_a ? t.sa_step : t.sb_step;
     const int sc_size = sc_a ? t.sa_size : t.sb_size;
     const int sc_shrink = sc_a ? 0 : t.sb_shrink;  // tile scales' window ends where it did
-    const int sc_at = sc_a ? t.a_row<GATHER>(sc_row) : t.sb_at<BROW>(sc_row);
-    const int sc_off = GATHER && sc_at < 0 ? kDropped : sc_at * 4;
+    const int sc_off = (sc_a ? sc_row : t.sb_at<BROW>(sc_row)) * 4;
     // Load L of stage s: the code loads, then the scales.  A stage past the range
     // reads zero codes (and some other stage's scales).
     auto issue = [&](int s, int L) {
+        if (AHEAD) return loads.issue(t, lds, wave, s, L);
         uint8_t* stage = lds + (s & 1) * kStageBytes;
         if (L < kLoads) {
             const int k0 = s * kBlock;
             const int base = k0 + piece * 16 < (s < s_hi ? K : 0) ? lane_off + k0 : kPastWindow;
             const int d = wave + kWaves * (L % (kLoads / 2));
             uint8_t* dst = stage + (L < kLoads / 2 ? 0 : BM * kRowStage) + d * 8 * kRowStage;
-            int off = base + 8 * d * K;
-            if (GATHER && L < kLoads / 2) off = base == kPastWindow || a_off[GATHER ? L : 0] < 0 ? kDropped : a_off[GATHER ? L : 0] + k0;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? t.ra : t.rb, (LdsPtr)dst, 16, off, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? t.ra : t.rb, (LdsPtr)dst, 16, base + 8 * d * K, 0, 0, 0);
         } else {
             const int at = s < s_hi ? s : s_lo;
             const Rsrc rs = make_rsrc(sc_base + at * sc_step, sc_size - at * sc_shrink);
@@ -348,7 +394,7 @@ __device__ __forceinline__ void tile_sums(v4f (&acc)[TB][TA], const F8Tile& t, u
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], BROW ? sb[e] * f : f, acc[i][j][e]);
     };
-    if (s_lo < s_hi) {  // K = 0 has no operands to read
+    if (!AHEAD && s_lo < s_hi) {  // K = 0 has no operands to read
 #pragma unroll
         for (int L = 0; L <= kLoads; ++L) issue(s_lo, L);
     }
@@ -360,6 +406,12 @@ __device__ __forceinline__ void tile_sums(v4f (&acc)[TB][TA], const F8Tile& t, u
         // wait, so that it adds none before the first operands arrive.)
         __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
         asm volatile("s_barrier" ::: "memory");
+        if (AHEAD) loads.cut(t, s + 1, wave, lane);
+        if (SKIP && idle) {
+#pragma unroll
+            for (int L = 0; L <= kLoads; ++L) issue(s + 1, L);
+            continue;
+        }
         v8i a_next = read_op(here + a_lo, here + a_hi, 0);
         v8i b[TB];
         v4f sb[BROW ? TB : 1];
@@ -414,12 +466,13 @@ __device__ __forceinline__ void tile_sums(v4f (&acc)[TB][TA], const F8Tile& t, u
 }
 
 // The sums of a T x T tile by 4 waves, through two LDS stages.
-template <int T, bool BROW, bool WIDE, bool GATHER>
+template <int T, bool BROW, bool WIDE, bool GATHER, bool SKIP>
 __device__ __forceinline__ void mid_sums(v4f (&acc)[MidPlan<T>::kF][MidPlan<T>::kF], const F8Tile& t, uint8_t* lds, int wave, int lane) {
     typedef MidPlan<T> P;
     typedef Operand<WIDE> Op;
     constexpr int F = P::kF;
     const int wm = wave / 2, wn = wave % 2;
+    const bool idle = wm * (T / 2) >= t.rows_a;
     // Code load q of a wave moves rows 8 d .. 8 d + 7 of the 2 T (A's, then B's), d =
     // 4 q + wave; slots as in the tile kernel (T is a multiple of 16).
     const int K = t.K, s_lo = t.s_lo, s_hi = t.s_hi;
@@ -474,6 +527,7 @@ __device__ __forceinline__ void mid_sums(v4f (&acc)[MidPlan<T>::kF][MidPlan<T>::
         __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
         asm volatile("s_barrier" ::: "memory");
         issue(s + 1);
+        if (SKIP && idle) continue;
         const float* fa = reinterpret_cast<const float*>(here + P::kCode) + a_row;
         const float* fb = reinterpret_cast<const float*>(here + P::kCode) + T + wn * (T / 2);
         typename Op::T b[F];

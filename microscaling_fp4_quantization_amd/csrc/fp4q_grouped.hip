@@ -42,25 +42,24 @@ struct GroupedParams {
     unsigned first;      // this launch's first workgroup
 };
 
-// Which of `tiles` row tiles by tiles_n a workgroup takes (tile_of's order, for fewer than 2^31);
-// false where there are fewer.
-__device__ __forceinline__ bool tile_at(unsigned g, unsigned tiles_m, unsigned tiles_n, int& tm, int& tn) {
-    const unsigned T = tiles_m * tiles_n, xcd = g % 8, idx = g / 8, per = T / 8, rem = T % 8;
-    if (idx >= per + (xcd < rem ? 1 : 0)) return false;
-    const unsigned t = xcd * per + min(xcd, rem) + idx;
+// Which of tiles_m by tiles_n tiles is the `idx`-th of an XCD's share (tile_of's order, for fewer
+// than 2^31), where the share has so many.
+__device__ __forceinline__ unsigned share_of(unsigned tiles, unsigned xcd) { return tiles / 8 + (xcd < tiles % 8 ? 1 : 0); }
+__device__ __forceinline__ void tile_at(unsigned xcd, unsigned idx, unsigned tiles_m, unsigned tiles_n, int& tm, int& tn) {
+    const unsigned T = tiles_m * tiles_n, t = xcd * (T / 8) + min(xcd, T % 8) + idx;
     const unsigned span = kGroupM * tiles_n, band = t / span, in = t - band * span, first = band * kGroupM;
     const unsigned gm = min(tiles_m - first, (unsigned)kGroupM), n = in / gm;
     tm = __builtin_amdgcn_readfirstlane(first + in - n * gm);
     tn = __builtin_amdgcn_readfirstlane(n);
-    return true;
 }
 
 // The tile of a workgroup: `side` rows of one group and as many of its expert's.  False: none.
 template <bool GATHER>
 __device__ __forceinline__ bool grouped_tile(const GroupedParams& p, int side, F8Tile& t, int& row0, int& n0) {
-    const int tiles_n = (p.N + side - 1) / side;
+    const unsigned tiles_m = group_tiles(p.groups, side), tiles_n = (p.N + side - 1) / side, group = p.first + blockIdx.x;
+    if (group / 8 >= share_of(tiles_m * tiles_n, group % 8)) return false;
     int tm, tn;
-    if (!tile_at(p.first + blockIdx.x, group_tiles(p.groups, side), tiles_n, tm, tn)) return false;
+    tile_at(group % 8, group / 8, tiles_m, tiles_n, tm, tn);
     const GroupTile g = group_tile(p.groups, side, tm);
     const bool rest = g.group >= p.groups.count;  // rows of no group: no products
     const int e = rest ? 0 : g.group;
@@ -97,8 +96,10 @@ __global__ __launch_bounds__(kThreads) void k_grouped(GroupedParams p) {
     F8Tile t;
     int row0, n0;
     if (!grouped_tile<GATHER>(p, BM, t, row0, n0)) return;
+    F8Loads<GATHER> loads;
+    loads.template first_stage<BROW>(t, lds, wave, lane);
     v4f acc[TB][TA];
-    tile_sums<BROW, GATHER>(acc, t, lds, wave, lane);
+    tile_sums<BROW, GATHER, true, true>(acc, t, lds, wave, lane, loads);
     wait_all_barrier();  // LDS is reused below
     const int eb = p.ct == 1 ? 4 : 2;
     char* c = p.c + (int64_t)row0 * p.N * eb;
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_grouped_mid(GroupedPa
     int row0, n0;
     if (!grouped_tile<GATHER>(p, T, t, row0, n0)) return;
     v4f acc[MidPlan<T>::kF][MidPlan<T>::kF];
-    mid_sums<T, BROW, WIDE, GATHER>(acc, t, lds, wave, lane);
+    mid_sums<T, BROW, WIDE, GATHER, true>(acc, t, lds, wave, lane);
     wait_all_barrier();  // LDS is reused below
     store_mid<T>(acc, lds, p.c + (int64_t)row0 * p.N * (p.ct == 1 ? 4 : 2), p.ct, t.rows_a, t.rows_b, n0, p.N, p.whole, wave, lane);
 }
@@ -220,15 +221,32 @@ struct OuterParams {
     unsigned first;
 };
 
-__device__ __forceinline__ bool outer_tile(const OuterParams& p, int side, F8Tile& t, int& m0, int& n0, int& e) {
-    const unsigned per_m = (p.M + side - 1) / side;
+// Each XCD takes a share of every expert's tiles (a run of tile_at's order within one), so that it
+// has its share of the large groups; up to 64 experts in order of their size, the largest first,
+// so that none of those starts when the others are done.  (16 experts of 4096 x 2048 and 16384 rows
+// in all, bf16: 390 us with the experts one after the other in tile_at's runs.)
+__device__ __forceinline__ bool outer_tile(const OuterParams& p, int side, unsigned group, F8Tile& t, int& m0, int& n0, int& e) {
+    const unsigned tiles_m = (p.M + side - 1) / side, tiles_n = (p.N + side - 1) / side;
+    const unsigned share = (tiles_m * tiles_n + 7) / 8;
+    if (group / 8 / share >= (unsigned)p.groups.count) return false;
     int tm, tn;
-    if (!tile_at(p.first + blockIdx.x, p.groups.count * per_m, (p.N + side - 1) / side, tm, tn)) return false;
-    e = tm / (int)per_m;
-    m0 = (tm - e * (int)per_m) * side;
+    if (group / 8 % share >= share_of(tiles_m * tiles_n, group % 8)) return false;
+    tile_at(group % 8, group / 8 % share, tiles_m, tiles_n, tm, tn);
+    const int lane = threadIdx.x % kWave;
+    e = (int)(group / 8 / share);
+    if (p.groups.count <= kWave) {
+        int lo, hi, rank = 0;
+        p.groups.range(lane, lo, hi);
+        const int mine = hi - lo;
+        for (int o = 0; o < p.groups.count; ++o) {
+            const int other = __builtin_amdgcn_readlane(mine, o);
+            rank += other > mine || (other == mine && o < lane) ? 1 : 0;
+        }
+        e = __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < p.groups.count && rank == e));
+    }
+    m0 = tm * side;
     n0 = tn * side;
     // Blocks of the groups before e, and its own.
-    const int lane = threadIdx.x % kWave;
     int before = 0, mine = 0;
     for (int c = 0; c <= e; c += kWave) {
         int lo, hi;
@@ -256,9 +274,11 @@ __global__ __launch_bounds__(kThreads) void k_grouped_outer(OuterParams p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     F8Tile t;
     int m0, n0, e;
-    if (!outer_tile(p, BM, t, m0, n0, e)) return;
+    if (!outer_tile(p, BM, p.first + blockIdx.x, t, m0, n0, e)) return;
+    F8Loads<false> loads;
+    loads.template first_stage<true>(t, lds, wave, lane);
     v4f acc[TB][TA];
-    tile_sums<true, false>(acc, t, lds, wave, lane);
+    tile_sums<true, false, false, true>(acc, t, lds, wave, lane, loads);
     wait_all_barrier();  // LDS is reused below
     char* c = p.c + ((int64_t)e * p.M + m0) * p.N * 2;  // (a binary32 C takes the smaller tiles)
     const Rsrc rc = make_rsrc(c, (int64_t)t.rows_a * p.N * 2);
@@ -274,9 +294,9 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_grouped_outer_mid(Out
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     F8Tile t;
     int m0, n0, e;
-    if (!outer_tile(p, T, t, m0, n0, e)) return;
+    if (!outer_tile(p, T, p.first + blockIdx.x, t, m0, n0, e)) return;
     v4f acc[MidPlan<T>::kF][MidPlan<T>::kF];
-    mid_sums<T, true, WIDE, false>(acc, t, lds, wave, lane);
+    mid_sums<T, true, WIDE, false, false>(acc, t, lds, wave, lane);
     wait_all_barrier();  // LDS is reused below
     store_mid<T>(acc, lds, p.c + ((int64_t)e * p.M + m0) * p.N * (p.ct == 1 ? 4 : 2), p.ct, t.rows_a, t.rows_b, n0, p.N, p.whole, wave, lane);
 }
@@ -383,7 +403,7 @@ int launch_grouped_outer(const GroupedOuterJob& j, char* msg, size_t msg_len) {
                   (int)(blocks * kBlock), static_cast<char*>(j.c), j.ct, j.N * eb % 16 == 0 && (uintptr_t)j.c % 16 == 0, 0};
     auto tiles = [&](int t) { return j.experts * ((j.M + t - 1) / t) * ((j.N + t - 1) / t); };
     const int tile = choose(j.ct == 1, (double)j.rows / 128 / (double)j.experts + 0.5, [&](int t) { return (double)tiles(t); });
-    const int64_t groups = tiles(tile);
+    const int64_t groups = (tiles(tile) / j.experts + 7) / 8 * 8 * j.experts;
     if (groups > INT32_MAX) return too_many(what, msg, msg_len);
     for (int64_t first = 0; first < groups; first += kMaxGrid) {
         const dim3 grid((unsigned)std::min(groups - first, kMaxGrid));
@@ -475,16 +495,32 @@ __global__ __launch_bounds__(kOrderThreads) void k_order_place(OrderParams p) {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, buckets = p.experts + 1;
     const int64_t lo = blockIdx.x * p.run, hi = min(lo + p.run, p.slots);
     count_run(p, lo, hi, counts, total);
-    for (int b = threadIdx.x; b < buckets; b += kOrderThreads) {
-        before[b] = 0;
-        if (p.runs == 1) continue;
-        int sum = 0, all = 0;
-        for (int r = 0; r < p.runs; ++r) {
-            if (r == (int)blockIdx.x) sum = all;
-            all += p.counts[(int64_t)r * buckets + b];
+    // The other runs' slots: kParts threads a bucket, each some of the runs, reads side by side.
+    for (int b = threadIdx.x; b < buckets; b += kOrderThreads) before[b] = 0;
+    if (p.runs > 1) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < buckets; b += kOrderThreads) total[b] = 0;
+        __syncthreads();
+        const int parts = kOrderThreads / buckets > 0 ? kOrderThreads / buckets : 1;
+        const int part = threadIdx.x / buckets, each = (p.runs + parts - 1) / parts;
+        const int r_end = min(p.runs, (part + 1) * each);
+        if (part < parts) {
+            const int b = threadIdx.x - part * buckets;
+            int sum = 0, all = 0;
+            for (int r0 = part * each; r0 < r_end; r0 += 16) {
+                int n[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) n[r] = p.counts[(int64_t)min(r0 + r, p.runs - 1) * buckets + b];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int one = r0 + r < r_end ? n[r] : 0;
+                    all += one;
+                    sum += r0 + r < (int)blockIdx.x ? one : 0;
+                }
+            }
+            atomicAdd(&before[b], sum);
+            atomicAdd(&total[b], all);
         }
-        before[b] = sum;
-        total[b] = all;
     }
     __syncthreads();
     if (wave == 0) {
