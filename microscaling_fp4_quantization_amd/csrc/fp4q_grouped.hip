@@ -126,12 +126,14 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_grouped_mid(GroupedPa
 
 // Few rows per group: a pass over the matrices of the experts that have any.  A workgroup takes 16
 // rows of one expert's matrix against its group, 16 rows of that at a time, its waves K blocks in
-// turn, the next block on its way; bound by the read of B, so always on the bf16 form.
+// turn, the next block on its way; bound by the read of B, so always on the bf16 form.  Half a
+// wave's registers go to blocks on their way, so that eight waves share a SIMD.
 constexpr int kFewRows = 16;
-constexpr int kFewMaxWaves = 16;
+constexpr int kFewMaxWaves = 8;
 
-template <bool GATHER>
+template <bool BROW, bool GATHER>
 __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_grouped_few(GroupedParams p) {
+    constexpr int SB = BROW ? 4 : 1;  // scales of a lane's four rows of B
     __shared__ __attribute__((aligned(16))) float red[kFewMaxWaves * 256];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -146,48 +148,69 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_grouped_few(GroupedPar
     const int r = lane % 16, q = lane / 16;
     const Rsrc rb = make_rsrc(p.b + ((int64_t)e * p.N + n0) * K, (int64_t)rows_b * K);
     const int64_t at = (int64_t)e * p.sb_rows + n0;
-    // A lane's four rows of B (the last for those that there are not), as places of tile scales.
-    const float* sb[4];
+    const float* sb = p.sb + at / kBlock * p.S;  // of the first row's block
+    int sb_at[SB];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sb[k] = p.sb + (at + min(4 * q + k, rows_b - 1)) / kBlock * p.S;
+    for (int k = 0; k < SB; ++k) sb_at[k] = BROW ? (int)((at % kBlock + min(4 * q + k, rows_b - 1)) / kBlock) * p.S : 0;
 
+    struct Block { u32x4_t a[2], b[2]; float sa, sb[SB]; };
+    auto place = [&](int s, int h) {
+        const int pos = s * kBlock + h * 64 + q * 16;
+        return s < S && pos < K ? pos : -1;
+    };
+    auto load_b = [&](Block& t, int s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pos = place(s, h);
+            t.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, pos >= 0 ? r * K + pos : kDropped, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < SB; ++k) t.sb[k] = sb[sb_at[k] + (s < S ? s : 0)];
+    };
+    Block now, next;
+    if (S > 0) load_b(now, wave);  // on its way while the rows of A are found
     for (int row0 = g.row; row0 < g.end; row0 += 16) {
         const int m = row0 + r;
-        const int token = m >= g.end ? -1 : GATHER ? p.tokens[m] : m;
+        const int token = m >= g.end ? -1 : GATHER ? p.tokens[m] : m - row0;
         const bool there = token >= 0 && token < p.a_rows;
-        const uint8_t* row = p.a + (int64_t)(there ? token : 0) * K;
-        struct Block { u32x4_t a[2], b[2]; float sa, sb[4]; };
-        auto load = [&](Block& t, int s) {
+        const Rsrc ra = GATHER ? make_rsrc(p.a, (int64_t)p.a_rows * K) : make_rsrc(p.a + (int64_t)row0 * K, (int64_t)min(16, g.end - row0) * K);
+        const float* sa = GATHER ? p.sa : p.sa + row0;
+        const int sa_size = (GATHER ? p.a_rows : min(16, g.end - row0)) * 4;
+        auto load_a = [&](Block& t, int s) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int pos = s * kBlock + h * 64 + q * 16;
-                t.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, s < S && pos < K ? r * K + pos : kDropped, 0, 0);
-                t.a[h] = u32x4_t{0, 0, 0, 0};
-                if (there && s < S && pos < K) t.a[h] = *reinterpret_cast<const u32x4_t*>(row + pos);
+                const int pos = place(s, h);
+                t.a[h] = __builtin_amdgcn_raw_buffer_load_b128(ra, there && pos >= 0 ? token * K + pos : kDropped, 0, 0);
             }
-            t.sa = there && s < S ? p.sa[(int64_t)s * p.a_rows + token] : 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) t.sb[k] = s < S ? sb[k][s] : 0.0f;
+            const Rsrc rs = make_rsrc(sa + (int64_t)(s < S ? s : 0) * p.a_rows, sa_size);
+            t.sa = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, there && s < S ? token * 4 : kDropped, 0, 0));
         };
         v4f acc[1][1] = {};
         auto sums = [&](auto careful) {
             constexpr bool CAREFUL = decltype(careful)::value;
-            Block now, next;
-            load(now, wave);
             for (int s = wave; s < S; s += waves) {
-                load(next, s + waves);
+                load_b(next, s + waves);
+                load_a(next, s + waves);
                 const Wide bw = widen(join(__builtin_bit_cast(v4i, now.b[0]), __builtin_bit_cast(v4i, now.b[1])));
                 const Wide aw = widen(join(__builtin_bit_cast(v4i, now.a[0]), __builtin_bit_cast(v4i, now.a[1])));
                 const v4f d = mma16(bw, aw);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    acc[0][0][k] = CAREFUL ? scaled_sum(d[k], now.sa, now.sb[k], acc[0][0][k]) : fmaf(d[k], now.sa * now.sb[k], acc[0][0][k]);
+                for (int k = 0; k < 4; ++k) {
+                    const float t = now.sb[BROW ? k : 0];
+                    acc[0][0][k] = CAREFUL ? scaled_sum(d[k], now.sa, t, acc[0][0][k]) : fmaf(d[k], now.sa * t, acc[0][0][k]);
+                }
                 now = next;
             }
         };
+        if (S > 0) {
+            if (row0 != g.row) load_b(now, wave);
+            load_a(now, wave);
+        }
         sums(std::false_type{});
         if (__builtin_expect(not_finite(acc), 0)) {
             acc[0][0] = v4f{};
+            load_b(now, wave);
+            load_a(now, wave);
             sums(std::true_type{});
         }
         // Register k of lane l: row of A l % 16, row of B 4 (l / 16) + k.
@@ -364,19 +387,25 @@ int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len) {
                     Groups{j.offsets, (int)j.experts, (int)j.rows, j.clear_rest}, (int)j.N, (int)j.K,
                     (int)((j.K + kBlock - 1) / kBlock), static_cast<char*>(j.c), j.ct, j.N * eb % 16 == 0 && (uintptr_t)j.c % 16 == 0, 0};
     const int64_t some = std::min(j.rows, j.experts + (j.clear_rest ? 1 : 0));  // groups that hold a row, at most
-    const bool gather = j.tokens != nullptr;
-    // Up to eight rows a group on average: a pass over the weights.  (With more, the 64 x 64 tile's
-    // reads of A are shared by its columns.)
+    const bool gather = j.tokens != nullptr, brow = j.stacked && j.N % kBlock != 0;
+    // Up to eight rows a group on average: a pass over the weights.  (64 experts of 2048 x 4096, weights
+    // from memory, by events: 64 rows 99 us, in 64 x 64 tiles 150; 256 rows 139 and 176; 512 rows 160
+    // and 187, but 140 and 128 where the weights are in the last-level cache; 1024 rows 210 and 138.)
     if (j.rows <= 8 * some) {
         const int64_t groups = some * ((j.N + kFewRows - 1) / kFewRows);
         if (groups > INT32_MAX) return too_many(what, msg, msg_len);
-        int waves = groups <= 256 ? kFewMaxWaves : groups <= 1024 ? 8 : 4;
-        while (waves > 1 && waves >= 2 * p.S) waves /= 2;
-        for (int64_t first = 0; first < groups; first += kMaxGrid / 2) {  // (workgroups of up to 1024 threads)
-            const dim3 grid((unsigned)std::min(groups - first, kMaxGrid / 2)), block(waves * kWave);
+        // Eight waves, of two K blocks or more each.  (64 experts of 2048 x 4096, 64 rows of 8 tokens,
+        // weights from memory, by events: 99 us; with 4 waves 105, with 16 143.  32 experts of
+        // 1024 x 1024, 32 rows: 13.5 with 8, 10.5 with 4.)
+        int waves = kFewMaxWaves;
+        while (waves > 1 && waves * 2 > p.S) waves /= 2;
+        for (int64_t first = 0; first < groups; first += kMaxGrid) {
+            const dim3 grid((unsigned)std::min(groups - first, kMaxGrid)), block(waves * kWave);
             p.first = (unsigned)first;
-            if (gather) FP4Q_LAUNCH(k_grouped_few<true>, grid, block, 0, stream, p);
-            else FP4Q_LAUNCH(k_grouped_few<false>, grid, block, 0, stream, p);
+            if (brow && gather) FP4Q_LAUNCH((k_grouped_few<true, true>), grid, block, 0, stream, p);
+            else if (brow) FP4Q_LAUNCH((k_grouped_few<true, false>), grid, block, 0, stream, p);
+            else if (gather) FP4Q_LAUNCH((k_grouped_few<false, true>), grid, block, 0, stream, p);
+            else FP4Q_LAUNCH((k_grouped_few<false, false>), grid, block, 0, stream, p);
         }
         return status(what, msg, msg_len);
     }
@@ -386,7 +415,6 @@ int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len) {
     });
     const int64_t groups = (j.rows + (tile - 1) * some) / tile * ((j.N + tile - 1) / tile);
     if (groups > INT32_MAX) return too_many(what, msg, msg_len);
-    const bool brow = j.stacked && j.N % kBlock != 0;
     if (brow && gather) launch_tiles<true, true>(p, tile, groups, stream);
     else if (brow) launch_tiles<true, false>(p, tile, groups, stream);
     else if (gather) launch_tiles<false, true>(p, tile, groups, stream);
