@@ -101,13 +101,11 @@ __global__ __launch_bounds__(kThreads) void k_grouped(GroupedParams p) {
     v4f acc[TB][TA];
     tile_sums<BROW, GATHER, true, true>(acc, t, lds, wave, lane, loads);
     wait_all_barrier();  // LDS is reused below
-    const int eb = p.ct == 1 ? 4 : 2;
-    char* c = p.c + (int64_t)row0 * p.N * eb;
-    const Rsrc rc = make_rsrc(c, (int64_t)t.rows_a * p.N * eb);
+    char* c = p.c + (int64_t)row0 * p.N * 2;  // (a binary32 C takes the smaller tiles)
+    const Rsrc rc = make_rsrc(c, (int64_t)t.rows_a * p.N * 2);
     int l = lane;  // opaque: the epilogue's addresses are not kept in registers through the K loop
     asm volatile("" : "+v"(l));
-    if (p.ct == 1) store_tile16<4>(acc, lds, c, rc, wave, wave >> 2, wave & 3, l, t.rows_a, n0, p.N, p.whole);
-    else store_tile16<2>(acc, lds, c, rc, wave, wave >> 2, wave & 3, l, t.rows_a, n0, p.N, p.whole);
+    store_tile16<2>(acc, lds, c, rc, wave, wave >> 2, wave & 3, l, t.rows_a, n0, p.N, p.whole);
 }
 
 template <int T, bool BROW, bool WIDE, bool GATHER>

@@ -47,7 +47,7 @@ def expert_order(topk_ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor
     tokens, top_k = ids.shape
     if top_k < 1:
         raise ValueError("topk_ids has no columns")
-    new = lambda *s: ids.new_empty(s, dtype=torch.int32)
+    new = ids.new_empty if ids.dtype == torch.int32 else lambda *s: ids.new_empty(s, dtype=torch.int32)
     n = tokens * top_k
     o = ExpertOrder(new(experts + 1 if experts > 0 else 0), new(n), new(n), new(tokens, top_k))
     stream, free = _raw_stream(ids.device), None
