@@ -295,19 +295,19 @@ struct F8Loads {
         const int r = (wave % 4) * kWave + lane, row = wave < 4 ? t.a_row<GATHER>(r) : t.sb_at<BROW>(r);
         sc_off = row >= 0 ? row * 4 : kDropped;
     }
-    // The last block of K: pieces past it are not read.
+    // Before the loads of stage s: pieces past K or s_hi are not read (zeros take their place).
     __device__ __forceinline__ void cut(const F8Tile& t, int s, int wave, int lane) {
-        if (__builtin_expect((s + 1) * kBlock <= t.K || s >= t.s_hi || s * kBlock + piece(wave, lane) * 16 < t.K, 1)) return;
+        if (__builtin_expect((s + 1) * kBlock <= t.K && s < t.s_hi, 1)) return;
+        const bool in = s < t.s_hi && s * kBlock + piece(wave, lane) * 16 < t.K;
 #pragma unroll
-        for (int L = 0; L < kLoads; ++L) at[L] = kDropped;
+        for (int L = 0; L < kLoads; ++L) at[L] = in ? at[L] : kDropped;
     }
-    // (Past s_hi: nothing, or some bytes of A that no product takes.)
     __device__ __forceinline__ void issue(const F8Tile& t, uint8_t* lds, int wave, int s, int L) const {
         uint8_t* stage = lds + (s & 1) * kStageBytes;
         if (L < kLoads) {
             const int d = wave + kWaves * (L % (kLoads / 2));
             uint8_t* dst = stage + (L < kLoads / 2 ? 0 : BM * kRowStage) + d * 8 * kRowStage;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? t.ra : t.rb, (LdsPtr)dst, 16, at[L], s < t.s_hi ? s * kBlock : kPastWindow, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(L < kLoads / 2 ? t.ra : t.rb, (LdsPtr)dst, 16, at[L], s * kBlock, 0, 0);
         } else {
             const bool sc_a = wave < 4;
             const int here = s < t.s_hi ? s : t.s_lo;

@@ -305,17 +305,21 @@ struct BigTile {
     static __device__ __forceinline__ int load_piece(int q, int wave, int lane) {
         return (lane % 8) ^ (q < kLoads / 2 ? 4 * (wave & 1) + lane / 16 : lane / 16 % 2 + 2 * (2 * load_row(q, wave) / F % 4));
     }
-    // The last stage of K: pieces past it are not read (zeros take their place).
+    // Before the loads of stage s: pieces past K or the range are not read (zeros take their place).
     __device__ __forceinline__ void cut(int K, int s, int wave, int lane) {
-        if (__builtin_expect((s + 1) * kBlock <= K || s >= s_hi, 1)) return;
+        if (__builtin_expect((s + 1) * kBlock <= K && s < s_hi, 1)) return;
+        if (s >= s_hi) {
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) at[q] = kPastWindow;
+            return;
+        }
 #pragma unroll
         for (int q = 0; q < kLoads; ++q) at[q] = s * kBlock + 16 * load_piece(q, wave, lane) < K ? at[q] : kPastWindow;
     }
-    // (s >= s_hi: nothing is read.)
     __device__ __forceinline__ void issue(uint8_t* lds, int wave, int s, int q) const {
         const bool is_a = q < kLoads / 2;
         uint8_t* dst = lds + (s & 1) * kStage + (is_a ? 0 : T * kRowStage) + load_row(q, wave) * 8 * kRowStage;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (LdsPtr)dst, 16, at[q], s < s_hi ? s * kBlock : kPastWindow, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (LdsPtr)dst, 16, at[q], s * kBlock, 0, 0);
     }
     __device__ __forceinline__ void first_stages(uint8_t* lds, int K, int wave, int lane) {
         if (s_lo >= s_hi) return;  // K = 0 has no operands to read
