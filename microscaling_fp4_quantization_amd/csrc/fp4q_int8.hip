@@ -25,7 +25,7 @@ namespace {
 // Quantizer.  WAVES waves per row (one: four rows per workgroup), a thread holding up to
 // CHUNKS pieces of 8 elements, so that the row is read once; longer rows are read twice.
 // A row that holds a NaN or an infinity gets that scale (NaN or infinity) and codes of 0:
-// on use all of it is NaN.
+// on use all of it is NaN.  Bound by memory: 8192 x 18944 bf16, 466 MB, 87 to 89 us (5.3 TB/s).
 
 constexpr float kMinScale = 0x1p-126f;
 // Scales for which the corrected quotient is RN32(x / s) wherever it can matter: from 2^-60
@@ -265,7 +265,9 @@ __device__ __forceinline__ void tile_at(unsigned g, int64_t rows, int64_t cols, 
 // are read while this half's products run, so that a stage is free half a block before its
 // products end: one barrier per block, and loads go out a block and a half before they are read.
 // Workgroups are persistent: a tile's first two stages are loaded while the tile before is
-// scaled and stored, straight from registers, so that LDS is free.
+// scaled and stored, straight from registers, so that LDS is free.  4096 x 4096 x 14336 to bf16:
+// 157 to 168 us (2.9 to 3.1 POP/s), the matrix cores busy in 70% to 72% of the cycles at 1.9 GHz;
+// 125 us with operands of zero, so that power is part of what bounds it.
 //
 // For that a lane's columns are neighbours: fragment i of a wave's B holds at position r its row
 // 4 F (r / 4) + 4 i + r % 4, so that lane l ends up with columns 4 F (l / 16) .. + 4 F - 1 of row

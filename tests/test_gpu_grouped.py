@@ -2,8 +2,7 @@
 
 Bounds are fp8_gemm_b128's: binary32 results are off by at most (K / 128 + 8) 2^-23 of size =
 |A_hat| |B_hat|^T; bf16 ones by 2^-14 of size (the 8-bit matrix cores' sums hold about 16 bits)
-and half a step of bf16, 2^-8 of the value (its own bound of half a step, 2^-9, doubled where
-the value crosses a power of two)."""
+and half a step of bf16, 2^-8 of the value."""
 import numpy as np
 import pytest
 import torch
