@@ -595,8 +595,8 @@ size_t expert_order_workspace_bytes(int64_t tokens, int32_t top_k, int32_t exper
  *               neither, in C.  Rows that no group owns are left as they are
  *   tokens      device, rows: the row of A that goes into each row of C (one that A does
  *               not have gives zeros); or NULL: row i of A (then a_rows == rows)
- *   N, K        as for fp8_gemm_b128; experts 1..512; with tokens, A is at most 2^31 - 1
- *               bytes
+ *   rows, N, K  at most 2^28; as for fp8_gemm_b128; experts 1..512; with tokens, A is at
+ *               most 2^31 - 1 bytes
  *   c, ct       device out, rows x N
  * No workspace.  Groups of up to 8 rows on average take a kernel that streams the
  * weights of the experts in use once; others tiles of 64, 128 or 256.  Arithmetic and

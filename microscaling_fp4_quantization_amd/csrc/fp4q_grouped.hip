@@ -65,6 +65,7 @@ __device__ __forceinline__ bool grouped_tile(const GroupedParams& p, int side, F
     int tm, tn;
     tile_at(group % 8, group / 8, tiles_m, tiles_n, tm, tn);
     const GroupTile g = group_tile(p.groups, side, tm);
+    if (g.group < 0) return false;
     const bool rest = g.group >= p.groups.count;  // rows of no group: no products
     const int e = rest ? 0 : g.group;
     row0 = g.row;

@@ -12,7 +12,8 @@ namespace {
 
 // Offsets outside 0 .. rows are taken as the nearest inside, a group that ends before it starts
 // as empty: no group holds a row that does not exist.  (Offsets out of order can make groups that
-// overlap, and more tiles than a launch has workgroups for: those are left out.)  With `rest`, the
+// overlap, and more tiles than a launch has workgroups for: those are left out.  At most 2^28 rows,
+// so that the tiles of 512 such groups are counted in 32 bits.)  With `rest`, the
 // rows behind the last group are one more.
 struct Groups {
     const int* offsets;

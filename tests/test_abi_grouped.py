@@ -44,6 +44,15 @@ def test_gemm_validation(L):
     assert gemm(n=0, a=None, sa=None, b=None, sb=None, off=None, c=None) == OK
 
 
+@pytest.mark.parametrize("tokens", [None, A])
+def test_gemm_rows_that_the_groups_tiles_cannot_count(L, tokens):
+    """512 groups that all hold every row (offsets out of order) take 2^22 tiles of 64 rows each at
+    2^28 rows: 2^30 for 256 of them, a sum that 32 bits hold; more rows are refused."""
+    for rows in ((1 << 28) + 1, 1 << 30, (1 << 31) - 1):
+        got = L.fp8_grouped_gemm_b128(A, B, 1 if tokens else rows, C, D, 0, E, 4, tokens, rows, 1, 16, F, 0, None)
+        assert got == SHAPE and "2^28" in err(L), rows
+
+
 def test_linear_validation(L):
     T, K, N, X = 40, 96, 70, 3
     saved, ws = L.fp8_grouped_linear_saved_bytes(T, K, N, X, 1, 1), L.fp8_grouped_linear_workspace_bytes(T, K, N, X)
