@@ -393,7 +393,8 @@ int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len) {
     const bool gather = j.tokens != nullptr, brow = j.stacked && j.N % kBlock != 0;
     // Up to eight rows a group on average: a pass over the weights.  (64 experts of 2048 x 4096, weights
     // from memory, by events: 64 rows 99 us, in 64 x 64 tiles 150; 256 rows 139 and 176; 512 rows 160
-    // and 187, but 140 and 128 where the weights are in the last-level cache; 1024 rows 210 and 138.)
+    // and 187, but 140 and 128 where the weights are in the last-level cache; 1024 rows 210 and 138.  The sizes
+    // are not known here: should one expert own all of 512 rows, 148 us, in tiles 24.)
     if (j.rows <= 8 * some) {
         const int64_t groups = some * ((j.N + kFewRows - 1) / kFewRows);
         if (groups > INT32_MAX) return too_many(what, msg, msg_len);

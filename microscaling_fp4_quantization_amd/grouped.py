@@ -78,7 +78,7 @@ def fp8_grouped_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes
     A: codes and row scales as fp8_quantize_b128 writes them.  W: codes experts x N x K with
     tile scales experts x ceil(N / 128) x ceil(K / 128), each expert's by itself; or both 2-D,
     the stacked matrix (experts * N) x K as ExpertWeights holds it.  ``tokens``: int32, one row
-    of A per row of C; without it row i of A is row i of C.  Rows that no group owns are left
+    of A per row of C (at most 2^28); without it row i of A is row i of C.  Rows that no group owns are left
     as they are in ``out`` (and are uninitialized without one).  It has no gradient
     (fp8_grouped_linear has): a backward pass through scales that require one raises."""
     a_rows, k = _b128_operand(a_codes, a_scales, B128_ROW, "a")

@@ -424,6 +424,99 @@ def test_training_steps_of_two_layers():
     assert h.grad.shape == h.shape and w1.grad.shape == w1.shape and bool(h.grad.isfinite().all()) and bool((w1.grad != 0).any())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sizes,n,k", [([3, 0, 5], 40, 72), ([200, 31, 400], 264, 136), ([700, 1, 900], 520, 384)])
+def test_linear_keeps_what_is_not_finite_to_its_expert(sizes, n, k, dtype):
+    """NaN and infinity in one expert's rows and behind the last group leave the other experts' bits alone."""
+    g = gen(n)
+    ends = sizes_to_ends(sizes)
+    rows = ends[-1] + 5
+    x = torch.randn(rows, k, generator=g, device=DEV).to(dtype)
+    w = torch.randn(len(sizes), n, k, generator=g, device=DEV).to(dtype)
+    dy = torch.randn(rows, n, generator=g, device=DEV).to(dtype)
+
+    def step(x, dy):
+        a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+        y = fq.fp8_grouped_linear(a, b, i32(ends))
+        return (y.detach(), *torch.autograd.grad(y, (a, b), dy))
+
+    y, dx, dw = step(x, dy)
+    bad_x, bad_dy = x.clone(), dy.clone()
+    bad_x[ends[-1]:], bad_dy[ends[-1]:] = float("nan"), float("inf")
+    for got, want in zip(step(bad_x, bad_dy), (y, dx, dw)):
+        assert torch.equal(got, want)
+    last = ends[-2]
+    bad_x[last], bad_dy[last] = float("inf"), float("nan")
+    yy, dxx, dww = step(bad_x, bad_dy)
+    keep = torch.ones(rows, dtype=torch.bool, device=DEV)
+    keep[last] = False
+    assert torch.equal(yy[keep], y[keep]) and torch.equal(dxx[keep], dx[keep]) and torch.equal(dww[:-1], dw[:-1])
+    assert bool(yy[last].isnan().all()) and bool(dxx[last].isnan().all()) and bool(dww[-1].isnan().all())
+
+
+def test_linear_backward_twice():
+    g = gen(3)
+    ends = sizes_to_ends([70, 0, 130])
+    x = torch.randn(200, 144, generator=g, device=DEV, requires_grad=True)
+    w = torch.randn(3, 96, 144, generator=g, device=DEV, requires_grad=True)
+    y = fq.fp8_grouped_linear(x, w, i32(ends))
+    dy = torch.randn(200, 96, generator=g, device=DEV)
+    first = torch.autograd.grad(y, (x, w), dy, retain_graph=True)
+    again = torch.autograd.grad(y, (x, w), dy)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    ends = i32(ends)
+    y = fq.fp8_grouped_linear(x, w, ends)
+    ends.add_(0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_one_token_in_many_rows():
+    """The same row of A for every row of C, in one group and in several: the same bits as each by itself."""
+    g = gen(8)
+    codes, scales = experts_of(torch.randn(3, 136, 256, generator=g, device=DEV))
+    qa = fq.fp8_quantize_b128(torch.randn(4, 256, generator=g, device=DEV))
+    for rows in (9, 400):
+        ends = [0, rows // 3, rows // 3, rows]
+        tokens = torch.full((rows,), 2, dtype=torch.int32, device=DEV)
+        c = fq.fp8_grouped_gemm_b128(qa.codes, qa.scales, codes, scales, i32(ends), tokens=tokens)
+        for e, (lo, hi) in enumerate(zip(ends, ends[1:])):
+            assert hi == lo or bool((c[lo:hi] == c[lo]).all())
+        assert not torch.equal(c[0], c[-1])
+
+
+@pytest.mark.parametrize("tokens", [20, 700])
+def test_one_graph_over_routings_of_any_sizes(tokens):
+    """A captured prompt is replayed with routings that give its experts other numbers of rows."""
+    g = gen(tokens)
+    e, top_k = 6, 2
+    codes, scales = experts_of(torch.randn(e, 200, 136, generator=g, device=DEV))
+    h = torch.randn(tokens, 136, generator=g, device=DEV)
+    ids = torch.zeros(tokens, top_k, dtype=torch.int64, device=DEV)
+
+    def call():
+        o = fq.expert_order(ids, e)
+        q = fq.fp8_quantize_b128(h)
+        return o, fq.fp8_grouped_gemm_b128(q.codes, q.scales, codes, scales, o.offsets, tokens=o.tokens)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        order, out = call()
+    for routing in (torch.rand(tokens, e, generator=g, device=DEV).topk(top_k).indices,
+                    torch.full((tokens, top_k), 4, device=DEV), torch.full((tokens, top_k), -1, device=DEV),
+                    torch.rand(tokens, e, generator=g, device=DEV).pow(8).topk(top_k).indices):
+        ids.copy_(routing)
+        out.fill_(5.0)
+        graph.replay()
+        want_order, want = call()
+        torch.cuda.synchronize()
+        end = int(want_order.offsets[-1])
+        assert torch.equal(order.offsets, want_order.offsets) and torch.equal(order.order, want_order.order)
+        assert torch.equal(out[:end], want[:end]) and bool((out[end:] == 5.0).all())
+
+
 def test_streams_threads_and_graphs():
     import threading
     g = gen(11)
