@@ -615,8 +615,8 @@ fp4q_status fp8_grouped_gemm_b128(const uint8_t* a_codes, const float* a_scales,
  *   x, y, dy, dx  rows x in and rows x out, dtype xt; w, dw experts x out x in, dtype
  *                 wt; contiguous, aligned to their elements
  *   offsets       device, experts + 1, as for fp8_grouped_gemm_b128 and the same for
- *                 both calls.  Rows behind the last group get zeros in y and dx; an
- *                 expert without rows gets a dw of zeros
+ *                 both calls.  Rows before the first group and behind the last get zeros
+ *                 in y and dx; an expert without rows gets a dw of zeros
  *   want_dx, want_dw, saved, ws  as for fp8_linear_forward
  *   rows, in, out  each below 2^21; experts 1..512
  * Errors as for fp8_linear_forward.

@@ -389,14 +389,16 @@ int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len) {
                     (int)(j.stacked ? j.N : (j.N + kBlock - 1) / kBlock * kBlock), j.tokens,
                     Groups{j.offsets, (int)j.experts, (int)j.rows, j.clear_rest}, (int)j.N, (int)j.K,
                     (int)((j.K + kBlock - 1) / kBlock), static_cast<char*>(j.c), j.ct, j.N * eb % 16 == 0 && (uintptr_t)j.c % 16 == 0, 0};
-    const int64_t some = std::min(j.rows, j.experts + (j.clear_rest ? 1 : 0));  // groups that hold a row, at most
+    // Groups that hold a row, at most: as the kernel is chosen, and with all rows of no group.
+    const int64_t some = std::min(j.rows, j.experts + (j.clear_rest ? 1 : 0));
+    const int64_t most = std::min(j.rows, j.experts + (j.clear_rest ? 2 : 0));
     const bool gather = j.tokens != nullptr, brow = j.stacked && j.N % kBlock != 0;
     // Up to eight rows a group on average: a pass over the weights.  (64 experts of 2048 x 4096, weights
     // from memory, by events: 64 rows 99 us, in 64 x 64 tiles 150; 256 rows 139 and 176; 512 rows 160
     // and 187, but 140 and 128 where the weights are in the last-level cache; 1024 rows 210 and 138.  The sizes
     // are not known here: should one expert own all of 512 rows, 148 us, in tiles 24.)
     if (j.rows <= 8 * some) {
-        const int64_t groups = some * ((j.N + kFewRows - 1) / kFewRows);
+        const int64_t groups = most * ((j.N + kFewRows - 1) / kFewRows);
         if (groups > INT32_MAX) return too_many(what, msg, msg_len);
         // Eight waves, of two K blocks or more each.  (64 experts of 2048 x 4096, 64 rows of 8 tokens,
         // weights from memory, by events: 99 us; with 4 waves 105, with 16 143.  32 experts of
@@ -417,7 +419,7 @@ int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len) {
     const int tile = choose(j.ct == 1, p.S, [&](int t) {
         return std::max((double)some, (double)j.rows / t + 0.5 * (double)some) * (double)((j.N + t - 1) / t);
     });
-    const int64_t groups = (j.rows + (tile - 1) * some) / tile * ((j.N + tile - 1) / tile);
+    const int64_t groups = (j.rows + (tile - 1) * most) / tile * ((j.N + tile - 1) / tile);
     if (groups > INT32_MAX) return too_many(what, msg, msg_len);
     if (brow && gather) launch_tiles<true, true>(p, tile, groups, stream);
     else if (brow) launch_tiles<true, false>(p, tile, groups, stream);

@@ -13,20 +13,24 @@ namespace {
 // Offsets outside 0 .. rows are taken as the nearest inside, a group that ends before it starts
 // as empty: no group holds a row that does not exist.  (Offsets out of order can make groups that
 // overlap, and more tiles than a launch has workgroups for: those are left out.  At most 2^28 rows,
-// so that the tiles of 512 such groups are counted in 32 bits.)  With `rest`, the
-// rows behind the last group are one more.
+// so that the tiles of 512 such groups are counted in 32 bits.)  With `rest`, the rows of no
+// group are two more: those behind the last group, and those before the first.
 struct Groups {
     const int* offsets;
     int count;   // groups
     int rows;
     bool rest;
 
-    __device__ __forceinline__ int total() const { return count + (rest ? 1 : 0); }
+    __device__ __forceinline__ int total() const { return count + (rest ? 2 : 0); }
+    __device__ __forceinline__ int bound(int e) const { return min(max(offsets[e], 0), rows); }
     __device__ __forceinline__ void range(int e, int& lo, int& hi) const {
         lo = hi = rows;
-        if (e < total()) {
-            lo = min(max(offsets[e], 0), rows);
-            hi = e < count ? min(max(offsets[e + 1], lo), rows) : rows;
+        if (e < count) {
+            lo = bound(e);
+            hi = min(max(offsets[e + 1], lo), rows);
+        } else if (e < total()) {
+            lo = bound(count);
+            if (e > count) hi = min(bound(0), lo), lo = 0;
         }
     }
 };

@@ -190,7 +190,7 @@ struct GroupedGemmJob {
     int64_t rows, N, K;
     void* c;
     int ct;                  // 0 bf16, 1 f32
-    bool clear_rest;         // rows behind the last group: zeros, else left as they are
+    bool clear_rest;         // rows of no group: zeros, else left as they are
     void* stream;
 };
 

@@ -185,9 +185,9 @@ def fp8_grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) 
     """x (rows x in-features, the rows by expert) times each expert's matrix of w (experts x
     out-features x in-features) transposed, both bfloat16 or float32, on 8-bit block-128
     operands; differentiable in both.  Expert e owns rows offsets[e] .. offsets[e + 1] - 1
-    (int32, as expert_order gives them; read on the device); rows behind the last group are
-    zeros in y and dx.  y and dx have x's dtype, dw has w's.  ``offsets`` must not be written
-    before the backward pass."""
+    (int32, as expert_order gives them, or a run of those for a run of the experts; read on the
+    device); rows before the first group and behind the last are zeros in y and dx.  y and dx
+    have x's dtype, dw has w's.  ``offsets`` must not be written before the backward pass."""
     if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
         raise ValueError(f"x has shape {tuple(x.shape)}, w {tuple(w.shape)}: needed are rows x in and experts x out x in")
     if x.device != w.device or not x.is_cuda:
