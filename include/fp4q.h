@@ -592,7 +592,9 @@ size_t expert_order_workspace_bytes(int64_t tokens, int32_t top_k, int32_t exper
  *               so no size of a group needs to be known to the host.  One outside
  *               0..rows is taken as the nearest inside, a group that ends before it
  *               starts as empty; groups that overlap leave the rows of either, or
- *               neither, in C.  Rows that no group owns are left as they are
+ *               neither, in C.  Rows that no group owns (slots of no expert, say) are left
+ *               as they are; fp8_grouped_gemm_b128_cleared gives them zeros, and all
+ *               others the same bits
  *   tokens      device, rows: the row of A that goes into each row of C (one that A does
  *               not have gives zeros); or NULL: row i of A (then a_rows == rows)
  *   rows, N, K  at most 2^28; as for fp8_gemm_b128; experts 1..512; with tokens, A is at
@@ -606,6 +608,10 @@ fp4q_status fp8_grouped_gemm_b128(const uint8_t* a_codes, const float* a_scales,
                                   const float* b_scales, int32_t stacked, const int32_t* offsets, int32_t experts,
                                   const int32_t* tokens, int64_t rows, int64_t N, int64_t K, void* c, int32_t ct,
                                   void* stream);
+fp4q_status fp8_grouped_gemm_b128_cleared(const uint8_t* a_codes, const float* a_scales, int64_t a_rows,
+                                          const uint8_t* b_codes, const float* b_scales, int32_t stacked,
+                                          const int32_t* offsets, int32_t experts, const int32_t* tokens, int64_t rows,
+                                          int64_t N, int64_t K, void* c, int32_t ct, void* stream);
 
 /*
  * A training step's expert layer on them, its rows already by expert: for the rows of

@@ -43,7 +43,7 @@ EXPORTS = ("mxfp4_quantize", "nvfp4_quantize", "nvfp4_quantize_noalloc", "fp4_qu
            "fp8_quantize_b128", "fp8_gemm_b128", "fp8_gemm_b128_workspace_bytes",
            "fp8_linear_forward", "fp8_linear_backward", "fp8_linear_saved_bytes", "fp8_linear_workspace_bytes",
            "int8_quantize_rows", "int8_gemm", "int8_gemm_workspace_bytes", "int8_linear", "int8_linear_workspace_bytes",
-           "expert_order", "expert_order_workspace_bytes", "fp8_grouped_gemm_b128",
+           "expert_order", "expert_order_workspace_bytes", "fp8_grouped_gemm_b128", "fp8_grouped_gemm_b128_cleared",
            "fp8_grouped_linear_forward", "fp8_grouped_linear_backward", "fp8_grouped_linear_saved_bytes",
            "fp8_grouped_linear_workspace_bytes",
            "moe_layer", "moe_layer_workspace_bytes",
@@ -111,10 +111,11 @@ def _bind(l):
     l.int8_gemm_workspace_bytes.restype = l.int8_linear_workspace_bytes.restype = sz
     l.expert_order.argtypes = [P, i32, i64, i32, i32, P, P, P, P, P, sz, P]
     l.expert_order_workspace_bytes.argtypes = [i64, i32, i32]
-    l.fp8_grouped_gemm_b128.argtypes = [P, P, i64, P, P, i32, P, i32, P, i64, i64, i64, P, i32, P]
+    for f in (l.fp8_grouped_gemm_b128, l.fp8_grouped_gemm_b128_cleared):
+        f.argtypes, f.restype = [P, P, i64, P, P, i32, P, i32, P, i64, i64, i64, P, i32, P], c.c_int
     l.fp8_grouped_linear_forward.argtypes = [P, i32, P, i32, P, i32, i64, i64, i64, P, i32, i32, P, sz, P, sz, P]
     l.fp8_grouped_linear_backward.argtypes = [P, i32, i32, P, i32, i64, i64, i64, P, P, P, sz, P, sz, P]
-    l.expert_order.restype = l.fp8_grouped_gemm_b128.restype = c.c_int
+    l.expert_order.restype = c.c_int
     l.fp8_grouped_linear_forward.restype = l.fp8_grouped_linear_backward.restype = c.c_int
     l.fp8_grouped_linear_saved_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
     l.fp8_grouped_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]

@@ -735,11 +735,10 @@ size_t expert_order_workspace_bytes(int64_t tokens, int32_t top_k, int32_t exper
     return fp4q::expert_order_workspace_bytes(tokens * top_k, experts);
 }
 
-fp4q_status fp8_grouped_gemm_b128(const uint8_t* a_codes, const float* a_scales, int64_t a_rows, const uint8_t* b_codes,
-                                  const float* b_scales, int32_t stacked, const int32_t* offsets, int32_t experts,
-                                  const int32_t* tokens, int64_t rows, int64_t N, int64_t K, void* c, int32_t ct,
-                                  void* stream) {
-    const char* fn = "fp8_grouped_gemm_b128";
+static fp4q_status grouped_gemm(const char* fn, const uint8_t* a_codes, const float* a_scales, int64_t a_rows, const uint8_t* b_codes,
+                                const float* b_scales, int32_t stacked, const int32_t* offsets, int32_t experts,
+                                const int32_t* tokens, int64_t rows, int64_t N, int64_t K, void* c, int32_t ct,
+                                bool clear_rest, void* stream) {
     TRY(check_dtype(fn, ct));
     TRY(check_experts(fn, experts));
     if (a_rows < 0 || rows < 0 || N < 0 || K < 0) return fail(FP4Q_ERR_SHAPE, "%s: negative size", fn);
@@ -765,7 +764,23 @@ fp4q_status fp8_grouped_gemm_b128(const uint8_t* a_codes, const float* a_scales,
     }
     char msg[256] = {0};
     return launched(fp4q::launch_grouped_gemm({a_codes, a_scales, a_rows, b_codes, b_scales, stacked != 0, offsets, experts, tokens, rows, N, K,
-                                               c, ct, false, stream}, msg, sizeof msg), msg);
+                                               c, ct, clear_rest, experts, stream}, msg, sizeof msg), msg);
+}
+
+fp4q_status fp8_grouped_gemm_b128(const uint8_t* a_codes, const float* a_scales, int64_t a_rows, const uint8_t* b_codes,
+                                  const float* b_scales, int32_t stacked, const int32_t* offsets, int32_t experts,
+                                  const int32_t* tokens, int64_t rows, int64_t N, int64_t K, void* c, int32_t ct,
+                                  void* stream) {
+    return grouped_gemm("fp8_grouped_gemm_b128", a_codes, a_scales, a_rows, b_codes, b_scales, stacked, offsets, experts,
+                        tokens, rows, N, K, c, ct, false, stream);
+}
+
+fp4q_status fp8_grouped_gemm_b128_cleared(const uint8_t* a_codes, const float* a_scales, int64_t a_rows, const uint8_t* b_codes,
+                                          const float* b_scales, int32_t stacked, const int32_t* offsets, int32_t experts,
+                                          const int32_t* tokens, int64_t rows, int64_t N, int64_t K, void* c, int32_t ct,
+                                          void* stream) {
+    return grouped_gemm("fp8_grouped_gemm_b128_cleared", a_codes, a_scales, a_rows, b_codes, b_scales, stacked, offsets, experts,
+                        tokens, rows, N, K, c, ct, true, stream);
 }
 
 // An expert layer's operands in memory, as LinearSaved and the others lay out a linear layer's.
@@ -861,7 +876,7 @@ fp4q_status fp8_grouped_linear_forward(const void* x, int32_t xt, const void* w,
                                                    {w, wt, experts, out, in, f.w.codes, f.w.scales, s.wt.codes, s.wt.scales, stream},
                                                    msg, sizeof msg), msg));
     return launched(fp4q::launch_grouped_gemm({f.x.codes, f.x.scales, rows, f.w.codes, f.w.scales, false, offsets, experts, nullptr, rows, out,
-                                               up16(in), y, xt, true, stream}, msg, sizeof msg), msg);
+                                               up16(in), y, xt, true, experts + 1, stream}, msg, sizeof msg), msg);
 }
 
 fp4q_status fp8_grouped_linear_backward(const void* dy, int32_t xt, int32_t wt, const int32_t* offsets, int32_t experts,
@@ -880,7 +895,7 @@ fp4q_status fp8_grouped_linear_backward(const void* dy, int32_t xt, int32_t wt, 
     char msg[256] = {0};
     TRY(launched(fp4q::launch_fp8_quantize_groups({dy, xt, rows, out, offsets, experts, b.dy.codes, b.dy.scales, b.dyt.codes, b.dyt.scales, stream}, msg, sizeof msg), msg));
     if (dx) TRY(launched(fp4q::launch_grouped_gemm({b.dy.codes, b.dy.scales, rows, s.wt.codes, s.wt.scales, false, offsets, experts, nullptr, rows, in,
-                                                    up16(out), dx, xt, true, stream}, msg, sizeof msg), msg));
+                                                    up16(out), dx, xt, true, experts + 1, stream}, msg, sizeof msg), msg));
     if (dw) TRY(launched(fp4q::launch_grouped_outer({b.dyt.codes, b.dyt.scales, s.xt.codes, s.xt.scales, offsets, experts, rows, out, in, dw, wt, stream}, msg, sizeof msg), msg));
     return ok();
 }

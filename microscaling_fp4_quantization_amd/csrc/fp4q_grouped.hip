@@ -389,8 +389,9 @@ int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len) {
                     (int)(j.stacked ? j.N : (j.N + kBlock - 1) / kBlock * kBlock), j.tokens,
                     Groups{j.offsets, (int)j.experts, (int)j.rows, j.clear_rest}, (int)j.N, (int)j.K,
                     (int)((j.K + kBlock - 1) / kBlock), static_cast<char*>(j.c), j.ct, j.N * eb % 16 == 0 && (uintptr_t)j.c % 16 == 0, 0};
-    // Groups that hold a row, at most: as the kernel is chosen, and with all rows of no group.
-    const int64_t some = std::min(j.rows, j.experts + (j.clear_rest ? 1 : 0));
+    // Groups that hold a row, at most: as the kernel is chosen (a product's is the same, and so are its
+    // bits, whether the other rows are cleared or not), and with all rows of no group.
+    const int64_t some = std::min(j.rows, j.chosen_by);
     const int64_t most = std::min(j.rows, j.experts + (j.clear_rest ? 2 : 0));
     const bool gather = j.tokens != nullptr, brow = j.stacked && j.N % kBlock != 0;
     // Up to eight rows a group on average: a pass over the weights.  (64 experts of 2048 x 4096, weights

@@ -191,6 +191,7 @@ struct GroupedGemmJob {
     void* c;
     int ct;                  // 0 bf16, 1 f32
     bool clear_rest;         // rows of no group: zeros, else left as they are
+    int64_t chosen_by;       // groups that a kernel is chosen for
     void* stream;
 };
 

@@ -9,8 +9,12 @@ A prompt through a mixture of experts, with h the tokens' hidden states:
     o = expert_order(topk_ids, experts)
     q = fp8_quantize_b128(h)
     up = fp8_grouped_gemm_b128(q.codes, q.scales, w13.codes, w13.scales, o.offsets, tokens=o.tokens)
+    ...
+    down = fp8_grouped_gemm_b128(a.codes, a.scales, w2.codes, w2.scales, o.offsets, clear_rest=True)
 
-and, for the weighted sum, row o.position[t, j] of what follows is token t's j-th expert's.
+and, for the weighted sum, row o.position[t, j] of ``down`` is token t's j-th expert's.  A slot of
+no expert has a row behind the last group: ``clear_rest`` makes that a row of zeros (without it no
+kernel writes it, and a weight of 0 does not remove a NaN that the memory held).
 """
 from __future__ import annotations
 
@@ -72,15 +76,16 @@ def _offsets(offsets: torch.Tensor, device) -> int:
 
 def fp8_grouped_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
                           offsets: torch.Tensor, *, tokens: Optional[torch.Tensor] = None, out_dtype=torch.float32,
-                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                          out: Optional[torch.Tensor] = None, clear_rest: bool = False) -> torch.Tensor:
     """C[i] = A_hat[tokens[i]] @ W_hat_e.T for offsets[e] <= i < offsets[e + 1].
 
     A: codes and row scales as fp8_quantize_b128 writes them.  W: codes experts x N x K with
     tile scales experts x ceil(N / 128) x ceil(K / 128), each expert's by itself; or both 2-D,
     the stacked matrix (experts * N) x K as ExpertWeights holds it.  ``tokens``: int32, one row
-    of A per row of C (at most 2^28); without it row i of A is row i of C.  Rows that no group owns are left
-    as they are in ``out`` (and are uninitialized without one).  It has no gradient
-    (fp8_grouped_linear has): a backward pass through scales that require one raises."""
+    of A per row of C (at most 2^28); without it row i of A is row i of C.  Rows that no group owns (expert_order
+    puts slots of no expert there) get zeros with ``clear_rest``; without it they are left as they
+    are in ``out``, and are uninitialized without one.  It has no gradient (fp8_grouped_linear has):
+    a backward pass through scales that require one raises."""
     a_rows, k = _b128_operand(a_codes, a_scales, B128_ROW, "a")
     dev = a_codes.device
     experts = _offsets(offsets, dev)
@@ -107,10 +112,10 @@ def fp8_grouped_gemm_b128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes
     if a_scales.device != dev or b_codes.device != dev or b_scales.device != dev or out.device != dev:
         raise ValueError("operands and out must be on one device")
     # An empty list of rows has no address: the call is none, but "without tokens" is another thing.
-    rc = lib().fp8_grouped_gemm_b128(a_codes.data_ptr(), a_scales.data_ptr(), a_rows, b_codes.data_ptr(), b_scales.data_ptr(),
-                                     stacked, offsets.data_ptr(), experts,
-                                     None if tokens is None else tokens.data_ptr() or offsets.data_ptr(), rows, n, k,
-                                     out.data_ptr(), _dtype_code(out), _raw_stream(dev))
+    call = lib().fp8_grouped_gemm_b128_cleared if clear_rest else lib().fp8_grouped_gemm_b128
+    rc = call(a_codes.data_ptr(), a_scales.data_ptr(), a_rows, b_codes.data_ptr(), b_scales.data_ptr(), stacked,
+              offsets.data_ptr(), experts, None if tokens is None else tokens.data_ptr() or offsets.data_ptr(), rows, n, k,
+              out.data_ptr(), _dtype_code(out), _raw_stream(dev))
     if rc:
         _check(rc)
     if (a_scales.requires_grad or b_scales.requires_grad) and torch.is_grad_enabled():
