@@ -133,8 +133,9 @@ def _sizes(rows, k, n, experts, want_dx, want_dw):
 
 class _Fp8GroupedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets):
-        want_dx, want_dw = ctx.needs_input_grad[:2]
+    def forward(ctx, x, w, offsets, grad):
+        # needs_input_grad goes by the inputs alone, whether a backward pass can follow or not.
+        want_dx, want_dw = (need and grad for need in ctx.needs_input_grad[:2])
         dev = x.device
         experts, n, k = w.shape
         rows = x.shape[0]
@@ -183,7 +184,7 @@ class _Fp8GroupedLinear(torch.autograd.Function):
             _check(rc)
         if free is not None:
             free.append(ws)
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 def fp8_grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
@@ -199,4 +200,4 @@ def fp8_grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) 
         raise ValueError("x and w must be on one device")
     if _offsets(offsets, x.device) != w.shape[0] or w.shape[0] < 1:
         raise ValueError(f"offsets are of {offsets.shape[0] - 1} experts, w has {w.shape[0]}")
-    return _Fp8GroupedLinear.apply(x, w, offsets)
+    return _Fp8GroupedLinear.apply(x, w, offsets, torch.is_grad_enabled())
