@@ -33,8 +33,9 @@ def _sizes(tokens, k, out, xt, wt, want_dx, want_dw):
 
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w):
-        want_dx, want_dw = ctx.needs_input_grad
+    def forward(ctx, x, w, grad):
+        # needs_input_grad goes by the inputs alone, whether a backward pass can follow or not.
+        want_dx, want_dw = (need and grad for need in ctx.needs_input_grad[:2])
         dev = x.device
         out, k = w.shape
         shape = x.shape
@@ -65,7 +66,7 @@ class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        want_dx, want_dw = ctx.needs_input_grad
+        want_dx, want_dw = ctx.needs_input_grad[:2]
         shape, tokens, k, out, xt, wt, w_dtype, need = ctx.sizes
         saved, = ctx.saved_tensors
         dev = dy.device
@@ -85,7 +86,7 @@ class _Fp8Linear(torch.autograd.Function):
             _check(rc)
         if free is not None:
             free.append(ws)
-        return dx, dw
+        return dx, dw, None
 
 
 def fp8_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
@@ -96,4 +97,4 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
         raise ValueError(f"x has shape {tuple(x.shape)}, w {tuple(w.shape)}: the last sizes must agree")
     if x.device != w.device or not x.is_cuda:
         raise ValueError("x and w must be on one device")
-    return _Fp8Linear.apply(x, w)
+    return _Fp8Linear.apply(x, w, torch.is_grad_enabled())

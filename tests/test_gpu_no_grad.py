@@ -57,6 +57,19 @@ def test_grouped_linear(calls, mode, x_grad):
     assert w.grad is not None and bool(w.grad[0].any()) and not bool(w.grad[1].any())
 
 
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_linear(calls, mode):
+    x = torch.randn(3, 70, 256, device=DEV, requires_grad=True)
+    w = torch.nn.Parameter(torch.randn(128, 256, device=DEV))
+    want = fq.fp8_linear(x, w)
+    with mode():
+        y = fq.fp8_linear(x, w)
+        assert not y.requires_grad and torch.equal(y, want)
+    trained, alone = forward_flags(calls, "fp8_linear_forward", 8)
+    assert trained[0] and trained[1] and trained[3] > 0
+    assert not alone[0] and not alone[1] and alone[2:] == (None, 0)
+
+
 def test_checkpointed_layers():
     """A forward pass without gradients, done again with them in the backward pass: the same gradients."""
     from torch.utils.checkpoint import checkpoint
