@@ -216,6 +216,13 @@ def _borrow(pool: dict, make, dev: torch.device, stream: int, nbytes: int):
     return make(dev, max(nbytes, 1 << 20)), free
 
 
+def _given(ws: torch.Tensor, dev: torch.device) -> torch.Tensor:
+    """A caller's workspace, whose every byte a kernel on `dev` may write."""
+    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous uint8 on {dev}")
+    return ws
+
+
 def workspace_bytes(rows: int = 0, cols: int = 0, block: int = 32) -> int:
     return int(lib().fp4q_workspace_bytes(rows, cols, block))
 

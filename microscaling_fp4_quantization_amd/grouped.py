@@ -24,7 +24,7 @@ from typing import Optional
 
 import torch
 
-from . import (_b128_operand, _borrow, _cdiv, _check, _dtype_code, _free_workspaces, _matrix, _NoGradient, _raw_stream,
+from . import (_b128_operand, _borrow, _cdiv, _check, _dtype_code, _free_workspaces, _given, _matrix, _NoGradient, _raw_stream,
                B128_ROW, gemm_workspace, lib)
 
 
@@ -55,7 +55,9 @@ def expert_order(topk_ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor
     n = tokens * top_k
     o = ExpertOrder(new(experts + 1 if experts > 0 else 0), new(n), new(n), new(tokens, top_k))
     stream, free = _raw_stream(ids.device), None
-    if ws is None and n > 4096:
+    if ws is not None:
+        _given(ws, ids.device)
+    elif n > 4096:
         ws, free = _borrow(_free_workspaces, gemm_workspace, ids.device, stream, _order_workspace(tokens, top_k, experts))
     rc = lib().expert_order(ids.data_ptr(), ids.dtype == torch.int64, tokens, top_k, experts, o.offsets.data_ptr(),
                             o.order.data_ptr(), o.tokens.data_ptr(), o.position.data_ptr(),

@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from . import _borrow, _cdiv, _check, _dtype_code, _free_workspaces, _matrix, _NoGradient, _raw_stream, gemm_workspace, lib
+from . import _borrow, _cdiv, _check, _dtype_code, _free_workspaces, _given, _matrix, _NoGradient, _raw_stream, gemm_workspace, lib
 
 
 @dataclass
@@ -90,7 +90,9 @@ def int8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tens
     bp, bt = _bias(bias, n, dev)
     l, ct = lib(), _dtype_code(out)
     stream, free = _raw_stream(dev), None
-    if ws is None and m > 16:  # at most 16 rows take none
+    if ws is not None:
+        _given(ws, dev)
+    elif m > 16:  # at most 16 rows take none
         need = l.int8_gemm_workspace_bytes(m, n, k)
         if need:
             ws, free = _borrow(_free_workspaces, gemm_workspace, dev, stream, need)
@@ -131,7 +133,9 @@ def int8_linear(x: torch.Tensor, w: Int8Quantized, bias: Optional[torch.Tensor] 
         raise ValueError(f"out must be contiguous, {m} x {n}, on x's device")
     bp, bt = _bias(bias, n, dev)
     stream, free = _raw_stream(dev), None
-    if ws is None:
+    if ws is not None:
+        _given(ws, dev)
+    else:
         need = _linear_workspace(m, k, n)
         if need:
             ws, free = _borrow(_free_workspaces, gemm_workspace, dev, stream, need)
