@@ -5,12 +5,28 @@ import pytest
 
 import tile_choice
 from test_abi import L  # noqa: F401  (the loaded library, built if it is missing)
+from test_gpu_grouped_kernels import PRODUCTS, STEPS
 from test_gpu_int8_kernels import LARGE, RANGES
 
 
 @pytest.mark.parametrize("shape,want", [*LARGE.items(), *RANGES.items()])
 def test_int8(shape, want):
     assert tile_choice.int8(*shape) == want
+
+
+@pytest.mark.parametrize("shape,bf16,f32", STEPS)
+def test_grouped_steps(shape, bf16, f32):
+    sizes, n, k = shape
+    rows, e = sum(sizes) + 5, len(sizes)
+    for wide, want in ((False, bf16), (True, f32)):
+        got = (tile_choice.grouped(rows, e + 1, n, k, wide), tile_choice.grouped(rows, e + 1, k, n, wide), tile_choice.outer(rows, e, n, k, wide))
+        assert got == want
+
+
+@pytest.mark.parametrize("shape,bf16,f32", PRODUCTS)
+def test_grouped_products(shape, bf16, f32):
+    sizes, n, k = shape
+    assert (tile_choice.grouped(sum(sizes) + 3, len(sizes), n, k, False), tile_choice.grouped(sum(sizes) + 3, len(sizes), n, k, True)) == (bf16, f32)
 
 
 def test_int8_formulas_are_the_librarys(L):
