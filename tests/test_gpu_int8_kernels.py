@@ -108,3 +108,51 @@ def test_a_token_among_others_and_alone(m, n, k):
     whole = fq.int8_gemm(a, sa, b, sb, bias)
     for lo, hi in ((0, 1), (m - 20, m - 3), (100, 190), (m - 1, m)):
         assert torch.equal(fq.int8_gemm(a[lo:hi], sa[lo:hi], b, sb, bias), whole[lo:hi])
+
+
+MORE = [(1, 300, 512), (16, 511, 4096), (333, 1031, 1008), (4100, 4099, 384)]  # few rows, tiles of 64 and 128
+
+
+@pytest.mark.parametrize("m,n,k", [*MORE, *LARGE, *RANGES])
+def test_padding(m, n, k):
+    """Rows and columns of zeros, as a padded batch and dropped channels leave them (scale 2^-126, every
+    product of scales below the range), and elsewhere codes that are not 0 under such a scale."""
+    a, sa, b, sb = operands(m, n, k, 31)
+    sa.clamp_(max=0.5)
+    for row in (m // 3, *range(max(m - 70, 0), m)):
+        a[row], sa[row] = 0, 2.0 ** -126
+    b[n // 2], sb[n // 2], b[n - 1], sb[n - 1] = 0, 2.0 ** -126, 0, 2.0 ** -126
+    bias = torch.randn(n, generator=gen(32), device=DEV)
+    for tiny in (False, True):
+        if tiny:
+            a[m // 2].fill_(1)
+            sa[m // 2] = 2.0 ** -126
+        acc = product(a, b)
+        want = by_range(acc, sa, sb)
+        assert torch.equal(fq.int8_gemm(a, sa, b, sb), want)
+        assert torch.equal(fq.int8_gemm(a, sa, b, sb, out_dtype=torch.bfloat16), want.bfloat16())
+        full = acc * (sa.double()[:, None] * sb.double()) + bias.double()
+        got = fq.int8_gemm(a, sa, b, sb, bias)
+        assert bool(((got.double() - full).abs() <= 2.0 ** -24 * (full.abs() + 2 * (full - bias.double()).abs()) * (1 + 2.0 ** -20)).all())
+        zero = (acc == 0)
+        assert torch.equal(got[zero], bias.expand(m, n)[zero])
+        if tiny and m // 2 == m // 3:
+            break  # (one row alone: it is not of zeros any more)
+        sa[m // 3] = float("inf")  # zeros under an infinite scale are NaN, whatever the other rows are
+        assert bool(fq.int8_gemm(a, sa, b, sb, bias)[m // 3].isnan().all())
+        sa[m // 3] = 2.0 ** -126
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,k,n", [(40, 200, 300), (600, 2048, 5000), (4100, 1040, 4099)])
+def test_linear_of_a_padded_batch(tokens, k, n, dtype):
+    """A batch padded with rows of zeros: its own tokens' bits, and the bias in the others."""
+    g = gen(tokens)
+    x = torch.randn(tokens, k, generator=g, device=DEV).to(dtype)
+    w = fq.int8_quantize_rows(torch.randn(n, k, generator=g, device=DEV) * 0.05)
+    bias = torch.randn(n, generator=g, device=DEV).to(dtype)
+    real = tokens * 2 // 3
+    want = fq.int8_linear(x[:real], w, bias)
+    x[real:] = 0
+    y = fq.int8_linear(x, w, bias)
+    assert torch.equal(y[:real], want) and torch.equal(y[real:], bias.expand(tokens - real, n))
