@@ -127,3 +127,41 @@ def test_nan_stays_in_its_rows_and_columns(sizes, n, k, form, dtype):
         keep[tokens == row] = False
     keep[ends[2]:ends[3], 128:256] = False
     assert torch.equal(got[keep], want[keep]) and bool(got[~keep].isnan().all())
+
+
+# Sizes, N, K; N is no multiple of 128, so that experts start inside a block of the stacked scales.
+# The pass over the weights, tiles of 64, of 128, of 256 in bf16.
+STACKED = [(([3, 0, 16, 1], 48, 400), 0, 0), (([128, 129, 0, 127], 200, 512), 64, 64), (([1000, 0, 1400], 2040, 2048), 128, 128),
+           (([3000, 0, 1701, 2500, 5000], 2200, 2064), 256, 128)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("large_scales", [False, True])
+@pytest.mark.parametrize("sizes,n,k", [s[0] for s in STACKED])
+def test_stacked_scales_and_gathered_rows(sizes, n, k, large_scales, dtype):
+    g = gen(n + 1)
+    e, ends = len(sizes), sizes_to_ends(sizes)
+    rows, a_rows, up = ends[-1] + 3, ends[-1] // 2 + 1, lambda v: -(-v // 128)
+    if large_scales:  # as in test_scale_products_past_the_range
+        few = lambda *s: (torch.randint(-9, 10, s, generator=g, device=DEV).div(9, rounding_mode="trunc") * 2.0 ** -9).to(torch.float8_e4m3fn)
+        pick = lambda *s: torch.exp2(62.0 + torch.randint(0, 6, s, generator=g, device=DEV))
+        a, sa, b, sb = few(a_rows, k), pick(up(k), a_rows), few(e * n, k), pick(up(e * n), up(k))
+    else:
+        qa = fq.fp8_quantize_b128(torch.randn(a_rows, k, generator=g, device=DEV))
+        qb = fq.fp8_quantize_b128(torch.randn(e * n, k, generator=g, device=DEV), TILE)
+        a, sa, b, sb = qa.codes, qa.scales, qb.codes, qb.scales
+    tokens = torch.randint(-1, a_rows + 1, (rows,), generator=g, device=DEV, dtype=torch.int32)  # some that A does not have
+    out = torch.full((rows, n), 77.0, dtype=dtype, device=DEV)
+    fq.fp8_grouped_gemm_b128(a, sa, b, sb, i32(ends), tokens=tokens, out=out)
+    av = torch.cat([value(a, sa, ROW), torch.zeros(1, a.shape[1], dtype=torch.float64, device=DEV)])
+    want, size = expect(av, value(b, sb, TILE).view(e, n, -1), ends, torch.where((tokens >= 0) & (tokens < a_rows), tokens, a_rows), rows)
+    assert bool((size[:ends[-1]] < 2.0 ** 127).all()) and bool((out[ends[-1]:] == 77.0).all())
+    assert bool(((out.double() - want).abs() <= bar(want, size, k, dtype))[:ends[-1]].all())
+    # NaN stays in its rows, and in its expert's columns.
+    some = int(tokens[ends[2]].clamp(0, a_rows - 1))
+    sa[0, some], b.view(torch.uint8)[2 * n + 5, 7] = float("nan"), 0x7F
+    got = fq.fp8_grouped_gemm_b128(a, sa, b, sb, i32(ends), tokens=tokens, out=torch.full_like(out, 77.0))
+    bad = (tokens == some)[:, None].expand(rows, n).clone()
+    bad[ends[2]:ends[3], 5] = True
+    bad[ends[-1]:] = False
+    assert bool(got[bad].isnan().all()) and torch.equal(got[~bad], out[~bad])

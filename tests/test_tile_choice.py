@@ -5,7 +5,7 @@ import pytest
 
 import tile_choice
 from test_abi import L  # noqa: F401  (the loaded library, built if it is missing)
-from test_gpu_grouped_kernels import PRODUCTS, STEPS
+from test_gpu_grouped_kernels import PRODUCTS, STACKED, STEPS
 from test_gpu_int8_kernels import LARGE, RANGES
 
 
@@ -23,7 +23,7 @@ def test_grouped_steps(shape, bf16, f32):
         assert got == want
 
 
-@pytest.mark.parametrize("shape,bf16,f32", PRODUCTS)
+@pytest.mark.parametrize("shape,bf16,f32", PRODUCTS + STACKED)
 def test_grouped_products(shape, bf16, f32):
     sizes, n, k = shape
     assert (tile_choice.grouped(sum(sizes) + 3, len(sizes), n, k, False), tile_choice.grouped(sum(sizes) + 3, len(sizes), n, k, True)) == (bf16, f32)
