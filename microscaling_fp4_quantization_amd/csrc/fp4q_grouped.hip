@@ -13,7 +13,13 @@
 //
 // What bounds them: few rows, memory (8 rows on 8 experts of 14336 x 4096: 60 to 71 us); many rows,
 // what bounds the dense product, and the tiles in which a group ends (65536 rows on 64 experts of
-// 2048 x 4096, bf16 C: 594 to 606 us gathered; the dense product of that size 488 to 508).
+// 2048 x 4096, bf16 C: 594 to 642 us gathered; the dense product of that size 488 to 508; a binary32 C,
+// in tiles of 128 on the bf16 cores, 1058 to 1207).
+//
+// A bf16 C's sums of 128 products are those of the 8-bit cores, which hold about 16 bits, twice as fast
+// as the bf16 ones: one element in 60 to 90 is another bf16 number than with sums in binary32, next to it but
+// where terms cancel, and the error against 64 bits is the same to three digits.  The blocks' sums are
+// added in binary32.  A binary32 C, and the pass over the weights, take the bf16 cores.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -330,7 +336,9 @@ __global__ __launch_bounds__(256, T == 128 ? 2 : 4) void k_grouped_outer_mid(Out
 // Which tile: the one whose modelled time is least, in microseconds, for `tiles(side)` of them with
 // `blocks` K blocks each (the numbers of the dense product: a K block of one workgroup while its
 // CU is shared, on the 8-bit and on the bf16 cores, and its latency when it is not; a workgroup's
-// start and end; how many share a CU).
+// start and end; how many share a CU).  The read of B is not in it: where that is what bounds a
+// product, it takes longer (512 rows on 64 experts of 2048 x 4096: 123 to 127 us in tiles of 64, 62 here),
+// and the tiles that can be chosen then take about the same (of 128: 126 to 130).
 struct TileCost {
     int tile, per_cu;
     double alone, each, each_wide, fixed;
@@ -394,10 +402,14 @@ int launch_grouped_gemm(const GroupedGemmJob& j, char* msg, size_t msg_len) {
     const int64_t some = std::min(j.rows, j.chosen_by);
     const int64_t most = std::min(j.rows, j.experts + (j.clear_rest ? 2 : 0));
     const bool gather = j.tokens != nullptr, brow = j.stacked && j.N % kBlock != 0;
-    // Up to eight rows a group on average: a pass over the weights.  (64 experts of 2048 x 4096, weights
-    // from memory, by events: 64 rows 99 us, in 64 x 64 tiles 150; 256 rows 139 and 176; 512 rows 160
-    // and 187, but 140 and 128 where the weights are in the last-level cache; 1024 rows 210 and 138.  The sizes
-    // are not known here: should one expert own all of 512 rows, 148 us, in tiles 24.)
+    // Up to eight rows a group on average: a pass over the weights.  (64 experts of 2048 x 4096, launches
+    // one after the other, over three sets of weights or one alike, against 64 x 64 tiles.  The same rows
+    // for each expert: 64 rows 110 to 130 us and 123 to 126; 256 rows 112 to 127 and 123 to 127; 512 rows
+    // 120 to 138 and 123 to 127; 640 rows 131 to 147 and 125 to 127; 1024 rows 143 to 153 and 126 to 128.
+    // Routed, the largest groups several times the mean: 128 rows 83 to 84 and 101 to 104; 256 rows 101 to
+    // 103 and 111 to 114; 384 rows 116 to 118 both; 512 rows 128 to 131 and 123 to 125; 640 rows 142 to 146
+    // and 122 to 127.  The sizes are not known here: should one expert own all of 512 rows, 147 to 150 us,
+    // in tiles 16 to 19.)
     if (j.rows <= 8 * some) {
         const int64_t groups = most * ((j.N + kFewRows - 1) / kFewRows);
         if (groups > INT32_MAX) return too_many(what, msg, msg_len);

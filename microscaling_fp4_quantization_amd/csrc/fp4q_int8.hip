@@ -859,7 +859,12 @@ __global__ __launch_bounds__(kFewMaxWaves * kWave) void k_gemm_i8_few(I8Params p
 
 // Which tile, and how many K ranges per tile: the pair whose modelled time is least, in
 // microseconds (a K block of one workgroup while its CU is shared, `each`, and its latency when
-// it is not, `alone`; a workgroup's start and epilogue; how many share a CU).
+// it is not, `alone`; a workgroup's start and epilogue; how many share a CU).  Choices beside the
+// tile and ranges that come next, us to bf16: 17 x 3584 x 18944 (64, 8) 25, (128, 8) 28; 64 x 18944 x 3584
+// (64, 1) and (64, 2) 26, (128, 1) 30, and of 17 rows (64, 1) 25, where (64, 2) takes 21; 333 x 1031 x 1008 (64, 1) 6.7, (64, 2) 9.6; 512 x 3584
+// x 18944 (128, 4) 65, (256, 8) 62; 1024 rows (256, 4) 86 to 90, (128, 2) 106; 2048 rows (256, 2) 139 to 149,
+// (128, 1) 160; 2048^3 (128, 1) 16.1, (64, 1) 17.3; 4096^3 (256, 1) 56, (128, 1) 70 to 76.  Latency that
+// nothing hides is not in it: 333 x 1031 x 1008 is 3.9 us by the model.
 constexpr int64_t kMaxPartialBytes = (int64_t)1 << 28;
 struct Choice {
     int tile, splits;
@@ -934,6 +939,11 @@ int launch_int8_quantize(const Int8QuantJob& j, char* msg, size_t msg_len) {
     const I8QuantParams p{j.x, j.rows, j.cols, (j.cols + 15) / 16 * 16, j.codes, j.scales, 0};
     hipStream_t stream = static_cast<hipStream_t>(j.stream);
     const int64_t chunks = (p.ld / 8 + kWave - 1) / kWave;  // of a wave
+    // Up to 512 rows, fewer than fill the chip by themselves: more waves a row.  (us, launches one after the
+    // other, beside what more rows take: 256 x 2048 3.3 and 4.3, 512 x 2048 3.6 and 4.3, 2048 x 2048 5.8 and
+    // 4.9; 1 x 3584 3.3 and 3.2, 512 x 3584 4.9 and 3.9, 2048 x 3584 11.8 and 7.2; 1 x 8192 3.4 and 4.0, 512 x
+    // 8192 5.3 and 4.9; 1 x 18944 4.0 and 4.3, 512 x 18944 8.8 and 9.2, 2048 x 18944 28 and 27.  A row of
+    // more than 16384 is read in part again: 1 x 32768 6.3 and 4.6.)
     if (j.rows <= 512 && chunks > 2) {
         if (chunks <= 4) launch_quantize_as<4, 1>(p, j.xt, stream);
         else launch_quantize_as<16, 2>(p, j.xt, stream);
