@@ -45,6 +45,8 @@ def expert_order(topk_ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor
     """The slots of a routing (topk_ids: int32 or int64, tokens x top_k) sorted by expert, in
     their order within one.  An id outside 0 .. experts - 1 names no expert: its slot comes
     behind all others', where no group is."""
+    if experts >= 1 << 31 or topk_ids.dim() == 2 and topk_ids.shape[1] >= 1 << 31:
+        raise ValueError("experts and the columns of topk_ids must be below 2^31")  # (the library takes them in 32 bits)
     ids = _matrix(topk_ids, "topk_ids")
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"topk_ids must be int32 or int64, not {ids.dtype}")

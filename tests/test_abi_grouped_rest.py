@@ -1,4 +1,9 @@
-"""fp8_grouped_gemm_b128_cleared refuses what fp8_grouped_gemm_b128 does, before any launch."""
+"""fp8_grouped_gemm_b128_cleared refuses what fp8_grouped_gemm_b128 does, and expert_order what the
+library cannot be told, before any launch."""
+import pytest
+import torch
+
+import microscaling_fp4_quantization_amd as fq
 from test_abi import L, err  # noqa: F401  (the loaded library, built if it is missing)
 
 OK, ARG, SHAPE, ALIGN = 0, 1, 2, 3
@@ -18,3 +23,13 @@ def test_validation(L):
     assert gemm(a=A + 8) == ALIGN and gemm(c=F + 1) == ALIGN and gemm(tok=A + 2) == ALIGN
     assert gemm(r=0, ar=0, a=None, sa=None, b=None, sb=None, off=None, c=None) == OK
     assert gemm(n=0, a=None, sa=None, b=None, sb=None, off=None, c=None) == OK
+
+
+def test_numbers_that_32_bits_do_not_hold():
+    """The library takes them in 32 bits, where 2^32 + 4 experts are 4."""
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    for experts in (1 << 31, (1 << 32) + 4):
+        with pytest.raises(ValueError, match="below 2\\^31"):
+            fq.expert_order(ids, experts)
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        fq.expert_order(torch.zeros(1, 1, dtype=torch.int32).expand(1, (1 << 32) + 8), 8)
