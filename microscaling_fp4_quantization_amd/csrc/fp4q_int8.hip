@@ -286,7 +286,7 @@ __device__ __forceinline__ void tile_at(unsigned g, int64_t rows, int64_t cols, 
 // products end: one barrier per block, and loads go out a block and a half before they are read.
 // Workgroups are persistent: a tile's first two stages are loaded while the tile before is
 // scaled and stored, straight from registers, so that LDS is free.  4096 x 4096 x 14336 to bf16:
-// 157 to 168 us (2.9 to 3.1 POP/s), the matrix cores busy in 70% to 72% of the cycles at 1.9 GHz;
+// 157 to 177 us by box (2.7 to 3.1 POP/s), the matrix cores busy in 70% to 72% of the cycles at 1.9 GHz;
 // 125 us with operands of zero, so that power is part of what bounds it.
 //
 // For that a lane's columns are neighbours: fragment i of a wave's B holds at position r its row
